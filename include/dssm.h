@@ -50,7 +50,7 @@
 extern "C" {
 #endif
 
-#define DSSM_VERSION 10300 /* major*10000 + minor*100 + patch */
+#define DSSM_VERSION 10400 /* major*10000 + minor*100 + patch */
 
 /* Status codes. */
 typedef enum {
@@ -377,6 +377,188 @@ int dssm_s5_forward_tv(const float* u, const dssm_s5_tv_params* p, const dssm_s5
 int dssm_s5_forward_timed(const float* u, const dssm_s5_params* p, const dssm_s5_shape* s,
                           int method, float* y, void* ws, size_t ws_bytes, void* stream,
                           void* const* events, int n_events);
+
+/* ------------------------------------------------------------------------
+ * The gated recurrence and what stands around it in a block.  These calls take
+ * activations of several types; their shapes follow the layer calls, time
+ * fastest.  Conventions that differ from the calls above:
+ * - `dtype` is the type of the activations (u, r, i, y, their gradients, ...);
+ *   parameters, states and statistics are float32.  All arithmetic is in
+ *   float32 (sums of gradients over batch and time in float64 at the end) and
+ *   every output is rounded once, to nearest even.
+ * - Pointers need the alignment of their element type (workspaces and
+ *   checkpoints 256 bytes).
+ * - stride_b / stride_g / ...: elements between two batch rows, at least H L;
+ *   the H L elements of a row are contiguous.  A joint projection's output
+ *   [B, 3 H, L] is passed as three slices with stride_b = 3 H L.
+ * - lens (may be NULL): [B] int32, the steps of each batch row that are live.
+ *   Steps at or past lens[b] are not read; outputs there are 0, and the state
+ *   is the one after step lens[b] - 1.  Values are clamped to 0 .. L.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  DSSM_F32 = 0,  /* float32 */
+  DSSM_BF16 = 1, /* bfloat16 */
+  DSSM_F16 = 2   /* IEEE half */
+} dssm_dtype;
+
+/* What a forward pass keeps for the backward pass. */
+typedef enum {
+  DSSM_CKPT_NONE = 0,
+  DSSM_CKPT_STATE = 1, /* the state entering every DSSM_GATED_CHUNK steps */
+  DSSM_CKPT_INT8 = 2   /* these states, and u, r, i in 8 bits */
+} dssm_ckpt_kind;
+
+#define DSSM_GATED_CHUNK 512 /* steps between two kept states */
+#define DSSM_CKPT8_GROUP 64  /* steps that share a power of two in 8 bits */
+
+typedef struct {
+  int B, H, L;
+  int dtype; /* dssm_dtype */
+} dssm_gated_shape;
+
+/* Inputs of the gated recurrence:
+ *   u, r, i [B, H, L] (stride_b between batch rows): input, recurrence gate and
+ *   input gate (both before the sigmoid);  log_re [H] float32;  lens [B] or NULL. */
+typedef struct {
+  const void* u;
+  const void* r;
+  const void* i;
+  long long stride_b;
+  const float* log_re;
+  const int* lens;
+} dssm_gated_inputs;
+
+/* Gradients: du, dr, di [B, H, L] (stride_b between batch rows), dlog_re [H]
+ * float32, dx0 [B, H] float32 (may be NULL). */
+typedef struct {
+  void* du;
+  void* dr;
+  void* di;
+  long long stride_b;
+  float* dlog_re;
+  float* dx0;
+} dssm_gated_grads;
+
+/* Bytes of workspace of dssm_gated_forward and dssm_gated_backward (host
+ * only).  Requires H <= 65535, B H <= 2^24, L <= 2^24, B H L <= 2^40. */
+int dssm_gated_workspace_size(const dssm_gated_shape* s, size_t* bytes);
+
+/* Bytes of a checkpoint of `kind` (0 for DSSM_CKPT_NONE).  Layout, every part
+ * padded to 256 bytes: the states [B, H, ceil(L / 512)] float32 entering the
+ * chunks, then for DSSM_CKPT_INT8 u, r and i, each as dssm_ckpt8_pack writes
+ * B H rows of L. */
+int dssm_gated_ckpt_size(const dssm_gated_shape* s, int kind, size_t* bytes);
+
+/* The gated linear recurrence: for every (b, h) a real mode whose decay and
+ * drive are gated at every step,
+ *   a_t = exp(-log_re[h]^2 sigmoid(r_t)),
+ *   x_t = a_t x_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) u_t,   y_t = x_t
+ * (sigmoid(r) = 1 is the mode lambda = exp(-log_re^2) of the layer above; the
+ * factor sqrt(1 - a^2) keeps the state's size whatever the decay).
+ *   x0 [B, H] float32 (may be NULL: zero): the state before step 0;
+ *   x_end [B, H] float32 (may be NULL): receives the state after the last live
+ *   step; it may be x0 (streaming in place) -- otherwise x0 is not changed.
+ * ckpt: dssm_gated_ckpt_size(kind) bytes for a backward pass (ignored for
+ * DSSM_CKPT_NONE).  Where 1 - a^2 is below float32's normal range it counts as
+ * 0.  Rows are walked by one or four waves; few long rows are split into
+ * segments joined through the workspace. */
+int dssm_gated_forward(const dssm_gated_inputs* in, const dssm_gated_shape* s, const float* x0,
+                       float* x_end, void* y, int kind, void* ckpt, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* One token for every (b, h): u, r, i, y [B, H] (s->L must be 1; stride_b >= H),
+ * states as above.  A stream with lens[b] <= 0 is idle: its state is kept and
+ * its output is 0.  No workspace; B H <= 2^31 - 1. */
+int dssm_gated_step(const dssm_gated_inputs* in, const dssm_gated_shape* s, const float* x0,
+                    float* x_end, void* y, void* stream);
+
+/* Gradients of f = sum(dy y) + sum(dx_end x_end).  kind and ckpt: what the
+ * forward pass of the same inputs kept (DSSM_CKPT_STATE or _INT8), with the
+ * same lens.  With DSSM_CKPT_STATE u, r and i are read again; with
+ * DSSM_CKPT_INT8 they are not (in->u, r, i and in->stride_b are ignored): the
+ * gradients are those of the map at the decoded u, r and i, with the state
+ * taken up again from the kept state at every chunk.
+ *   dy [B, H, L];  dx_end [B, H] float32 (may be NULL: zero).
+ * dlog_re is summed over b and t in a fixed order (results repeat bit for bit);
+ * with B = 0 or L = 0 it is zero. */
+int dssm_gated_backward(const dssm_gated_inputs* in, const dssm_gated_shape* s, int kind,
+                        const void* ckpt, const void* dy, const float* dx_end,
+                        const dssm_gated_grads* g, void* ws, size_t ws_bytes, void* stream);
+
+/* Activations in 8 bits.  x [rows, L] in groups of 64 steps (the last one
+ * shorter): x ~ q 2^E, q whole with |q| <= 127, E the smallest exponent with
+ * max |x| <= 127 2^E and not below -126; the one rounding is that of x 2^-E to
+ * even (where that would pass the largest value of x's type, |q| is 63).  A
+ * group that holds Inf or NaN stands for NaN.  Layout of `blob`
+ * (256-byte aligned): int8 q [rows, L rounded up to 16], padded to 256 bytes,
+ * then one byte E + 127 per group [rows, ceil(L / 64)] (255: NaN).
+ * Requires 0 <= rows, 0 <= L <= 2^24, rows L <= 2^40. */
+int dssm_ckpt8_size(long long rows, int L, size_t* bytes);
+int dssm_ckpt8_pack(const void* x, long long rows, int L, int dtype, void* blob, void* stream);
+int dssm_ckpt8_unpack(const void* blob, long long rows, int L, int dtype, void* x, void* stream);
+
+/* The norms around a layer, joined with its gate, residual scale and sum.
+ * Over the H channels of every (b, t):
+ *   norm(a) = (a - mean) / sqrt(mean((a - mean)^2) + eps)  (mean 0 for
+ *   DSSM_NORM_RMS),
+ *   v = norm(y) w_post,  o = x + scale v silu(g),  n = norm(o) w_pre,
+ * o the residual stream after the layer and n what the next layer reads (the
+ * second norm is of the stream as it is stored, in `dtype`). */
+typedef enum { DSSM_NORM_RMS = 0, DSSM_NORM_LAYER = 1 } dssm_norm;
+
+typedef struct {
+  int B, H, L;
+  int dtype; /* dssm_dtype */
+  int norm;  /* dssm_norm */
+  float eps; /* >= 0; read by the forward call */
+} dssm_resnorm_shape;
+
+typedef struct {
+  const float* w_post; /* [H]; unused without y */
+  const float* scale;  /* [H]; unused without y */
+  const float* w_pre;  /* [H]; unused without n */
+} dssm_resnorm_params;
+
+/* dx, dy, dg (stride_dg between batch rows) [B, H, L]; dw_post, dscale, dw_pre
+ * [H] float32. */
+typedef struct {
+  void* dx;
+  void* dy;
+  void* dg;
+  long long stride_dg;
+  float* dw_post;
+  float* dscale;
+  float* dw_pre;
+} dssm_resnorm_grads;
+
+/* x [B, H, L];  y [B, H, L] or NULL: without y there is no sum, o must be NULL
+ * and n = norm(x) w_pre;  g [B, H, L] (stride_g between batch rows) or NULL: no
+ * gate (silu(g) replaced by 1);  o [B, H, L];  n [B, H, L], or NULL with y: the
+ * stream only.  stats (may be NULL) receives what the backward pass needs:
+ * float32 [2, B, L] (1 / sqrt of y, of o) for DSSM_NORM_RMS, [4, B, L] (mean and
+ * 1 / sqrt of y, then of o) for DSSM_NORM_LAYER; rows of a norm that the call
+ * does not form are not written.  Requires H <= 8192 (a workgroup holds the
+ * channels of a few steps; larger H: DSSM_ERR_UNSUPPORTED) and
+ * B ceil(L / 4) <= 2^22.
+ * A single token is L = 1. */
+int dssm_resnorm_forward(const void* x, const void* y, const void* g, long long stride_g,
+                         const dssm_resnorm_params* p, const dssm_resnorm_shape* s,
+                         const int* lens, void* o, void* n, float* stats, void* stream);
+
+/* Bytes of workspace of dssm_resnorm_backward. */
+int dssm_resnorm_workspace_size(const dssm_resnorm_shape* s, size_t* bytes);
+
+/* Gradients of f = sum(d_o o) + sum(d_n n) at the forward call's o (its x, in
+ * the call without y) and stats, with the same y, g and lens.  d_o or d_n may
+ * be NULL (zero; both: DSSM_ERR_INVALID_ARG); without y d_n is required and dx =
+ * d_o + the norm's gradient, dy, dg, dw_post and dscale are not written and may
+ * be NULL; without g dg is not; without d_n dw_pre is set to zero.  The
+ * parameters' sums run in a fixed order; with B = 0 or L = 0 they are zero. */
+int dssm_resnorm_backward(const void* o, const void* y, const void* g, long long stride_g,
+                          const float* stats, const dssm_resnorm_params* p,
+                          const dssm_resnorm_shape* s, const int* lens, const void* d_o,
+                          const void* d_n, const dssm_resnorm_grads* gr, void* ws,
+                          size_t ws_bytes, void* stream);
 
 /* Timing variants: identical results to dssm_forward_fft / dssm_forward_scan;
  * the kernels of stage k are launched with hipExtLaunchKernel so that the GPU

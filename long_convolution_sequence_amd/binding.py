@@ -22,6 +22,12 @@ OP_GEN, OP_FFT, OP_SCAN, OP_BWD, OP_S5_SCAN, OP_S5_FFT, OP_S5_FUSED = 0, 1, 2, 3
 # convolution, or fused with both projections (v and x on chip)
 S5_SCAN, S5_FFT, S5_FUSED = 0, 1, 2
 CAST_RE, CAST_RE_IM = 0, 1  # Re K, or Re K * Im K (DLR-prod)
+F32, BF16, F16 = 0, 1, 2  # activation types of the gated recurrence and the block around it
+# what a gated forward keeps: nothing, the states entering its chunks, or these
+# and u, r, i in 8 bits
+CKPT_NONE, CKPT_STATE, CKPT_INT8 = 0, 1, 2
+GATED_CHUNK, CKPT8_GROUP = 512, 64
+NORM_RMS, NORM_LAYER = 0, 1
 
 # Every function the header declares (checked by the ABI tests).
 EXPORTS = [
@@ -33,6 +39,9 @@ EXPORTS = [
     "dssm_forward_scan_state", "dssm_step",
     "dssm_s5_workspace_size", "dssm_s5_tv_workspace_size", "dssm_s5_forward",
     "dssm_s5_forward_timed", "dssm_s5_forward_tv",
+    "dssm_gated_workspace_size", "dssm_gated_ckpt_size", "dssm_gated_forward", "dssm_gated_step",
+    "dssm_gated_backward", "dssm_ckpt8_size", "dssm_ckpt8_pack", "dssm_ckpt8_unpack",
+    "dssm_resnorm_forward", "dssm_resnorm_workspace_size", "dssm_resnorm_backward",
 ]
 
 
@@ -64,6 +73,39 @@ class S5Params(ctypes.Structure):
 class S5TVParams(ctypes.Structure):
     _fields_ = [("lam_c", ctypes.c_void_p), ("Bt", ctypes.c_void_p), ("C", ctypes.c_void_p),
                 ("D", ctypes.c_void_p), ("delta", ctypes.c_void_p)]
+
+
+class GatedShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class GatedInputs(ctypes.Structure):
+    _fields_ = [("u", ctypes.c_void_p), ("r", ctypes.c_void_p), ("i", ctypes.c_void_p),
+                ("stride_b", ctypes.c_longlong), ("log_re", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)]
+
+
+class GatedGrads(ctypes.Structure):
+    _fields_ = [("du", ctypes.c_void_p), ("dr", ctypes.c_void_p), ("di", ctypes.c_void_p),
+                ("stride_b", ctypes.c_longlong), ("dlog_re", ctypes.c_void_p),
+                ("dx0", ctypes.c_void_p)]
+
+
+class ResnormShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class ResnormParams(ctypes.Structure):
+    _fields_ = [("w_post", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p)]
+
+
+class ResnormGrads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dg", ctypes.c_void_p),
+                ("stride_dg", ctypes.c_longlong), ("dw_post", ctypes.c_void_p),
+                ("dscale", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p)]
 
 
 class DSSMError(RuntimeError):
@@ -136,6 +178,25 @@ def lib():
     L.dssm_s5_forward_tv.restype = ctypes.c_int
     L.dssm_s5_forward_tv.argtypes = [vp, ctypes.POINTER(S5TVParams), ctypes.POINTER(S5Shape), vp,
                                      vp, vp, sz, vp]
+    P = ctypes.POINTER
+    gi, gs, gg = P(GatedInputs), P(GatedShape), P(GatedGrads)
+    rp, rs, rg = P(ResnormParams), P(ResnormShape), P(ResnormGrads)
+    for name, args in (
+            ("dssm_gated_workspace_size", [gs, P(sz)]),
+            ("dssm_gated_ckpt_size", [gs, ctypes.c_int, P(sz)]),
+            ("dssm_gated_forward", [gi, gs, vp, vp, vp, ctypes.c_int, vp, vp, sz, vp]),
+            ("dssm_gated_step", [gi, gs, vp, vp, vp, vp]),
+            ("dssm_gated_backward", [gi, gs, ctypes.c_int, vp, vp, vp, gg, vp, sz, vp]),
+            ("dssm_ckpt8_size", [ctypes.c_longlong, ctypes.c_int, P(sz)]),
+            ("dssm_ckpt8_pack", [vp, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, vp, vp]),
+            ("dssm_ckpt8_unpack", [vp, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, vp, vp]),
+            ("dssm_resnorm_forward", [vp, vp, vp, ctypes.c_longlong, rp, rs, vp, vp, vp, vp, vp]),
+            ("dssm_resnorm_workspace_size", [rs, P(sz)]),
+            ("dssm_resnorm_backward", [vp, vp, vp, ctypes.c_longlong, vp, rp, rs, vp, vp, vp, rg,
+                                       vp, sz, vp])):
+        f = getattr(L, name)
+        f.restype = ctypes.c_int
+        f.argtypes = args
     _lib = L
     return L
 
@@ -516,6 +577,407 @@ def s5_forward_tv(u, lam_c, Bt, C, D, delta, step, y=None, workspace=None, strea
                                    ss.data_ptr(), yy.data_ptr(), ws.data_ptr(), nbytes,
                                    _stream(stream)))
     return y
+
+
+# ----------------------------------------------------------------------------
+# the gated recurrence, 8-bit checkpoints, the residual norm
+# ----------------------------------------------------------------------------
+
+def _dtype_code(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    return code
+
+
+def _like(t, name, ref, refname):
+    """t has ref's shape, type and device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype != ref.dtype:
+        raise TypeError("%s is %s, %s is %s" % (name, t.dtype, refname, ref.dtype))
+    if t.device != ref.device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, ref.device))
+    if t.shape != ref.shape:
+        raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), tuple(ref.shape)))
+    return t
+
+
+def _plain(t, name, ref, refname):
+    """_like, and contiguous."""
+    _like(t, name, ref, refname)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _batch_stride(t, name):
+    """Elements between the batch rows of t [B, H, L] (or [B, H]), whose H L
+    elements are contiguous."""
+    inner = t.shape[1] * t.shape[2] if t.dim() == 3 else t.shape[1]
+    if t.numel() == 0:
+        return inner
+    st = t.stride()
+    want = 1
+    for d in range(t.dim() - 1, 0, -1):
+        if t.shape[d] > 1 and st[d] != want:
+            raise ValueError("%s must be contiguous within each batch row" % name)
+        want *= t.shape[d]
+    if t.shape[0] == 1:
+        return inner
+    if st[0] < inner:
+        raise ValueError("%s has overlapping batch rows" % name)
+    return st[0]
+
+
+def _one_stride(ts):
+    out = [_batch_stride(t, name) for t, name in ts]
+    if any(s != out[0] for s in out):
+        raise ValueError("%s must have the same batch stride" % ", ".join(n for _, n in ts))
+    return out[0]
+
+
+def _lens_ptr(lens, B, device):
+    if lens is None:
+        return None
+    torch = _torch()
+    if not isinstance(lens, torch.Tensor) or lens.dtype != torch.int32:
+        raise TypeError("lens must be an int32 tensor")
+    if lens.device != device or not lens.is_contiguous() or lens.numel() != B:
+        raise ValueError("lens must be a contiguous tensor of %d on %s" % (B, device))
+    return lens.data_ptr()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch_on(device, stream):
+    """Makes `device` the current one for a launch and gives the stream to
+    launch on: the caller's, or the device's current one."""
+    import contextlib
+
+    torch = _torch()
+    if stream is not None and stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    here = torch.cuda.current_device() == device.index
+    return (contextlib.nullcontext() if here else torch.cuda.device(device)), s.cuda_stream
+
+
+def _bytes(fn, args, given, name, device, stream):
+    """A workspace or checkpoint of the size fn reports: the caller's, or new."""
+    torch = _torch()
+    need = ctypes.c_size_t(0)
+    check(fn(*(args + [ctypes.byref(need)])))
+    if given is None:
+        with _on_stream(stream):
+            given = torch.empty(max(need.value, 256), dtype=torch.uint8, device=device)
+    elif not isinstance(given, torch.Tensor) or given.device != device or not given.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor on %s" % (name, device))
+    n = given.numel() * given.element_size()
+    if n < need.value and name != "workspace":  # a workspace's size the library checks itself
+        raise ValueError("%s has %d bytes, needs %d" % (name, n, need.value))
+    return given, n
+
+
+def _gated_rows(u, r, i, dims):
+    code = _dtype_code(u, "u")
+    if u.dim() != dims:
+        raise ValueError("u must be %s" % ("[B, H, L]" if dims == 3 else "[B, H]"))
+    _like(r, "r", u, "u")
+    _like(i, "i", u, "u")
+    return code, _one_stride([(u, "u"), (r, "r"), (i, "i")])
+
+
+def _gated_forward(u, r, i, log_re, kind, x, x_out, lens, y, ckpt, workspace, stream):
+    torch = _torch()
+    code, sb = _gated_rows(u, r, i, 3)
+    B, H, L = u.shape
+    dev = u.device
+    lr = _dev_f32(log_re, "log_re", H, dev)
+    xx = None if x is None else _dev_f32(x, "x", B * H, dev)
+    xo = xx if x_out is None else _dev_f32(x_out, "x_out", B * H, dev)
+    if y is None:
+        y = _empty(u.shape, u.dtype, dev, stream)
+    _plain(y, "y", u, "u")
+    lp = _lens_ptr(lens, B, dev)
+    shape = GatedShape(B, H, L, code)
+    sp = ctypes.byref(shape)
+    with_dev, st = _launch_on(dev, stream)
+    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, [sp], workspace, "workspace", dev, stream)
+    if kind != CKPT_NONE:
+        ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, [sp, kind], ckpt, "ckpt", dev, stream)
+    inp = GatedInputs(u.data_ptr(), r.data_ptr(), i.data_ptr(), sb, lr.data_ptr(), lp)
+    with with_dev:
+        check(lib().dssm_gated_forward(ctypes.byref(inp), sp, _ptr(xx), _ptr(xo), y.data_ptr(),
+                                       kind, _ptr(ckpt), ws.data_ptr(), nbytes, st))
+    return y, ckpt
+
+
+def gated_forward(u, r, i, log_re, x=None, x_out=None, lens=None, y=None, workspace=None,
+                  stream=None):
+    """The gated recurrence: x_t = a_t x_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) u_t,
+    a_t = exp(-log_re^2 sigmoid(r_t)), y_t = x_t.  u, r, i [B,H,L] f32, bf16 or
+    f16 (slices of a joint [B,3H,L] projection are taken as they are), log_re
+    [H] f32 -> y [B,H,L].  x [B,H] f32: the state before the first step, None
+    for zero; the state after the last goes to x_out, or back to x.  lens [B]
+    int32: live steps per batch row (y is 0 behind them)."""
+    return _gated_forward(u, r, i, log_re, CKPT_NONE, x, x_out, lens, y, None, workspace,
+                          stream)[0]
+
+
+def gated_forward_ckpt(u, r, i, log_re, kind=CKPT_STATE, x=None, x_out=None, lens=None, y=None,
+                       ckpt=None, workspace=None, stream=None):
+    """gated_forward that keeps what gated_backward needs: returns (y, ckpt).
+    kind CKPT_STATE: the states entering every 512 steps (the backward pass
+    takes u, r, i again); CKPT_INT8: also u, r, i in 8 bits (it does not)."""
+    if kind not in (CKPT_STATE, CKPT_INT8):
+        raise ValueError("kind must be CKPT_STATE or CKPT_INT8")
+    return _gated_forward(u, r, i, log_re, kind, x, x_out, lens, y, ckpt, workspace, stream)
+
+
+def gated_step(u_t, r_t, i_t, log_re, x, x_out=None, lens=None, y=None, stream=None):
+    """One token of the gated recurrence: u_t, r_t, i_t [B,H] -> y_t [B,H]; the
+    state x [B,H] f32 is updated in place, or left and written to x_out.
+    lens [B] int32: rows with 0 are idle (state kept, y 0)."""
+    code, sb = _gated_rows(u_t, r_t, i_t, 2)
+    B, H = u_t.shape
+    dev = u_t.device
+    lr = _dev_f32(log_re, "log_re", H, dev)
+    xx = _dev_f32(x, "x", B * H, dev)
+    xo = xx if x_out is None else _dev_f32(x_out, "x_out", B * H, dev)
+    if y is None:
+        y = _empty(u_t.shape, u_t.dtype, dev, stream)
+    _plain(y, "y", u_t, "u_t")
+    shape = GatedShape(B, H, 1, code)
+    inp = GatedInputs(u_t.data_ptr(), r_t.data_ptr(), i_t.data_ptr(), sb, lr.data_ptr(),
+                      _lens_ptr(lens, B, dev))
+    with_dev, st = _launch_on(dev, stream)
+    with with_dev:
+        check(lib().dssm_gated_step(ctypes.byref(inp), ctypes.byref(shape), xx.data_ptr(),
+                                    xo.data_ptr(), y.data_ptr(), st))
+    return y
+
+
+def gated_backward(dy, ckpt, kind, log_re, u=None, r=None, i=None, dx=None, lens=None, du=None,
+                   dr=None, di=None, workspace=None, stream=None):
+    """Gradients of f = sum(dy y) + sum(dx x_end) for the forward call that kept
+    `ckpt` (gated_forward_ckpt of the same kind, shape and lens).  dy [B,H,L];
+    u, r, i as there for CKPT_STATE, None for CKPT_INT8; dx [B,H] f32 or None.
+    Returns a dict du, dr, di [B,H,L], dlog_re [H] f32, dx0 [B,H] f32 (du, dr,
+    di given: slices of one [B,3H,L] buffer are written as they are)."""
+    torch = _torch()
+    code = _dtype_code(dy, "dy")
+    if dy.dim() != 3:
+        raise ValueError("dy must be [B, H, L]")
+    if kind not in (CKPT_STATE, CKPT_INT8):
+        raise ValueError("kind must be CKPT_STATE or CKPT_INT8")
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    B, H, L = dy.shape
+    dev = dy.device
+    sb = H * L
+    if kind == CKPT_STATE:
+        if u is None or r is None or i is None:
+            raise ValueError("CKPT_STATE keeps states only: u, r and i are needed")
+        for t, name in ((u, "u"), (r, "r"), (i, "i")):
+            _like(t, name, dy, "dy")
+        sb = _one_stride([(u, "u"), (r, "r"), (i, "i")])
+    elif u is not None or r is not None or i is not None:
+        raise ValueError("CKPT_INT8 holds u, r and i itself: pass none")
+    lr = _dev_f32(log_re, "log_re", H, dev)
+    dxx = None if dx is None else _dev_f32(dx, "dx", B * H, dev)
+    out = {}
+    for name, t in (("du", du), ("dr", dr), ("di", di)):
+        out[name] = _empty(dy.shape, dy.dtype, dev, stream) if t is None else _like(t, name, dy, "dy")
+    gsb = _one_stride([(out[k], k) for k in ("du", "dr", "di")])
+    out["dlog_re"] = _empty((H,), torch.float32, dev, stream)
+    out["dx0"] = _empty((B, H), torch.float32, dev, stream)
+    shape = GatedShape(B, H, L, code)
+    sp = ctypes.byref(shape)
+    with_dev, st = _launch_on(dev, stream)
+    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, [sp], workspace, "workspace", dev, stream)
+    ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, [sp, kind], ckpt, "ckpt", dev, stream)
+    inp = GatedInputs(_ptr(u), _ptr(r), _ptr(i), sb, lr.data_ptr(), _lens_ptr(lens, B, dev))
+    g = GatedGrads(out["du"].data_ptr(), out["dr"].data_ptr(), out["di"].data_ptr(), gsb,
+                   out["dlog_re"].data_ptr(), out["dx0"].data_ptr())
+    with with_dev:
+        check(lib().dssm_gated_backward(ctypes.byref(inp), sp, kind, ckpt.data_ptr(),
+                                        dy.data_ptr(), _ptr(dxx), ctypes.byref(g), ws.data_ptr(),
+                                        nbytes, st))
+    return out
+
+
+def _rows_of(shape):
+    if len(shape) == 0:
+        raise ValueError("at least one dimension is needed")
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return rows, shape[-1]
+
+
+def ckpt8_size(shape):
+    """Bytes of a tensor of this shape in 8 bits."""
+    out = ctypes.c_size_t(0)
+    check(lib().dssm_ckpt8_size(*_rows_of(tuple(shape)), ctypes.byref(out)))
+    return out.value
+
+
+def ckpt8_pack(x, blob=None, stream=None):
+    """x [..., L] f32, bf16 or f16 in 8 bits: groups of 64 along L as int8 times
+    a power of two.  Returns a uint8 tensor (the layout is dssm_ckpt8_pack's)."""
+    code = _dtype_code(x, "x")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    rows, L = _rows_of(x.shape)
+    dev = x.device
+    blob, _ = _bytes(lib().dssm_ckpt8_size, [rows, L], blob, "blob", dev, stream)
+    with_dev, st = _launch_on(dev, stream)
+    with with_dev:
+        check(lib().dssm_ckpt8_pack(x.data_ptr(), rows, L, code, blob.data_ptr(), st))
+    return blob
+
+
+def ckpt8_unpack(blob, shape, dtype, x=None, stream=None):
+    """The values a ckpt8_pack blob stands for, in `dtype`."""
+    torch = _torch()
+    if not isinstance(blob, torch.Tensor) or not blob.is_cuda:
+        raise ValueError("blob must be a device tensor")
+    shape = tuple(shape)
+    rows, L = _rows_of(shape)
+    dev = blob.device
+    _bytes(lib().dssm_ckpt8_size, [rows, L], blob, "blob", dev, stream)
+    if x is None:
+        x = _empty(shape, dtype, dev, stream)
+    code = _dtype_code(x, "x")
+    if tuple(x.shape) != shape or x.dtype != dtype or x.device != dev or not x.is_contiguous():
+        raise ValueError("x must be a contiguous %s tensor of %s on %s" % (dtype, shape, dev))
+    with_dev, st = _launch_on(dev, stream)
+    with with_dev:
+        check(lib().dssm_ckpt8_unpack(blob.data_ptr(), rows, L, code, x.data_ptr(), st))
+    return x
+
+
+def _resnorm_dims(x, name):
+    """B, H, L of [B, H, L], or of [B, H] as one step."""
+    if x.dim() not in (2, 3):
+        raise ValueError("%s must be [B, H, L] or [B, H]" % name)
+    return x.shape[0], x.shape[1], (x.shape[2] if x.dim() == 3 else 1)
+
+
+def _resnorm_params(w_post, scale, w_pre, H, dev, y, n):
+    def vec(t, name, used):
+        return _dev_f32(t, name, H, dev) if used or t is not None else None
+
+    keep = (vec(w_post, "w_post", y), vec(scale, "scale", y), vec(w_pre, "w_pre", n))
+    return ResnormParams(*[_ptr(t) for t in keep]), keep
+
+
+def _resnorm_forward(x, y, g, w_post, scale, w_pre, norm, eps, lens, o, n, stats, stream):
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    B, H, L = _resnorm_dims(x, "x")
+    dev = x.device
+    _plain(x, "x", x, "x")
+    if y is None and (g is not None or o is not None):
+        raise ValueError("a gate or a stream output needs y")
+    if y is None and w_pre is None:
+        raise ValueError("without y there is only n: w_pre is needed")
+    sg = 0
+    if y is not None:
+        _plain(y, "y", x, "x")
+        o = _empty(x.shape, x.dtype, dev, stream) if o is None else _plain(o, "o", x, "x")
+        if g is not None:
+            sg = _batch_stride(_like(g, "g", x, "x"), "g")
+    if w_pre is not None:
+        n = _empty(x.shape, x.dtype, dev, stream) if n is None else _plain(n, "n", x, "x")
+    elif n is not None:
+        raise ValueError("n needs w_pre")
+    prm, keep = _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, n is not None)
+    if stats is True:
+        stats = _empty((4 if norm == NORM_LAYER else 2, B, L), torch.float32, dev, stream)
+    shape = ResnormShape(B, H, L, code, int(norm), float(eps))
+    with_dev, st = _launch_on(dev, stream)
+    with with_dev:
+        check(lib().dssm_resnorm_forward(x.data_ptr(), _ptr(y), _ptr(g), sg, ctypes.byref(prm),
+                                         ctypes.byref(shape), _lens_ptr(lens, B, dev), _ptr(o),
+                                         _ptr(n), _ptr(stats), st))
+    del keep
+    return o, n, stats
+
+
+def resnorm_forward(x, y, g, w_post, scale, w_pre, norm=NORM_RMS, eps=1e-6, lens=None, o=None,
+                    n=None, stream=None):
+    """Around a layer: o = x + scale norm(y) w_post silu(g), n = norm(o) w_pre,
+    the norms over the H channels.  x, y, g [B,H,L] (or [B,H]: one token; g may
+    be a slice of a joint projection), w_post, scale, w_pre [H] f32.  Returns
+    (o, n).  g None: no gate; y None: n = norm(x) w_pre and o is None; w_pre
+    None: n is None."""
+    return _resnorm_forward(x, y, g, w_post, scale, w_pre, norm, eps, lens, o, n, None,
+                            stream)[:2]
+
+
+def resnorm_forward_stats(x, y, g, w_post, scale, w_pre, norm=NORM_RMS, eps=1e-6, lens=None,
+                          o=None, n=None, stream=None):
+    """resnorm_forward that also returns what resnorm_backward needs: (o, n, stats)."""
+    return _resnorm_forward(x, y, g, w_post, scale, w_pre, norm, eps, lens, o, n, True, stream)
+
+
+def resnorm_backward(o, y, g, stats, w_post, scale, w_pre, do, dn, norm=NORM_RMS, lens=None,
+                     dg=None, workspace=None, stream=None):
+    """Gradients of f = sum(do o) + sum(dn n) at resnorm_forward_stats's o (its
+    x, if that call had no y) and stats.  do or dn may be None.  Returns a dict
+    dx, dy, dg, dw_post, dscale, dw_pre (None where the call has no such
+    input)."""
+    torch = _torch()
+    code = _dtype_code(o, "o")
+    B, H, L = _resnorm_dims(o, "o")
+    dev = o.device
+    _plain(o, "o", o, "o")
+    if y is None and g is not None:
+        raise ValueError("a gate needs y")
+    if dn is not None and w_pre is None:
+        raise ValueError("dn needs w_pre")
+    for t, name in ((y, "y"), (do, "do"), (dn, "dn")):
+        if t is not None:
+            _plain(t, name, o, "o")
+    sg = 0 if g is None else _batch_stride(_like(g, "g", o, "o"), "g")
+    rows = 4 if norm == NORM_LAYER else 2
+    st_ = _dev_f32(stats, "stats", rows * B * L, dev)
+    prm, keep = _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, dn is not None)
+    new = lambda: _empty(o.shape, o.dtype, dev, stream)
+    vec = lambda: _empty((H,), torch.float32, dev, stream)
+    out = dict(dx=new(), dy=None if y is None else new(), dg=None, dw_post=None, dscale=None,
+               dw_pre=vec())
+    sdg = 0
+    if y is not None:
+        out["dw_post"], out["dscale"] = vec(), vec()
+    if g is not None:
+        out["dg"] = new() if dg is None else _like(dg, "dg", o, "o")
+        sdg = _batch_stride(out["dg"], "dg")
+    elif dg is not None:
+        raise ValueError("dg needs g")
+    shape = ResnormShape(B, H, L, code, int(norm), 0.0)
+    sp = ctypes.byref(shape)
+    with_dev, st = _launch_on(dev, stream)
+    ws, nbytes = _bytes(lib().dssm_resnorm_workspace_size, [sp], workspace, "workspace", dev,
+                        stream)
+    gr = ResnormGrads(_ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dg"]), sdg,
+                      _ptr(out["dw_post"]), _ptr(out["dscale"]), _ptr(out["dw_pre"]))
+    with with_dev:
+        check(lib().dssm_resnorm_backward(o.data_ptr(), _ptr(y), _ptr(g), sg, st_.data_ptr(),
+                                          ctypes.byref(prm), sp, _lens_ptr(lens, B, dev), _ptr(do),
+                                          _ptr(dn), ctypes.byref(gr), ws.data_ptr(), nbytes, st))
+    del keep
+    return out
 
 
 class HipEvents:

@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdssm.so")
 BUILD_STAMPS = os.path.join(HERE, "_build_stamps")
 LIB_STAMPS = os.path.join(HERE, "libdssm_stamps.so")
-SOURCES = ["api.hip", "chunk.hip", "eig_gen.hip", "fft.hip", "grad.hip", "scan.hip", "s5.hip"]
+SOURCES = ["api.hip", "api_seq.hip", "chunk.hip", "ckpt8.hip", "eig_gen.hip", "fft.hip",
+           "gated.hip", "grad.hip", "resnorm.hip", "scan.hip", "s5.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 FLAGS = [

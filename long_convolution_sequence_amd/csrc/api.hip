@@ -13,8 +13,10 @@
 using namespace dssm;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace dssm {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -35,6 +37,10 @@ int hip_check(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(DSSM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
   return DSSM_OK;
 }
+
+}  // namespace dssm
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

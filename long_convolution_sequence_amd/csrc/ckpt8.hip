@@ -1,0 +1,89 @@
+// Activations in 8 bits: pack and unpack.  Rows of L steps, groups of 64 steps
+// as int8 times a power of two (the format is described in seq_common.h).  A
+// lane holds 8 steps, 8 lanes a group; both kernels only stream memory.
+#include <algorithm>
+
+#include "dssm_internal.h"
+#include "seq_common.h"
+
+namespace dssm {
+namespace {
+
+// Lane slots of a row: 8 steps each, whole groups (8 slots).
+__host__ __device__ inline int row_slots(int L) { return ckpt8_groups(L) * 8; }
+
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, long n, int L,
+                                                   int8_t* __restrict__ q8,
+                                                   uint8_t* __restrict__ e8) {
+  const int slots = row_slots(L);
+  const int pitch = ckpt8_row(L), groups = ckpt8_groups(L);
+  // n is a multiple of 8: the lanes of a group take part together
+  for (long k = (long)blockIdx.x * 256 + threadIdx.x; k < n; k += (long)gridDim.x * 256) {
+    const long row = k / slots;
+    const int t = (int)(k - row * slots) * 8;
+    const int ns = min(max(L - t, 0), 8);
+    float v[8];
+    load_n<T, 8>(x + row * L + t, ns, v);
+    uint2 q;
+    const int byte = quantise8<T>(v, 8, &q);
+    if (ns > 0) {
+      *reinterpret_cast<uint2*>(q8 + row * pitch + t) = q;
+      if ((t & (kGroup - 1)) == 0) e8[row * groups + t / kGroup] = (uint8_t)byte;
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void unpack_kernel(const int8_t* __restrict__ q8,
+                                                     const uint8_t* __restrict__ e8, long n, int L,
+                                                     T* __restrict__ x) {
+  const int slots = (L + 7) / 8;
+  const int pitch = ckpt8_row(L), groups = ckpt8_groups(L);
+  for (long k = (long)blockIdx.x * 256 + threadIdx.x; k < n; k += (long)gridDim.x * 256) {
+    const long row = k / slots;
+    const int t = (int)(k - row * slots) * 8;
+    float v[8];
+    dequantise8(*reinterpret_cast<const uint2*>(q8 + row * pitch + t),
+                e8[row * groups + t / kGroup], v);
+    store_n<T, 8>(x + row * L + t, L - t, v);
+  }
+}
+
+template <typename T>
+hipError_t run(const void* x, long rows, int L, void* blob, void* out, hipStream_t st) {
+  int8_t* q8 = static_cast<int8_t*>(blob);
+  uint8_t* e8 = reinterpret_cast<uint8_t*>(blob) + ckpt8_exp_offset(rows, L);
+  const long n = rows * (out ? (L + 7) / 8 : row_slots(L));
+  const dim3 grid((unsigned)std::min<long>((n + 255) / 256, 8192));
+  if (out)
+    hipLaunchKernelGGL((unpack_kernel<T>), grid, dim3(256), 0, st, q8, e8, n, L,
+                       static_cast<T*>(out));
+  else
+    hipLaunchKernelGGL((pack_kernel<T>), grid, dim3(256), 0, st, static_cast<const T*>(x), n, L,
+                       q8, e8);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ckpt8_pack(const void* x, long rows, int L, int dtype, void* blob,
+                             hipStream_t st) {
+  switch (dtype) {
+    case 0: return run<float>(x, rows, L, blob, nullptr, st);
+    case 1: return run<__bf16>(x, rows, L, blob, nullptr, st);
+    default: return run<_Float16>(x, rows, L, blob, nullptr, st);
+  }
+}
+
+hipError_t launch_ckpt8_unpack(const void* blob, long rows, int L, int dtype, void* x,
+                               hipStream_t st) {
+  void* b = const_cast<void*>(blob);
+  switch (dtype) {
+    case 0: return run<float>(nullptr, rows, L, b, x, st);
+    case 1: return run<__bf16>(nullptr, rows, L, b, x, st);
+    default: return run<_Float16>(nullptr, rows, L, b, x, st);
+  }
+}
+
+}  // namespace dssm

@@ -9,6 +9,13 @@
 
 namespace dssm {
 
+// Status of an entry point (api.hip): fail() leaves the message that
+// dssm_last_error() returns on this thread and passes `code` on, ok() clears
+// it, hip_check() turns a HIP error into DSSM_ERR_HIP.
+int fail(int code, const char* fmt, ...);
+int ok();
+int hip_check(hipError_t e, const char* what);
+
 // Optional pair of caller-owned events that the GPU stamps at the start and
 // the end of one kernel (hipExtLaunchKernel): timing of that kernel alone,
 // without the dispatch gap before it.
@@ -251,5 +258,75 @@ hipError_t launch_s5_fused(const void* apk_in, const int* rexp_in, const void* a
 hipError_t launch_s5_proj_out(const void* apk_out, const int* rexp_out, const float* x,
                               const float* D, const float* u, int B, int H, int P, int L, float* y,
                               hipStream_t st, KEvents ev = {});
+
+// ---------------------------------------------------------------------------
+// Gated recurrence (gated.hip); dtype: a dssm_dtype value
+// ---------------------------------------------------------------------------
+struct GatedCall {
+  const void *u, *r, *i;  // [B,H,L], elements between batch rows: stride_b
+  long long stride_b;
+  const float* log_re;    // [H]
+  const int* lens;        // [B] or null
+  int B, H, L;
+  const float* x0;        // [B,H] or null: state before step 0
+  float* xT;              // [B,H] or null: state after the last step (may be x0)
+  void* y;
+  int kind;               // what the checkpoint keeps (a dssm_ckpt_kind value)
+  void* ckpt;
+  void* ws;
+  // backward
+  const void* dy;
+  const float* dx;        // [B,H] or null
+  void *du, *dr, *di;
+  long long grad_stride_b;
+  float *dx0, *dlog_re;   // dx0 may be null
+};
+// A checkpoint: the states entering the chunks [B H][ceil(L / 512)] float32
+// first, then (kind 2) u, r and i as 8-bit blobs at the offsets q8.
+struct GatedCkpt {
+  size_t q8[3] = {0, 0, 0};
+  size_t total = 0;
+};
+GatedCkpt gated_ckpt_layout(long rows, int L, int kind);
+size_t gated_workspace(int B, int H, int L);
+hipError_t launch_gated_forward(const GatedCall& c, int dtype, hipStream_t st);
+hipError_t launch_gated_backward(const GatedCall& c, int dtype, hipStream_t st);
+hipError_t launch_gated_step(const GatedCall& c, int dtype, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// 8-bit checkpoints (ckpt8.hip)
+// ---------------------------------------------------------------------------
+// A blob: int8 [rows][L rounded up to 16], then at ckpt8_exp_offset the
+// exponent bytes [rows][ceil(L / 64)].
+size_t ckpt8_exp_offset(long rows, int L);
+size_t ckpt8_bytes(long rows, int L);
+hipError_t launch_ckpt8_pack(const void* x, long rows, int L, int dtype, void* blob,
+                             hipStream_t st);
+hipError_t launch_ckpt8_unpack(const void* blob, long rows, int L, int dtype, void* x,
+                               hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Residual norm (resnorm.hip)
+// ---------------------------------------------------------------------------
+constexpr int kResnormMaxH = 8192;
+struct ResnormCall {
+  const void *x, *y, *g;  // y null: only n = norm(x) w_pre;  g null: no gate
+  long long stride_g;     // elements between batch rows of g
+  const float *w_post, *scale, *w_pre;
+  const int* lens;        // [B] or null
+  int B, H, L, layer;
+  float eps;
+  void *o, *n;            // n may be null (o too, without y)
+  float* stats;           // forward: may be null
+  // backward: x is the stored stream (o, or x without y)
+  const void *d_o, *d_n;  // either may be null
+  void *dx, *dy, *dg;
+  long long stride_dg;
+  float *dw_post, *dscale, *dw_pre;
+  void* ws;
+};
+size_t resnorm_workspace(int B, int H, int L, int dtype);
+hipError_t launch_resnorm_forward(const ResnormCall& c, int dtype, hipStream_t st);
+hipError_t launch_resnorm_backward(const ResnormCall& c, int dtype, hipStream_t st);
 
 }  // namespace dssm

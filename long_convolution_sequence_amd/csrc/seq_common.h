@@ -1,0 +1,136 @@
+// Shared device helpers of the gated recurrence, the 8-bit checkpoints and the
+// residual norm: element types, loads and stores of a few consecutive steps at
+// any alignment, and the 8-bit group format.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dssm {
+
+constexpr int kLaneSteps = 8;               // consecutive steps held by one lane
+constexpr int kChunk = 64 * kLaneSteps;     // steps of one wave tile, between two kept states
+constexpr int kGroup = 64;                  // steps that share a power of two in 8 bits
+
+// Rows of an 8-bit checkpoint: int8 steps padded to 16 bytes, one exponent byte per group.
+__host__ __device__ inline int ckpt8_row(int L) { return (L + 15) / 16 * 16; }
+__host__ __device__ inline int ckpt8_groups(int L) { return (L + kGroup - 1) / kGroup; }
+
+// N consecutive elements, aligned as one element: the device reads and writes
+// them in one instruction at any address.
+template <typename T, int N>
+struct VecOf {
+  typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+};
+
+// out[0..N) = p[0..N) as float; elements at or past `n` are not read and are 0.
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, int n, float* out) {
+  if (n >= N) {
+    const typename VecOf<T, N>::type v = *reinterpret_cast<const typename VecOf<T, N>::type*>(p);
+#pragma unroll
+    for (int k = 0; k < N; ++k) out[k] = (float)v[k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) out[k] = k < n ? (float)p[k] : 0.f;
+  }
+}
+
+// p[0..min(n, N)) = in, rounded to nearest even once.
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* p, int n, const float* in) {
+  if (n >= N) {
+    typename VecOf<T, N>::type v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = (T)in[k];
+    *reinterpret_cast<typename VecOf<T, N>::type*>(p) = v;
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < n) p[k] = (T)in[k];
+  }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 1 / (1 + exp(-x)) and, to full relative precision, 1 minus it.  Where exp(-x)
+// is too large for its reciprocal the first is 0 and the second 1; NaN passes.
+__device__ __forceinline__ float sigmoid_pair(float x, float* rest) {
+  const float t = exp2_fast(-kLog2e * x);
+  const float s = __builtin_amdgcn_rcpf(1.f + t);
+  *rest = t > 0x1p126f ? 1.f : t * s;
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// 8 bits: x ~ q 2^E, |q| <= 127, E the smallest power with max|x| <= 127 2^E,
+// not below -126; stored as the byte E + 127.  Scaling by powers of two is
+// exact, so the one rounding is that to a whole number (to even).  A group
+// that holds Inf or NaN stores 255 and stands for NaN.  Values next to the
+// largest of x's type would round to a power of two past it: there q stops at 63.
+// ---------------------------------------------------------------------------
+constexpr int kExpNan = 255;
+
+// The group's byte from the largest bit pattern of |x| in it (NaN > Inf > finite).
+__device__ __forceinline__ int group_byte(uint32_t top) {
+  if (top >= 0x7f800000u) return kExpNan;
+  // top = m 2^k, m in [1/2, 1): E = k - 7 if m <= 127/128, else k - 6
+  const int k = (int)(top >> 23) - 126;
+  const int e = k - 7 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return max(e, -126) + 127;
+}
+
+__device__ __forceinline__ float pow2f(int n) {  // 2^n, -127 < n < 128
+  return __uint_as_float((uint32_t)(n + 127) << 23);
+}
+
+// The scale a stored byte stands for.
+__device__ __forceinline__ float group_scale(int byte) {
+  return byte == kExpNan ? __uint_as_float(0x7fc00000u) : pow2f(byte - 127);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The byte of the one scale whose 64 would be past the largest value of T
+// (2^16 for half, 2^128 else).
+template <typename T>
+constexpr int last_byte() { return 128 - 6 + 127; }
+template <>
+constexpr int last_byte<_Float16>() { return 16 - 6 + 127; }
+
+// Eight steps of one lane, of type T, in 8 bits; the lanes of a group are
+// `width` (<= 8) neighbours.  Returns the group's byte.
+template <typename T>
+__device__ __forceinline__ int quantise8(const float* x, int width, uint2* out) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, abs_bits(x[k]));
+  for (int o = 1; o < width; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  const int byte = group_byte(top);
+  const float inv = byte == kExpNan ? 0.f : pow2f(127 - byte);
+  int q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q[k] = byte == kExpNan ? 0 : (int)__builtin_rintf(x[k] * inv);
+  if (byte == last_byte<T>()) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q[k] = min(max(q[k], -63), 63);
+  }
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(q[k] & 255) << (8 * (k & 3));
+  *out = make_uint2(w[0], w[1]);
+  return byte;
+}
+
+__device__ __forceinline__ void dequantise8(uint2 q, int byte, float* x) {
+  const float s = group_scale(byte);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t w = k < 4 ? q.x : q.y;
+    x[k] = (float)(int)(int8_t)(w >> (8 * (k & 3))) * s;
+  }
+}
+
+}  // namespace dssm

@@ -23,10 +23,15 @@ pages define, in float64, from the float32 input values promoted exactly:
   Space Layers for Sequence Modeling", section 3, computed as a sequential
   recurrence and as a direct causal sum over a prefix; and its continuous-time
   form with a step size that changes from step to step (zero-order hold).
+* ``gated`` -- the gated linear recurrence stepped one step after another, its
+  gradients by the chain rule, and the values an 8-bit checkpoint stands for.
+* ``resnorm`` -- the norms around a layer with its gate and residual scale, and
+  their gradients.
 
 Parity status: every function is pinned by the ``-m "not gpu"`` tests in
 ``tests/test_oracle_pins.py`` (closed forms, a library DFT, brute-force
-Toeplitz/circulant matrices and invariants).  No function is "parity unpinned".
+Toeplitz/circulant matrices and invariants) and, for the last two,
+``tests/test_oracle_gated_pins.py`` (closed forms, differences).  No function is "parity unpinned".
 """
 
 from .dlr import (  # noqa: F401
@@ -39,3 +44,5 @@ from .dlr import (  # noqa: F401
 )
 from .dlr_grad import dlr_backward  # noqa: F401
 from .s5 import s5_recurrence, s5_direct_prefix, s5_recurrence_tv  # noqa: F401
+from .gated import gated_recurrence, gated_backward, ckpt8  # noqa: F401
+from .resnorm import resnorm_stream, resnorm_out, resnorm_backward  # noqa: F401

@@ -1,0 +1,325 @@
+"""GPU parity of the gated recurrence (forward, streaming, one token, backward
+from kept states and from 8 bits) against the float64 oracle."""
+import numpy as np
+import pytest
+
+import oracle
+from long_convolution_sequence_amd import binding as bd
+
+from seq_cases import (KINDS, STEP, c_gated, close, dtype_of, gated_inputs, lens_of, np64, say,
+                       spoil_padding, torch_)
+
+pytestmark = pytest.mark.gpu
+
+# (B, H, L, type, ragged): rows inside a lane, inside a wave, over several tiles of one wave
+# (many rows), of four waves, and split into segments; lengths around every border
+SHAPES = [
+    (2, 3, 1, "f32", False), (3, 5, 7, "bf16", True), (4, 3, 8, "f16", True), (2, 3, 9, "f32", False),
+    (3, 7, 63, "bf16", True), (3, 2, 64, "f32", True), (4, 3, 65, "f16", False),
+    (5, 3, 300, "f32", True), (2, 3, 511, "bf16", False), (3, 3, 512, "f32", True),
+    (3, 3, 513, "f32", True), (4, 5, 2047, "f16", True), (2, 3, 2048, "bf16", False),
+    (2, 3, 2049, "f32", False), (3, 2, 6145, "f32", True), (1, 1, 20000, "f32", False),
+    (4, 131, 2100, "bf16", True), (4, 2049, 530, "f16", True), (8, 1024, 1030, "f32", False),
+]
+IDS = ["B%dH%dL%d-%s%s" % (b, h, l, t, "-ragged" if r else "") for b, h, l, t, r in SHAPES]
+
+
+def prepared(B, H, L, dtype, ragged, seed, joint=False):
+    say("case: B=%d H=%d L=%d %s ragged=%d seed=%d" % (B, H, L, dtype, ragged, seed))
+    s = gated_inputs(B, H, L, dtype, seed, joint)
+    s["lens"] = lens_of(B, L, seed) if ragged else None
+    if ragged:
+        for k in ("u", "r", "i", "dy"):
+            spoil_padding(s[k], s["lens"])
+    return s
+
+
+def reference(s, **kw):
+    a = [np64(s[k]) for k in ("u", "r", "i", "log_re")]
+    lens = None if s["lens"] is None else s["lens"].cpu().numpy()
+    if s["lens"] is not None:
+        a[:3] = [np.nan_to_num(t) for t in a[:3]]
+    return oracle.gated_recurrence(*a, x0=np64(s["x0"]), lens=lens, **kw)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_forward_and_state(shape):
+    B, H, L, dtype, ragged = shape
+    torch = torch_()
+    s = prepared(*shape, seed=L + H, joint=L % 2 == 1)
+    xo = torch.full_like(s["x0"], float("nan"))
+    y = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"], x=s["x0"], x_out=xo, lens=s["lens"])
+    ref, end = reference(s)
+    mag, mend = reference(s, magnitude=True)
+    close(y, ref, mag, c_gated(L), dtype, "y")
+    close(xo, end, mend, c_gated(L), "f32", "state")
+
+
+@pytest.mark.parametrize("kind", ["state", "int8"])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_backward(shape, kind):
+    B, H, L, dtype, ragged = shape
+    torch = torch_()
+    s = prepared(*shape, seed=2 * L + H, joint=L % 2 == 0)
+    k = KINDS[kind]
+    y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], k, x=s["x0"],
+                                    x_out=torch.empty_like(s["x0"]), lens=s["lens"])
+    plain = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"], x=s["x0"],
+                             x_out=torch.empty_like(s["x0"]), lens=s["lens"])
+    assert torch.equal(y, plain)
+    kept = dict(u=s["u"], r=s["r"], i=s["i"]) if kind == "state" else {}
+    got = bd.gated_backward(s["dy"], ckpt, k, s["log_re"], dx=s["dx"], lens=s["lens"], **kept)
+    lens = None if s["lens"] is None else s["lens"].cpu().numpy()
+    u, r, i, dy = (np.nan_to_num(np64(s[n])) for n in ("u", "r", "i", "dy"))
+    nch = -(-L // 512)
+    # the states a checkpoint begins with are the forward pass's own
+    starts = np64(ckpt[:4 * B * H * nch].view(torch.float32).view(B, H, nch))
+    if kind == "int8":
+        u, r, i = (oracle.ckpt8(t) for t in (u, r, i))
+    args = (u, r, i, np64(s["log_re"]), dy, np64(s["dx"]), np64(s["x0"]), lens, starts)
+    ref = oracle.gated_backward(*args)
+    mag = oracle.gated_backward(*args, magnitude=True)
+    for n, v, m, t in zip(("du", "dr", "di", "dlog_re", "dx0"), ref, mag,
+                          (dtype, dtype, dtype, "f32", "f32")):
+        close(got[n], v, m, 2 * c_gated(L), t, n)
+    if ragged:
+        for b, n in enumerate(lens):
+            assert not np64(got["du"])[b, :, n:].any()
+    again = bd.gated_backward(s["dy"], ckpt, k, s["log_re"], dx=s["dx"], lens=s["lens"], **kept)
+    for n in got:
+        assert torch.equal(got[n], again[n]), n + " differs between two calls"
+
+
+def test_kept_states_are_the_forward_passes():
+    torch = torch_()
+    s = prepared(2, 3, 1700, "f32", False, seed=5)
+    _, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], x=s["x0"],
+                                    x_out=torch.empty_like(s["x0"]))
+    y, _ = reference(s)
+    mag, _ = reference(s, magnitude=True)
+    got = ckpt[:4 * 6 * 4].view(torch.float32).view(2, 3, 4)
+    assert torch.equal(got[..., 0], s["x0"])
+    for c in (1, 2, 3):
+        close(got[..., c], y[..., c * 512 - 1], mag[..., c * 512 - 1], c_gated(1700), "f32", "start")
+
+
+def test_eight_bits_hold_what_the_oracle_says():
+    """The three blobs of a checkpoint decode to the oracle's values, bit for bit."""
+    torch = torch_()
+    for L, ragged in ((70, True), (1000, False), (5, True)):
+        s = prepared(3, 4, L, "bf16", ragged, seed=L)
+        _, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], bd.CKPT_INT8,
+                                        lens=s["lens"])
+        off = (4 * 12 * -(-L // 512) + 255) // 256 * 256
+        n = bd.ckpt8_size((3, 4, L))
+        for k, name in enumerate(("u", "r", "i")):
+            got = bd.ckpt8_unpack(ckpt[off + k * n:off + (k + 1) * n], (3, 4, L), torch.float32)
+            assert np.array_equal(np64(got), oracle.ckpt8(np.nan_to_num(np64(s[name])))), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_stream_in_parts_and_tokens(dtype):
+    """Parts of a sequence, then single tokens, from the state the last left."""
+    torch = torch_()
+    B, H, L = 3, 37, 700
+    s = prepared(B, H, L, dtype, False, seed=11)
+    x = s["x0"].clone()
+    ys = []
+    for lo, hi in ((0, 1), (1, 600), (600, 697)):
+        part = [s[k][:, :, lo:hi].contiguous() for k in ("u", "r", "i")]
+        ys.append(bd.gated_forward(*part, s["log_re"], x=x))
+    for t in range(697, 700):
+        tok = [s[k][:, :, t].contiguous() for k in ("u", "r", "i")]
+        ys.append(bd.gated_step(*tok, s["log_re"], x)[..., None])
+    ref, end = reference(s)
+    mag, mend = reference(s, magnitude=True)
+    close(torch.cat(ys, -1), ref, mag, c_gated(L) + 40, dtype, "y")
+    close(x, end, mend, c_gated(L) + 40, "f32", "state")
+
+
+@pytest.mark.parametrize("B,H,dtype", [(1, 1, "f32"), (5, 63, "bf16"), (3, 1000, "f16"),
+                                       (64, 4096, "bf16"), (7, 2049, "f32")])
+def test_step(B, H, dtype):
+    """One token: slices of a joint projection, idle streams, old states kept."""
+    torch = torch_()
+    s = prepared(B, H, 1, dtype, False, seed=B + H, joint=True)
+    u, r, i = (s[k][..., 0] for k in ("u", "r", "i"))
+    s["lens"] = torch.tensor([b % 3 for b in range(B)], dtype=torch.int32, device="cuda")
+    for b in range(0, B, 3):
+        for t in (u, r, i):
+            t[b] = float("nan")
+    xo = torch.empty_like(s["x0"])
+    before = s["x0"].clone()
+    y = bd.gated_step(u, r, i, s["log_re"], s["x0"], x_out=xo, lens=s["lens"])
+    assert torch.equal(s["x0"], before)
+    s["lens"] = s["lens"].clamp(max=1)
+    ref, end = reference(s)
+    mag, mend = reference(s, magnitude=True)
+    close(y[..., None], ref, mag, 64, dtype, "y")
+    close(xo, end, mend, 64, "f32", "state")
+    assert torch.equal(xo[::3], before[::3])
+    y2 = bd.gated_step(u, r, i, s["log_re"], s["x0"], lens=s["lens"])
+    assert torch.equal(y2, y) and torch.equal(s["x0"], xo)
+
+
+def test_no_state_and_empty_sequences():
+    torch = torch_()
+    s = prepared(2, 3, 100, "f32", False, seed=3)
+    y = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"])
+    z = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"], x=torch.zeros_like(s["x0"]))
+    assert torch.equal(y, z)
+    none = s["u"][..., :0].contiguous()
+    xo = torch.full_like(s["x0"], float("nan"))
+    y, ckpt = bd.gated_forward_ckpt(none, none, none, s["log_re"], x=s["x0"], x_out=xo)
+    assert y.shape == (2, 3, 0) and torch.equal(xo, s["x0"])
+    g = bd.gated_backward(none, ckpt, bd.CKPT_STATE, s["log_re"], u=none, r=none, i=none,
+                          dx=s["dx"])
+    assert torch.equal(g["dx0"], s["dx"]) and not g["dlog_re"].any()
+    none = s["u"][:0].contiguous()
+    y, ckpt = bd.gated_forward_ckpt(none, none, none, s["log_re"])
+    g = bd.gated_backward(none, ckpt, bd.CKPT_STATE, s["log_re"], u=none, r=none, i=none)
+    assert y.shape == (0, 3, 100) and g["du"].shape == (0, 3, 100)
+    assert g["dlog_re"].shape == (3,) and not g["dlog_re"].any()
+
+
+def test_extreme_gates_and_parameters():
+    """log_re of 0 and tiny ones (no decay, no drive), gates open and shut beyond
+    exp's range: finite, and the oracle's values."""
+    torch = torch_()
+    B, H, L = 2, 6, 530
+    s = prepared(B, H, L, "f32", False, seed=9)
+    s["log_re"][:] = torch.tensor([0.0, -0.0, 1e-22, 1e-12, 3e-4, 30.0])
+    s["r"][0, :, :100], s["r"][0, :, 100:200] = 200.0, -200.0
+    s["i"][1, :, :100], s["i"][1, :, 100:200] = 200.0, -200.0
+    y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], x=s["x0"],
+                                    x_out=torch.empty_like(s["x0"]))
+    ref, _ = reference(s)
+    mag, _ = reference(s, magnitude=True)
+    # 1 - a^2 below 2^-126 counts as 0, so sqrt(1 - a^2) is off by up to 2^-63 in every step: at
+    # most L values of u, G or u G below 2^6 add that up where nothing decays.  close() multiplies
+    # a magnitude by c STEP, so the sum is divided by it.
+    lost = L * 2.0 ** 6 * 2.0 ** -63
+    # exp(-r log2(e)) at |r| = 200 carries 2 * 200 more roundings of its exponent
+    c = c_gated(L) + 400
+    close(y, ref, mag + lost / (c * STEP), c, "f32", "y")
+    got = bd.gated_backward(s["dy"], ckpt, bd.CKPT_STATE, s["log_re"], u=s["u"], r=s["r"],
+                            i=s["i"], dx=s["dx"])
+    starts = np64(ckpt[:4 * B * H * 2].view(torch.float32).view(B, H, 2))
+    args = tuple(np64(s[k]) for k in ("u", "r", "i", "log_re", "dy", "dx", "x0")) + (None, starts)
+    r, m = oracle.gated_backward(*args), oracle.gated_backward(*args, magnitude=True)
+    for n, v, g in zip(("du", "dr", "di", "dlog_re", "dx0"), r, m):
+        if n == "dlog_re":  # the channels whose 1 - a^2 is below float32's range count it as 0
+            assert torch.isfinite(got[n]).all() and not got[n][:2].any()
+            close(got[n][3:], v[3:], g[3:], 2 * c, "f32", n)
+        else:
+            close(got[n], v, g + lost / (2 * c * STEP), 2 * c, "f32", n)
+
+
+def test_a_bad_row_stays_its_own():
+    """NaN and Inf in one row's inputs leave every other row as it was."""
+    torch = torch_()
+    for L in (5, 40, 700):
+        s = prepared(3, 5, L, "f32", False, seed=L)
+        ref = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"])
+        for k, v in (("u", float("inf")), ("r", float("nan")), ("i", float("nan"))):
+            t = s[k].clone()
+            t[1, 2, L // 2] = v
+            y = bd.gated_forward(*[t if n == k else s[n] for n in ("u", "r", "i")], s["log_re"])
+            assert not torch.isfinite(y[1, 2, L // 2])
+            y[1, 2] = ref[1, 2]
+            assert torch.equal(y, ref)
+
+
+def test_gradients_into_slices_of_one_buffer():
+    torch = torch_()
+    B, H, L = 3, 10, 130
+    s = prepared(B, H, L, "bf16", False, seed=21, joint=True)
+    _, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"])
+    kept = dict(u=s["u"], r=s["r"], i=s["i"])
+    a = bd.gated_backward(s["dy"], ckpt, bd.CKPT_STATE, s["log_re"], **kept)
+    buf = torch.full((B, 3 * H + 1, L), 7.0, dtype=torch.bfloat16, device="cuda")
+    b = bd.gated_backward(s["dy"], ckpt, bd.CKPT_STATE, s["log_re"], du=buf[:, :H],
+                          dr=buf[:, H:2 * H], di=buf[:, 2 * H:3 * H], **kept)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+    assert (buf[:, 3 * H:] == 7.0).all()
+
+
+@pytest.mark.parametrize("shape", [(2, 3, 300), (2, 3, 9000)])
+def test_captured_and_replayed(shape):
+    """A captured forward and backward pass, replayed on new inputs with eager
+    work between the replays."""
+    torch = torch_()
+    B, H, L = shape
+    s = prepared(B, H, L, "bf16", False, seed=31)
+
+    def both():
+        y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], bd.CKPT_INT8,
+                                        x=s["x0"], x_out=s["xT"])
+        g = bd.gated_backward(s["dy"], ckpt, bd.CKPT_INT8, s["log_re"], dx=s["dx"])
+        return [y, s["xT"]] + [g[k] for k in ("du", "dr", "di", "dlog_re", "dx0")]
+
+    s["xT"] = torch.empty_like(s["x0"])
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for rep in range(4):
+        new = prepared(B, H, L, "bf16", False, seed=40 + rep)
+        for k in ("u", "r", "i", "dy", "x0", "dx", "log_re"):
+            s[k].copy_(new[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        for a, b in zip(got, both()):
+            assert torch.equal(a, b), rep
+
+
+def test_on_another_stream():
+    torch = torch_()
+    s = prepared(2, 4, 3000, "f32", False, seed=51)
+    ref = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"])
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    y = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"], stream=st)
+    st.synchronize()
+    assert torch.equal(y, ref)
+
+
+def test_binding_refuses():
+    torch = torch_()
+    s = prepared(2, 4, 64, "bf16", False, seed=61)
+    u, r, i, lr = s["u"], s["r"], s["i"], s["log_re"]
+    with pytest.raises(TypeError):
+        bd.gated_forward(u, r.float(), i, lr)
+    with pytest.raises(TypeError):
+        bd.gated_forward(u.double(), r.double(), i.double(), lr)
+    with pytest.raises(TypeError):
+        bd.gated_forward(u, r, i, lr.bfloat16())
+    for bad in (r[:, :, :32], r.transpose(1, 2).contiguous().transpose(1, 2), r.cpu(),
+                torch.empty(2, 8, 64, dtype=r.dtype, device="cuda")[:, ::2]):
+        with pytest.raises((ValueError, TypeError)):
+            bd.gated_forward(u, bad, i, lr)
+    with pytest.raises(ValueError):
+        bd.gated_forward(u, r, i, lr[:3].contiguous())
+    with pytest.raises(TypeError):
+        bd.gated_forward(u, r, i, lr, lens=torch.zeros(2, device="cuda"))
+    with pytest.raises(ValueError):
+        bd.gated_forward(u, r, i, lr, lens=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        bd.gated_forward(u, r, i, lr, y=torch.empty(2, 64, 4, dtype=u.dtype, device="cuda"))
+    with pytest.raises(bd.DSSMError):
+        bd.gated_forward(u, r, i, lr, y=u)
+    with pytest.raises(bd.DSSMError) as e:
+        bd.gated_forward(u, r, i, lr, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == bd.DSSM_ERR_WORKSPACE
+    _, ckpt = bd.gated_forward_ckpt(u, r, i, lr)
+    with pytest.raises(ValueError):
+        bd.gated_backward(s["dy"], ckpt, bd.CKPT_STATE, lr)
+    with pytest.raises(ValueError):
+        bd.gated_backward(s["dy"], ckpt, bd.CKPT_INT8, lr)  # too small for 8 bits
+    with pytest.raises(ValueError):
+        bd.gated_backward(s["dy"], ckpt, bd.CKPT_INT8, lr, u=u, r=r, i=i)
+    with pytest.raises(ValueError):
+        bd.gated_step(u, r, i, lr, s["x0"])
