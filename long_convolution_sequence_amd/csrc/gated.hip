@@ -25,39 +25,94 @@
 namespace dssm {
 namespace {
 
-constexpr float kTiny = 1.17549435e-38f;  // below it 1 - a^2 counts as 0 (no drive, no gradient)
+constexpr float kTiny = 1.17549435e-38f;
 
-struct Gate {
-  float a, q, s, w;  // decay, sigmoid(r), sigmoid(i), 1 - a^2
-  float nq, ns;      // 1 - q, 1 - s
-};
-
-// kappa = log_re^2 log2(e).  1 - a^2 loses its digits where a is close to 1:
-// there it is the series of 1 - exp(-x), x = 2 z, up to the term that 24 bits see.
-__device__ __forceinline__ Gate gate(float r, float i, float kappa, float* e) {
-  Gate g;
-  g.q = sigmoid_pair(r, &g.nq);
-  g.s = sigmoid_pair(i, &g.ns);
-  *e = kappa * g.q;
-  g.a = exp2_fast(-*e);
-  const float x = *e * (2.f / kLog2e);
-  const float far = fmaf(-g.a, g.a, 1.f);
-  // x (1 - x/2 (1 - x/3 (1 - x/4 (1 - x/5 (1 - x/6 (1 - x/7))))))
-  float p = fmaf(x, -1.f / 7.f, 1.f);
-  p = fmaf(x * p, -1.f / 6.f, 1.f);
-  p = fmaf(x * p, -1.f / 5.f, 1.f);
-  p = fmaf(x * p, -1.f / 4.f, 1.f);
-  p = fmaf(x * p, -1.f / 3.f, 1.f);
-  p = fmaf(x * p, -1.f / 2.f, 1.f);
-  g.w = x < 0.5f ? x * p : far;
-  if (!(g.w >= kTiny)) g.w = g.w != g.w ? g.w : 0.f;
-  return g;
+// 1 - exp2(-2 e) for small e: the series of 1 - exp(-x), x = 2 ln(2) e.
+// Where exp2(-e) is close to 1, 1 - a^2 would lose its digits.  The border
+// weighs the series' length against them: 16-bit outputs see 2^-12, so five
+// terms up to x = 1/4 (the sixth is 2^-19 of the first; above, 1 - a^2 keeps
+// 2^-22); float32 takes eight up to x = 1/2 (2^-27, 2^-23).
+template <typename T>
+__device__ __forceinline__ float one_minus_sq(float e, float a) {
+  constexpr double c = 2.0 * 0.69314718055994530942;
+  const float far = fmaf(-a, a, 1.f);
+  float p, edge;
+  if (sizeof(T) == 2) {
+    edge = (float)(0.25 / c);
+    p = (float)(c * c * c * c * c / 120.0);
+  } else {
+    edge = (float)(0.5 / c);
+    p = (float)(-c * c * c * c * c * c * c * c / 40320.0);
+    p = fmaf(p, e, (float)(c * c * c * c * c * c * c / 5040.0));
+    p = fmaf(p, e, (float)(-c * c * c * c * c * c / 720.0));
+    p = fmaf(p, e, (float)(c * c * c * c * c / 120.0));
+  }
+  p = fmaf(p, e, (float)(-c * c * c * c / 24.0));
+  p = fmaf(p, e, (float)(c * c * c / 6.0));
+  p = fmaf(p, e, (float)(-c * c / 2.0));
+  p = fmaf(p, e, (float)c);
+  return e < edge ? p * e : far;
 }
 
-// Inclusive scan over groups of n lanes (n a power of two), in time order or
-// (REV) against it: (S1, V1) then (S2, V2) = (S1 + S2, exp2(-S2) V1 + V2).
+// A value from another lane, by the data-parallel primitives of the vector
+// unit; lanes the pattern does not reach get 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL,
+                                                               ROWS, 0xf, CTRL < 0x140));
+}
+constexpr int kRowShl = 0x100, kRowShr = 0x110, kWaveShl = 0x130, kWaveShr = 0x138,
+              kBcast15 = 0x142, kBcast31 = 0x143;
+
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void pair_step(float& S, float& V) {
+  const float Sp = dpp<CTRL, ROWS>(S), Vp = dpp<CTRL, ROWS>(V);
+  V = fmaf(exp2_fast(-S), Vp, V);
+  S += Sp;
+}
+
+// Inclusive scan over a wave, in time order or (REV) against it: (S1, V1)
+// then (S2, V2) = (S1 + S2, exp2(-S2) V1 + V2).  Lanes without a neighbour
+// join (0, 0), which changes nothing.
 template <bool REV>
-__device__ __forceinline__ void pair_scan(float& S, float& V, int gl, int n) {
+__device__ __forceinline__ void wave_scan(float& S, float& V) {
+  if (!REV) {
+    pair_step<kRowShr + 1, 0xf>(S, V);
+    pair_step<kRowShr + 2, 0xf>(S, V);
+    pair_step<kRowShr + 4, 0xf>(S, V);
+    pair_step<kRowShr + 8, 0xf>(S, V);
+    pair_step<kBcast15, 0xa>(S, V);  // rows 1 and 3 join the row before
+    pair_step<kBcast31, 0xc>(S, V);  // rows 2 and 3 join the first half
+  } else {
+    pair_step<kRowShl + 1, 0xf>(S, V);
+    pair_step<kRowShl + 2, 0xf>(S, V);
+    pair_step<kRowShl + 4, 0xf>(S, V);
+    pair_step<kRowShl + 8, 0xf>(S, V);
+    const int lane = threadIdx.x & 63;
+    {  // rows 0 and 2 join the row after
+      const bool in = !(lane & 16);
+      const float S1 = lane_of(S, 16), V1 = lane_of(V, 16);
+      const float S3 = lane_of(S, 48), V3 = lane_of(V, 48);
+      const float Sp = in ? (lane & 32 ? S3 : S1) : 0.f, Vp = in ? (lane & 32 ? V3 : V1) : 0.f;
+      V = fmaf(exp2_fast(-S), Vp, V);
+      S += Sp;
+    }
+    {  // the first half joins the second
+      const float Sh = lane_of(S, 32), Vh = lane_of(V, 32);
+      const float Sp = lane < 32 ? Sh : 0.f, Vp = lane < 32 ? Vh : 0.f;
+      V = fmaf(exp2_fast(-S), Vp, V);
+      S += Sp;
+    }
+  }
+}
+
+// The same over groups of n lanes (n a power of two), for short rows.
+template <bool REV>
+__device__ __forceinline__ void group_scan(float& S, float& V, int gl, int n) {
   for (int o = 1; o < n; o <<= 1) {
     const float Sp = REV ? __shfl_down(S, o) : __shfl_up(S, o);
     const float Vp = REV ? __shfl_down(V, o) : __shfl_up(V, o);
@@ -68,14 +123,26 @@ __device__ __forceinline__ void pair_scan(float& S, float& V, int gl, int n) {
   }
 }
 
-// The neighbour's inclusive pair (nothing before the first lane).
-template <bool REV>
+// The neighbour's inclusive pair ((0, 0) at the first lane).
+template <bool REV, bool SHORT>
 __device__ __forceinline__ void pair_shift(float& S, float& V, int gl, int n) {
-  const float Sp = REV ? __shfl_down(S, 1) : __shfl_up(S, 1);
-  const float Vp = REV ? __shfl_down(V, 1) : __shfl_up(V, 1);
-  const bool first = REV ? gl == n - 1 : gl == 0;
-  S = first ? 0.f : Sp;
-  V = first ? 0.f : Vp;
+  S = dpp<REV ? kWaveShl : kWaveShr, 0xf>(S);
+  V = dpp<REV ? kWaveShl : kWaveShr, 0xf>(V);
+  if (SHORT && (REV ? gl == n - 1 : gl == 0)) S = V = 0.f;
+}
+
+// Scans a tile and leaves each lane what enters it; St, Vt: the whole tile's
+// pair (for rows of whole waves).
+template <bool REV, bool SHORT>
+__device__ __forceinline__ void tile_scan(float& S, float& V, int gl, int n, float* St,
+                                          float* Vt) {
+  if (SHORT)
+    group_scan<REV>(S, V, gl, n);
+  else
+    wave_scan<REV>(S, V);
+  *St = lane_of(S, REV ? 0 : 63);
+  *Vt = lane_of(V, REV ? 0 : 63);
+  pair_shift<REV, SHORT>(S, V, gl, n);
 }
 
 // What enters segment `seg` of a split row: the pairs of the segments before
@@ -91,8 +158,8 @@ __device__ float join_segments(const float2* agg, int nseg, int seg, float start
     float2 t = make_float2(0.f, 0.f);
     if (j < count) t = agg[REV ? nseg - 1 - j : j];
     float S = t.x, V = t.y;
-    pair_scan<false>(S, V, lane, 64);
-    c = fmaf(exp2_fast(-__shfl(S, 63)), c, __shfl(V, 63));
+    wave_scan<false>(S, V);
+    c = fmaf(exp2_fast(-lane_of(S, 63)), c, lane_of(V, 63));
   }
   return c;
 }
@@ -123,58 +190,130 @@ struct Args {
   int lpr;          // lanes per row (64 unless rows are short)
 };
 
-__device__ __forceinline__ int row_len(const Args& p, long row) {
+__device__ __forceinline__ int row_len(const Args& p, long b) {
   if (!p.lens) return p.L;
-  return min(max(p.lens[row / p.H], 0), p.L);
+  return min(max(p.lens[b], 0), p.L);
 }
 
 __device__ __forceinline__ int clamp8(int n) { return min(max(n, 0), 8); }
 
-// u, r, i of a lane's 8 steps from step t (nv of them live), from the inputs
-// or (Q8) their 8-bit form; dead steps are 0.
-template <typename T, bool Q8>
-__device__ __forceinline__ void load_one(const Args& p, const void* x, int which, long row, int t,
-                                         int nv, float* out) {
-  if (Q8) {
+// Eight steps of one lane as they lie in memory, so that the next tile's can be
+// on their way while this one is worked on.  Steps that are not live hold
+// `fill`: for the recurrence gate -inf, which shuts it (a = 1, no drive, no
+// gradient), for the others 0.
+template <typename T>
+struct Raw {
+  typename VecOf<T, 8>::type v;
+  __device__ __forceinline__ void fetch(const T* p, int nv, T fill) {
+    if (nv == 8) {
+      v = *reinterpret_cast<const typename VecOf<T, 8>::type*>(p);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) out[k] = 0.f;
-    if (nv > 0) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p.q8[which] + (size_t)row * ckpt8_row(p.L) + t);
-      const int byte = p.e8[which][(size_t)row * ckpt8_groups(p.L) + t / kGroup];
-      dequantise8(q, byte, out);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) out[k] = k < nv ? out[k] : 0.f;
+      for (int k = 0; k < 8; ++k) v[k] = k < nv ? p[k] : fill;
     }
-  } else {
-    const long b = row / p.H;
-    const T* base = static_cast<const T*>(x) + b * p.sb + (row - b * p.H) * p.L;
-    load_n<T, 8>(base + t, nv, out);
   }
-}
+  __device__ __forceinline__ void get(float* out, int, float) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out[k] = (float)v[k];
+  }
+};
+
+// The same of a row in 8 bits.
+struct Raw8 {
+  uint2 q;
+  int byte;
+  __device__ __forceinline__ void fetch(const int8_t* q8, const uint8_t* e8, int t, int nv) {
+    q = make_uint2(0, 0);
+    byte = 1;
+    if (nv > 0) {
+      q = *reinterpret_cast<const uint2*>(q8 + t);
+      byte = e8[t / kGroup];
+    }
+  }
+  __device__ __forceinline__ void get(float* out, int nv, float fill) const {
+    dequantise8(q, byte, out);
+    if (nv < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) out[k] = k < nv ? out[k] : fill;
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ T shut() { return (T)(-__builtin_inff()); }
+
+// u, r and i of a row, from the inputs or (Q8) their 8-bit form.
+template <typename T, bool Q8>
+struct Source {
+  const T *u, *r, *i;
+  __device__ Source(const Args& p, long row, long b) {
+    const size_t at = (size_t)(b * p.sb + (row - b * p.H) * p.L);
+    u = static_cast<const T*>(p.u) + at;
+    r = static_cast<const T*>(p.r) + at;
+    i = static_cast<const T*>(p.i) + at;
+  }
+  struct Tile {
+    Raw<T> u, r, i;
+  };
+  __device__ __forceinline__ void fetch_r(Tile& x, int t, int nv) const {
+    x.r.fetch(r + t, nv, shut<T>());
+  }
+  __device__ __forceinline__ void fetch(Tile& x, int t, int nv) const {
+    x.u.fetch(u + t, nv, (T)0.f);
+    x.r.fetch(r + t, nv, shut<T>());
+    x.i.fetch(i + t, nv, (T)0.f);
+  }
+};
+
+template <typename T>
+struct Source<T, true> {
+  const int8_t* q[3];
+  const uint8_t* e[3];
+  __device__ Source(const Args& p, long row, long) {
+#pragma unroll
+    for (int m = 0; m < 3; ++m) {
+      q[m] = p.q8[m] + (size_t)row * ckpt8_row(p.L);
+      e[m] = p.e8[m] + (size_t)row * ckpt8_groups(p.L);
+    }
+  }
+  struct Tile {
+    Raw8 u, r, i;
+  };
+  __device__ __forceinline__ void fetch_r(Tile& x, int t, int nv) const {
+    x.r.fetch(q[1], e[1], t, nv);
+  }
+  __device__ __forceinline__ void fetch(Tile& x, int t, int nv) const {
+    x.u.fetch(q[0], e[0], t, nv);
+    x.r.fetch(q[1], e[1], t, nv);
+    x.i.fetch(q[2], e[2], t, nv);
+  }
+};
 
 // Which row, segment and lanes a thread works on.  WPR waves share a row; with
-// WPR == 1 a workgroup of 4 waves holds 4 rows, or 4 (64 / lpr) short ones.
-template <int WPR>
+// WPR == 1 a workgroup of 4 waves holds 4 rows, or (SHORT: rows of at most
+// 256 steps) 4 (64 / n) of them, n lanes each.
+template <int WPR, bool SHORT>
 struct Place {
-  long row;
-  int seg, gl, n, wave, lane;
+  long row, b;
+  int seg, gl, n, wave, lane, t0;
   bool live;
   __device__ Place(const Args& p) {
     lane = threadIdx.x & 63;
-    wave = threadIdx.x >> 6;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     seg = 0;
-    n = 64;
+    n = SHORT ? p.lpr : 64;
+    gl = SHORT ? lane & (n - 1) : lane;
     if (WPR == 1) {
-      n = p.lpr;
-      gl = lane & (n - 1);
-      row = ((long)blockIdx.x * 4 + wave) * (64 / n) + lane / n;
+      row = (long)blockIdx.x * 4 + wave;
+      if (SHORT) row = row * (64 / n) + lane / n;
     } else {
-      gl = lane;
       row = blockIdx.x / p.nseg;
-      seg = blockIdx.x % p.nseg;
+      seg = blockIdx.x - (int)row * p.nseg;
     }
     live = row < p.rows;
     if (!live) row = p.rows - 1;
+    b = row / p.H;
+    t0 = (WPR > 1 ? wave * kChunk : 0) + gl * 8;
   }
 };
 
@@ -185,7 +324,7 @@ constexpr int threads_of() { return WPR == 1 ? 256 : 64 * WPR; }
 // what enters it and what leaves the tile.  One barrier: the buffers alternate.
 template <int WPR, bool REV>
 __device__ __forceinline__ float tile_carry(float2 (*tot)[WPR], int flip, int wave, int lane,
-                                            float S, float V, float& carry) {
+                                            float S, float V, float& carry, float* Ssum) {
   if (WPR == 1) {
     const float in = carry;
     carry = fmaf(exp2_fast(-S), carry, V);
@@ -200,68 +339,76 @@ __device__ __forceinline__ float tile_carry(float2 (*tot)[WPR], int flip, int wa
     if (w == wave) in = c;
     const float2 t = tot[flip][w];
     c = fmaf(exp2_fast(-t.x), c, t.y);
+    if (Ssum) *Ssum += t.x;
   }
   carry = c;
   return in;
 }
 
+// log_re^2 log2(e), finite unless NaN: a shut gate times it has to be 0.
+__device__ __forceinline__ float kappa_of(float lr2) {
+  const float k = lr2 * kLog2e;
+  return k > 3.4e38f ? 3.4e38f : k;
+}
+
 // Forward over a row (or one segment of it).  AGG: only the segment's pair.
 // CK: 0 nothing kept, 1 the state entering every chunk, 2 also u, r, i in 8 bits.
-template <typename T, int WPR, int CK, bool AGG>
+template <typename T, int WPR, int CK, bool SHORT, bool AGG>
 __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
   __shared__ float2 tot[2][WPR];
-  const Place<WPR> at(p);
-  const int len = row_len(p, at.row);
-  const float lr = p.log_re[at.row % p.H];
-  const float kappa = lr * lr * kLog2e;
-  const int tile = kChunk * WPR;
+  const Place<WPR, SHORT> at(p);
+  const int len = at.live ? row_len(p, at.b) : 0;
+  const int end = at.live ? p.L : 0;
+  const float lr = p.log_re[at.row - at.b * p.H];
+  const float kappa = kappa_of(lr * lr);
+  constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  const Source<T, false> src(p, at.row, at.b);
+  typename Source<T, false>::Tile next;
+  if (t_lo < t_hi) src.fetch(next, t_lo * tile + at.t0, clamp8(len - t_lo * tile - at.t0));
   float carry = (p.x0 && !AGG) ? p.x0[at.row] : 0.f;
   if (WPR > 1 && !AGG && p.nseg > 1)
     carry = join_segments<false>(p.agg + at.row * p.nseg, p.nseg, at.seg, carry);
   float Sseg = 0.f;
   for (int k = t_lo; k < t_hi; ++k) {
-    const int t = k * tile + (WPR > 1 ? at.wave * kChunk : 0) + at.gl * 8;
-    const int nv = at.live ? clamp8(len - t) : 0;
-    const int ns = at.live ? clamp8(p.L - t) : 0;
+    const int t = k * tile + at.t0;
+    const int nv = clamp8(len - t);
+    const typename Source<T, false>::Tile now = next;
+    if (k + 1 < t_hi) src.fetch(next, t + tile, clamp8(len - t - tile));
     float u[8], r[8], i[8], a[8], b[8];
-    load_one<T, false>(p, p.u, 0, at.row, t, nv, u);
-    load_one<T, false>(p, p.r, 1, at.row, t, nv, r);
-    load_one<T, false>(p, p.i, 2, at.row, t, nv, i);
+    now.u.get(u, nv, 0.f);
+    now.r.get(r, nv, 0.f);
+    now.i.get(i, nv, 0.f);
     float S = 0.f, V = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float e;
-      const Gate g = gate(r[j], i[j], kappa, &e);
-      const bool in = j < nv;
-      a[j] = in ? g.a : 1.f;
-      b[j] = in ? __builtin_amdgcn_sqrtf(g.w) * (g.s * u[j]) : 0.f;
-      S += in ? e : 0.f;
+      float rest;
+      const float e = kappa * sigmoid_pair(r[j], &rest);
+      const float s = sigmoid_pair(i[j], &rest);
+      a[j] = exp2_fast(-e);
+      b[j] = __builtin_amdgcn_sqrtf(one_minus_sq<T>(e, a[j])) * (s * u[j]);
+      S += e;
       V = fmaf(a[j], V, b[j]);
     }
-    pair_scan<false>(S, V, at.gl, at.n);
-    const float St = __shfl(S, 63), Vt = __shfl(V, 63);  // used where a wave is one row's
-    pair_shift<false>(S, V, at.gl, at.n);
-    Sseg += St;
-    const float in = tile_carry<WPR, false>(tot, (k - t_lo) & 1, at.wave, at.lane, St, Vt, carry);
-    if (AGG) {
-      // the segment's exponent sum: every wave's part
-      if (WPR > 1) {
-#pragma unroll
-        for (int w = 0; w < WPR; ++w)
-          if (w != at.wave) Sseg += tot[(k - t_lo) & 1][w].x;
-      }
-      continue;
-    }
-    if (CK >= 1 && at.live && at.gl == 0 && t < p.L)
+    float St, Vt;
+    tile_scan<false, SHORT>(S, V, at.gl, at.n, &St, &Vt);
+    const float in = tile_carry<WPR, false>(tot, (k - t_lo) & 1, at.wave, at.lane, St, Vt, carry,
+                                            AGG ? &Sseg : nullptr);
+    if (AGG) continue;
+    const int ns = clamp8(end - t);
+    if (CK >= 1 && at.gl == 0 && t < end)
       p.bounds[(size_t)at.row * ((p.L + kChunk - 1) / kChunk) + t / kChunk] = in;
     if (CK == 2) {
+      if (nv < 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = j < nv ? r[j] : 0.f;
+      }
       const float* x[3] = {u, r, i};
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         uint2 q;
-        const int byte = quantise8<T>(x[m], min(8, at.n), &q);
+        const int byte = quantise8<T>(x[m], SHORT ? min(8, at.n) : 8, &q);
         if (ns > 0) {
           *reinterpret_cast<uint2*>(p.q8[m] + (size_t)at.row * ckpt8_row(p.L) + t) = q;
           if ((t & (kGroup - 1)) == 0)
@@ -274,12 +421,14 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       h = fmaf(a[j], h, b[j]);
-      y[j] = j < nv ? h : 0.f;
+      y[j] = h;
+    }
+    if (nv < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = j < nv ? y[j] : 0.f;
     }
     store_n<T, 8>(static_cast<T*>(p.y) + (size_t)at.row * p.L + t, ns, y);
-    if (WPR == 1 && at.n < 64) {  // short rows: the last lane's state is the row's
-      carry = __shfl(h, at.lane | (at.n - 1));
-    }
+    if (SHORT) carry = __shfl(h, at.lane | (at.n - 1));  // the last lane's state is the row's
   }
   if (!at.live) return;
   if (AGG) {
@@ -294,34 +443,37 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
 template <typename T, int WPR, bool Q8>
 __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_agg_kernel(Args p) {
   __shared__ float2 tot[2][WPR];
-  const Place<WPR> at(p);
-  const int len = row_len(p, at.row);
-  const float lr = p.log_re[at.row % p.H];
-  const float kappa = lr * lr * kLog2e;
-  const int tile = kChunk * WPR;
+  const Place<WPR, false> at(p);
+  const int len = row_len(p, at.b);
+  const float lr = p.log_re[at.row - at.b * p.H];
+  const float kappa = kappa_of(lr * lr);
+  constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  const Source<T, Q8> src(p, at.row, at.b);
+  const T* dyp = static_cast<const T*>(p.dy) + (size_t)at.row * p.L;
   float carry = 0.f, Sseg = 0.f;
   for (int k = t_hi - 1; k >= t_lo; --k) {
-    const int t = k * tile + at.wave * kChunk + at.gl * 8;
+    const int t = k * tile + at.t0;
     const int nv = clamp8(len - t);
+    typename Source<T, Q8>::Tile now;
+    Raw<T> g;
+    src.fetch_r(now, t, nv);
+    g.fetch(dyp + t, nv, (T)0.f);
     float r[8], dy[8];
-    load_one<T, Q8>(p, p.r, 1, at.row, t, nv, r);
-    load_n<T, 8>(static_cast<const T*>(p.dy) + (size_t)at.row * p.L + t, nv, dy);
+    now.r.get(r, nv, -__builtin_inff());
+    g.get(dy, nv, 0.f);
     float S = 0.f, V = 0.f;
 #pragma unroll
     for (int j = 7; j >= 0; --j) {
-      float nq;
-      const float e = j < nv ? kappa * sigmoid_pair(r[j], &nq) : 0.f;
+      float rest;
+      const float e = kappa * sigmoid_pair(r[j], &rest);
       V = exp2_fast(-e) * (dy[j] + V);
       S += e;
     }
-    pair_scan<true>(S, V, at.gl, 64);
-    const int flip = (t_hi - 1 - k) & 1;
-    const float St = __shfl(S, 0), Vt = __shfl(V, 0);
-    tile_carry<WPR, true>(tot, flip, at.wave, at.lane, St, Vt, carry);
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) Sseg += tot[flip][w].x;
+    float St, Vt;
+    tile_scan<true, false>(S, V, at.gl, 64, &St, &Vt);
+    tile_carry<WPR, true>(tot, (t_hi - 1 - k) & 1, at.wave, at.lane, St, Vt, carry, &Sseg);
   }
   if (threadIdx.x == 0) p.agg[at.row * p.nseg + at.seg] = make_float2(Sseg, carry);
 }
@@ -329,93 +481,118 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_agg_kernel(Args p
 // Backward over a row (or one segment of it), tiles from the last to the
 // first.  Each wave's tile is one chunk, whose entering state the checkpoint
 // holds: the states need no walk of their own.
-template <typename T, int WPR, bool Q8>
+template <typename T, int WPR, bool SHORT, bool Q8>
 __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_kernel(Args p) {
   __shared__ float2 tot[2][WPR];
   __shared__ double red[threads_of<WPR>() / 64];
-  const Place<WPR> at(p);
-  const int len = row_len(p, at.row);
-  const float lr = p.log_re[at.row % p.H];
+  const Place<WPR, SHORT> at(p);
+  const int len = at.live ? row_len(p, at.b) : 0;
+  const int end = at.live ? p.L : 0;
+  const float lr = p.log_re[at.row - at.b * p.H];
   const float lr2 = lr * lr;
-  const float kappa = lr2 * kLog2e;
-  const long b = at.row / p.H;
-  const size_t gbase = (size_t)(b * p.sdb + (at.row - b * p.H) * p.L);
-  const int tile = kChunk * WPR;
+  const float kappa = kappa_of(lr2);
+  const size_t gbase = (size_t)(at.b * p.sdb + (at.row - at.b * p.H) * p.L);
+  constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int nch = (p.L + kChunk - 1) / kChunk;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  const Source<T, Q8> src(p, at.row, at.b);
+  const T* dyp = static_cast<const T*>(p.dy) + (size_t)at.row * p.L;
+  const float* bounds = p.bounds + (size_t)at.row * nch;
+  typename Source<T, Q8>::Tile next;
+  Raw<T> next_g;
+  float next_x = 0.f;
+  auto fetch = [&](int k) {
+    const int t = k * tile + at.t0;
+    src.fetch(next, t, clamp8(len - t));
+    next_g.fetch(dyp + t, clamp8(len - t), (T)0.f);
+    next_x = bounds[min(t / kChunk, nch - 1)];
+  };
+  if (t_lo < t_hi) fetch(t_hi - 1);
   float carry = p.dx ? p.dx[at.row] : 0.f;
   if (WPR > 1 && p.nseg > 1)
     carry = join_segments<true>(p.agg + at.row * p.nseg, p.nseg, at.seg, carry);
   double acc = 0.0;
   for (int k = t_hi - 1; k >= t_lo; --k) {
-    const int t = k * tile + (WPR > 1 ? at.wave * kChunk : 0) + at.gl * 8;
-    const int nv = at.live ? clamp8(len - t) : 0;
-    const int ns = at.live ? clamp8(p.L - t) : 0;
-    float u[8], r[8], i[8], dy[8], a[8], e[8], hp[8];
-    load_one<T, Q8>(p, p.u, 0, at.row, t, nv, u);
-    load_one<T, Q8>(p, p.r, 1, at.row, t, nv, r);
-    load_one<T, Q8>(p, p.i, 2, at.row, t, nv, i);
-    load_n<T, 8>(static_cast<const T*>(p.dy) + (size_t)at.row * p.L + t, nv, dy);
-    const int ch = min(t / kChunk, nch - 1);
-    const float bound = p.bounds[(size_t)at.row * nch + ch];
+    const int t = k * tile + at.t0;
+    const int nv = clamp8(len - t);
+    const typename Source<T, Q8>::Tile now = next;
+    const Raw<T> g = next_g;
+    const float bound = next_x;
+    if (k > t_lo) fetch(k - 1);
+    float u[8], r[8], i[8], dy[8];
+    now.u.get(u, nv, 0.f);
+    now.r.get(r, nv, -__builtin_inff());
+    now.i.get(i, nv, 0.f);
+    g.get(dy, nv, 0.f);
+    float a[8], q[8], qn[8], b[8], bn[8], c2[8], hp[8];
     // the states before each step, from the chunk's entering state
     float S = 0.f, V = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const Gate g = gate(r[j], i[j], kappa, &e[j]);
-      if (j >= nv) e[j] = 0.f;
-      a[j] = j < nv ? g.a : 1.f;
-      hp[j] = j < nv ? __builtin_amdgcn_sqrtf(g.w) * (g.s * u[j]) : 0.f;  // b_j for now
-      S += e[j];
-      V = fmaf(a[j], V, hp[j]);
+      float sn;
+      q[j] = sigmoid_pair(r[j], &qn[j]);
+      const float s = sigmoid_pair(i[j], &sn);
+      const float e = kappa * q[j];
+      a[j] = exp2_fast(-e);
+      const float w = one_minus_sq<T>(e, a[j]);
+      const float rs = __builtin_amdgcn_rsqf(w < kTiny ? kTiny : w);  // 1 / beta
+      const float B = w * rs * s;  // du = G B
+      b[j] = B;
+      bn[j] = sn;
+      c2[j] = a[j] * rs;  // a / beta
+      S += e;
+      V = fmaf(a[j], V, B * u[j]);
     }
     const float Sl = S;
-    pair_scan<false>(S, V, at.gl, at.n);
-    pair_shift<false>(S, V, at.gl, at.n);
+    float St, Vt;
+    tile_scan<false, SHORT>(S, V, at.gl, at.n, &St, &Vt);
     float h = fmaf(exp2_fast(-S), bound, V);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float bj = hp[j];
       hp[j] = h;
-      h = fmaf(a[j], h, bj);
+      h = fmaf(a[j], h, b[j] * u[j]);
     }
     // the gradients entering each lane from the right
     S = Sl;
     V = 0.f;
 #pragma unroll
     for (int j = 7; j >= 0; --j) V = a[j] * (dy[j] + V);
-    pair_scan<true>(S, V, at.gl, at.n);
-    const float St = __shfl(S, 0), Vt = __shfl(V, 0);  // used where a wave is one row's
-    pair_shift<true>(S, V, at.gl, at.n);
-    const float in =
-        tile_carry<WPR, true>(tot, (t_hi - 1 - k) & 1, at.wave, at.lane, St, Vt, carry);
+    tile_scan<true, SHORT>(S, V, at.gl, at.n, &St, &Vt);
+    const float in = tile_carry<WPR, true>(tot, (t_hi - 1 - k) & 1, at.wave, at.lane, St, Vt,
+                                           carry, nullptr);
     float c = fmaf(exp2_fast(-S), in, V);
-    float sum = 0.f;
 #pragma unroll
     for (int j = 7; j >= 0; --j) {
-      float ej;
-      const Gate g = gate(r[j], i[j], kappa, &ej);
       const float G = dy[j] + c;
-      const float rs = g.w > 0.f ? __builtin_amdgcn_rsqf(g.w) : (g.w != g.w ? g.w : 0.f);
-      const float beta = g.w * rs;
-      const float db = G * g.s;  // gradient of beta u
-      const float aG = a[j] * G;
-      const float dz = fmaf(db * u[j], g.a * g.a * rs, -aG * hp[j]);
-      c = aG;
-      const float bu = db * beta;
-      const float di_ = bu * u[j] * g.ns;
-      const float dzq = dz * g.q;
-      sum += j < nv ? dzq : 0.f;
-      u[j] = j < nv ? bu : 0.f;
-      i[j] = j < nv ? di_ : 0.f;
-      r[j] = j < nv ? dzq * g.nq * lr2 : 0.f;
+      c = a[j] * G;
+      const float du = G * b[j];
+      const float gb = du * u[j];
+      const float dz = fmaf(gb * c2[j], c2[j], -c * hp[j]);
+      u[j] = du;
+      i[j] = gb * bn[j];
+      r[j] = dz * q[j];
+    }
+    if (nv < 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] = j < nv ? u[j] : 0.f;
+        r[j] = j < nv ? r[j] : 0.f;
+        i[j] = j < nv ? i[j] : 0.f;
+      }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sum += r[j];
+      r[j] *= qn[j] * lr2;
     }
     acc += (double)sum;
+    const int ns = clamp8(end - t);
     store_n<T, 8>(static_cast<T*>(p.du) + gbase + t, ns, u);
     store_n<T, 8>(static_cast<T*>(p.dr) + gbase + t, ns, r);
     store_n<T, 8>(static_cast<T*>(p.di) + gbase + t, ns, i);
-    if (WPR == 1 && at.n < 64) carry = __shfl(c, at.lane & ~(at.n - 1));
+    if (SHORT) carry = __shfl(c, at.lane & ~(at.n - 1));
   }
   if (p.dx0 && at.live && at.gl == 0 && (WPR == 1 || (threadIdx.x == 0 && at.seg == 0)))
     p.dx0[at.row] = carry;
@@ -450,32 +627,42 @@ __global__ __launch_bounds__(256) void gated_dlog_kernel(const double* __restric
   if ((threadIdx.x & 63) == 0) dlog_re[h] = (float)(2.0 * (double)log_re[h] * s);
 }
 
-// One token for every (b, h).
-template <typename T>
+// One token for every (b, h); V neighbouring channels to a thread.
+template <typename T, int V>
 __global__ __launch_bounds__(256) void gated_step_kernel(const T* __restrict__ u,
                                                          const T* __restrict__ r,
                                                          const T* __restrict__ i, long long sb,
                                                          const float* __restrict__ log_re,
-                                                         const int* __restrict__ lens, long n,
-                                                         int H, const float* x0, float* x,
-                                                         T* __restrict__ y) {
-  const long k = (long)blockIdx.x * 256 + threadIdx.x;
+                                                         const int* __restrict__ lens, unsigned n,
+                                                         unsigned per, int H, const float* x0,
+                                                         float* x, T* __restrict__ y) {
+  const unsigned k = blockIdx.x * 256 + threadIdx.x;
   if (k >= n) return;
-  const long b = k / H;
-  const long h = k - b * H;
-  const float xv = x0 ? x0[k] : 0.f;
-  if (lens && lens[b] <= 0) {  // an idle stream: no input is read
-    y[k] = (T)0.f;
-    if (x) x[k] = xv;
-    return;
+  const unsigned b = k / per;
+  const int h = (int)(k - b * per) * V;
+  const size_t row = (size_t)b * H + h;
+  const int m = min(V, H - h);
+  float xv[V], uv[V], rv[V], iv[V], lr[V], yv[V];
+  // an idle stream's inputs are not read
+  const int live = lens && lens[b] <= 0 ? 0 : m;
+  load_n<float, V>(x0 ? x0 + row : log_re + h, x0 ? m : 0, xv);
+  load_n<T, V>(u + b * sb + h, live, uv);
+  load_n<T, V>(r + b * sb + h, live, rv);
+  load_n<T, V>(i + b * sb + h, live, iv);
+  load_n<float, V>(log_re + h, live, lr);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float rest;
+    const float e = kappa_of(lr[j] * lr[j]) * sigmoid_pair(rv[j], &rest);
+    const float s = sigmoid_pair(iv[j], &rest);
+    const float a = exp2_fast(-e);
+    const float v =
+        fmaf(a, xv[j], __builtin_amdgcn_sqrtf(one_minus_sq<float>(e, a)) * (s * uv[j]));
+    xv[j] = live ? v : xv[j];
+    yv[j] = live ? v : 0.f;
   }
-  const float lr = log_re[h];
-  float e;
-  const long at = b * sb + h;
-  const Gate g = gate((float)r[at], (float)i[at], lr * lr * kLog2e, &e);
-  const float v = fmaf(g.a, xv, __builtin_amdgcn_sqrtf(g.w) * (g.s * (float)u[at]));
-  if (x) x[k] = v;
-  y[k] = (T)v;
+  if (x) store_n<float, V>(x + row, m, xv);
+  store_n<T, V>(y + row, m, yv);
 }
 
 // Waves per row, lanes per row and segments per row.
@@ -497,7 +684,7 @@ Plan plan_of(long rows, int L) {
   p.wpr = 4;
   const int ntile = (L + 4 * kChunk - 1) / (4 * kChunk);
   // few rows: segments of whole tiles, about 1024 workgroups in all
-  long nseg = rows >= 512 ? 1 : std::min<long>(ntile, (1024 + rows - 1) / rows);
+  const long nseg = rows >= 512 ? 1 : std::min<long>(ntile, (1024 + rows - 1) / rows);
   p.seg_tiles = (int)((ntile + nseg - 1) / nseg);
   p.nseg = (ntile + p.seg_tiles - 1) / p.seg_tiles;
   return p;
@@ -548,25 +735,36 @@ unsigned grid_of(const Plan& p, long rows) {
   return (unsigned)((rows + per - 1) / per);
 }
 
-template <typename T, int WPR>
+template <typename T, int WPR, bool SHORT>
 hipError_t fwd_launch(const Args& a, const Plan& pl, int kind, hipStream_t st) {
   const dim3 grid(grid_of(pl, a.rows)), block(threads_of<WPR>());
-  if (pl.nseg > 1)
-    hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 0, true>), grid, block, 0, st, a);
+  if constexpr (WPR > 1) {
+    if (pl.nseg > 1)
+      hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 0, false, true>), grid, block, 0, st, a);
+  }
   switch (kind) {
-    case 0: hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 0, false>), grid, block, 0, st, a); break;
-    case 1: hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 1, false>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 2, false>), grid, block, 0, st, a); break;
+    case 0: hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 0, SHORT, false>), grid, block, 0, st, a); break;
+    case 1: hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 1, SHORT, false>), grid, block, 0, st, a); break;
+    default: hipLaunchKernelGGL((gated_fwd_kernel<T, WPR, 2, SHORT, false>), grid, block, 0, st, a); break;
   }
   return hipGetLastError();
 }
 
-template <typename T, int WPR, bool Q8>
+template <typename T, int WPR, bool SHORT, bool Q8>
 hipError_t bwd_launch(const Args& a, const Plan& pl, hipStream_t st) {
   const dim3 grid(grid_of(pl, a.rows)), block(threads_of<WPR>());
-  if (pl.nseg > 1) hipLaunchKernelGGL((gated_bwd_agg_kernel<T, WPR, Q8>), grid, block, 0, st, a);
-  hipLaunchKernelGGL((gated_bwd_kernel<T, WPR, Q8>), grid, block, 0, st, a);
+  if constexpr (WPR > 1) {
+    if (pl.nseg > 1) hipLaunchKernelGGL((gated_bwd_agg_kernel<T, WPR, Q8>), grid, block, 0, st, a);
+  }
+  hipLaunchKernelGGL((gated_bwd_kernel<T, WPR, SHORT, Q8>), grid, block, 0, st, a);
   return hipGetLastError();
+}
+
+template <typename T, bool Q8>
+hipError_t bwd_plan(const Args& a, const Plan& pl, hipStream_t st) {
+  if (pl.wpr > 1) return bwd_launch<T, 4, false, Q8>(a, pl, st);
+  return pl.lpr < 64 ? bwd_launch<T, 1, true, Q8>(a, pl, st)
+                     : bwd_launch<T, 1, false, Q8>(a, pl, st);
 }
 
 template <typename T>
@@ -575,27 +773,33 @@ hipError_t gated_run(const GatedCall& c, bool backward, hipStream_t st) {
   const Plan pl = plan_of(rows, c.L);
   const Args a = make_args(c, pl);
   if (!backward) {
-    return pl.wpr == 1 ? fwd_launch<T, 1>(a, pl, c.kind, st) : fwd_launch<T, 4>(a, pl, c.kind, st);
+    if (pl.wpr > 1) return fwd_launch<T, 4, false>(a, pl, c.kind, st);
+    return pl.lpr < 64 ? fwd_launch<T, 1, true>(a, pl, c.kind, st)
+                       : fwd_launch<T, 1, false>(a, pl, c.kind, st);
   }
-  hipError_t e;
-  if (c.kind == 2)
-    e = pl.wpr == 1 ? bwd_launch<T, 1, true>(a, pl, st) : bwd_launch<T, 4, true>(a, pl, st);
-  else
-    e = pl.wpr == 1 ? bwd_launch<T, 1, false>(a, pl, st) : bwd_launch<T, 4, false>(a, pl, st);
+  const hipError_t e = c.kind == 2 ? bwd_plan<T, true>(a, pl, st) : bwd_plan<T, false>(a, pl, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(gated_dlog_kernel, dim3((unsigned)((c.H + 3) / 4)), dim3(256), 0, st, a.part,
                      c.log_re, c.B, c.H, pl.nseg, c.dlog_re);
   return hipGetLastError();
 }
 
+template <typename T, int V>
+hipError_t step_launch(const GatedCall& c, hipStream_t st) {
+  const unsigned per = (unsigned)(c.H + V - 1) / V;
+  const unsigned n = (unsigned)c.B * per;
+  hipLaunchKernelGGL((gated_step_kernel<T, V>), dim3((n + 255) / 256), dim3(256), 0, st,
+                     static_cast<const T*>(c.u), static_cast<const T*>(c.r),
+                     static_cast<const T*>(c.i), c.stride_b, c.log_re, c.lens, n, per, c.H, c.x0,
+                     c.xT, static_cast<T*>(c.y));
+  return hipGetLastError();
+}
+
+// Up to 2^17 channels a thread each fills the device sooner; more are
+// bound by memory and take four to a thread.
 template <typename T>
 hipError_t step_run(const GatedCall& c, hipStream_t st) {
-  const long n = (long)c.B * c.H;
-  hipLaunchKernelGGL((gated_step_kernel<T>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st,
-                     static_cast<const T*>(c.u), static_cast<const T*>(c.r),
-                     static_cast<const T*>(c.i), c.stride_b, c.log_re, c.lens, n, c.H, c.x0, c.xT,
-                     static_cast<T*>(c.y));
-  return hipGetLastError();
+  return (long)c.B * c.H <= (1L << 17) ? step_launch<T, 1>(c, st) : step_launch<T, 4>(c, st);
 }
 
 }  // namespace
