@@ -538,8 +538,8 @@ typedef struct {
  * float32 [2, B, L] (1 / sqrt of y, of o) for DSSM_NORM_RMS, [4, B, L] (mean and
  * 1 / sqrt of y, then of o) for DSSM_NORM_LAYER; rows of a norm that the call
  * does not form are not written.  Requires H <= 8192 (a workgroup holds the
- * channels of a few steps; larger H: DSSM_ERR_UNSUPPORTED) and
- * B ceil(L / 4) <= 2^22.
+ * channels of a few steps; larger H: DSSM_ERR_UNSUPPORTED), L <= 2^20
+ * and B ceil(L / 4) <= 2^22.
  * A single token is L = 1. */
 int dssm_resnorm_forward(const void* x, const void* y, const void* g, long long stride_g,
                          const dssm_resnorm_params* p, const dssm_resnorm_shape* s,

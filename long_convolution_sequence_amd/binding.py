@@ -583,16 +583,25 @@ def s5_forward_tv(u, lam_c, Bt, C, D, delta, step, y=None, workspace=None, strea
 # the gated recurrence, 8-bit checkpoints, the residual norm
 # ----------------------------------------------------------------------------
 
+# The checks below pass a good tensor in a few attribute reads (a single token's
+# call costs about as much on the host as on the device); what is wrong with a
+# bad one is found out only then.
+
 def _dtype_code(t, name):
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        dt = t.dtype
+        if dt is torch.bfloat16:
+            return BF16
+        if dt is torch.float32:
+            return F32
+        if dt is torch.float16:
+            return F16
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
-    if code is None:
+    if t.dtype not in (torch.float32, torch.bfloat16, torch.float16):
         raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
-    return code
+    raise ValueError("%s must be a device tensor" % name)
 
 
 def _like(t, name, ref, refname):
@@ -600,7 +609,7 @@ def _like(t, name, ref, refname):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype != ref.dtype:
+    if t.dtype is not ref.dtype:
         raise TypeError("%s is %s, %s is %s" % (name, t.dtype, refname, ref.dtype))
     if t.device != ref.device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, ref.device))
@@ -617,11 +626,26 @@ def _plain(t, name, ref, refname):
     return t
 
 
+def _vec(t, name, numel, device):
+    """Address of a contiguous float32 device tensor of `numel` elements."""
+    torch = _torch()
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.numel() == numel
+            and t.device == device and t.is_contiguous()):
+        t = _dev_f32(t, name, numel, device)
+    return t.data_ptr()
+
+
+def _opt_vec(t, name, numel, device):
+    return None if t is None else _vec(t, name, numel, device)
+
+
 def _batch_stride(t, name):
     """Elements between the batch rows of t [B, H, L] (or [B, H]), whose H L
     elements are contiguous."""
-    inner = t.shape[1] * t.shape[2] if t.dim() == 3 else t.shape[1]
-    if t.numel() == 0:
+    inner = 1
+    for n in t.shape[1:]:
+        inner *= n
+    if t.is_contiguous():
         return inner
     st = t.stride()
     want = 1
@@ -636,11 +660,11 @@ def _batch_stride(t, name):
     return st[0]
 
 
-def _one_stride(ts):
-    out = [_batch_stride(t, name) for t, name in ts]
-    if any(s != out[0] for s in out):
-        raise ValueError("%s must have the same batch stride" % ", ".join(n for _, n in ts))
-    return out[0]
+def _one_stride(a, b, c, names):
+    s = _batch_stride(a, names[0])
+    if _batch_stride(b, names[1]) != s or _batch_stride(c, names[2]) != s:
+        raise ValueError("%s, %s and %s must have the same batch stride" % names)
+    return s
 
 
 def _lens_ptr(lens, B, device):
@@ -658,24 +682,38 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch_on(device, stream):
-    """Makes `device` the current one for a launch and gives the stream to
-    launch on: the caller's, or the device's current one."""
-    import contextlib
-
+def _new(t, stream):
+    """An uninitialised contiguous tensor of t's shape and type, on `stream`."""
     torch = _torch()
-    if stream is not None and stream.device != device:
+    if stream is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current, on the caller's stream or the
+    device's current one; a failure raises."""
+    torch = _torch()
+    if stream is None:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    elif stream.device != device:
         raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    here = torch.cuda.current_device() == device.index
-    return (contextlib.nullcontext() if here else torch.cuda.device(device)), s.cuda_stream
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != DSSM_OK:
+        check(status)
 
 
 def _bytes(fn, args, given, name, device, stream):
     """A workspace or checkpoint of the size fn reports: the caller's, or new."""
     torch = _torch()
     need = ctypes.c_size_t(0)
-    check(fn(*(args + [ctypes.byref(need)])))
+    check(fn(*args, ctypes.byref(need)))
     if given is None:
         with _on_stream(stream):
             given = torch.empty(max(need.value, 256), dtype=torch.uint8, device=device)
@@ -693,31 +731,24 @@ def _gated_rows(u, r, i, dims):
         raise ValueError("u must be %s" % ("[B, H, L]" if dims == 3 else "[B, H]"))
     _like(r, "r", u, "u")
     _like(i, "i", u, "u")
-    return code, _one_stride([(u, "u"), (r, "r"), (i, "i")])
+    return code, _one_stride(u, r, i, ("u", "r", "i"))
 
 
 def _gated_forward(u, r, i, log_re, kind, x, x_out, lens, y, ckpt, workspace, stream):
-    torch = _torch()
     code, sb = _gated_rows(u, r, i, 3)
     B, H, L = u.shape
     dev = u.device
-    lr = _dev_f32(log_re, "log_re", H, dev)
-    xx = None if x is None else _dev_f32(x, "x", B * H, dev)
-    xo = xx if x_out is None else _dev_f32(x_out, "x_out", B * H, dev)
-    if y is None:
-        y = _empty(u.shape, u.dtype, dev, stream)
-    _plain(y, "y", u, "u")
-    lp = _lens_ptr(lens, B, dev)
-    shape = GatedShape(B, H, L, code)
-    sp = ctypes.byref(shape)
-    with_dev, st = _launch_on(dev, stream)
-    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, [sp], workspace, "workspace", dev, stream)
+    inp = GatedInputs(u.data_ptr(), r.data_ptr(), i.data_ptr(), sb, _vec(log_re, "log_re", H, dev),
+                      _lens_ptr(lens, B, dev))
+    xp = _opt_vec(x, "x", B * H, dev)
+    xo = xp if x_out is None else _vec(x_out, "x_out", B * H, dev)
+    y = _new(u, stream) if y is None else _plain(y, "y", u, "u")
+    sp = ctypes.byref(GatedShape(B, H, L, code))
+    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, (sp,), workspace, "workspace", dev, stream)
     if kind != CKPT_NONE:
-        ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, [sp, kind], ckpt, "ckpt", dev, stream)
-    inp = GatedInputs(u.data_ptr(), r.data_ptr(), i.data_ptr(), sb, lr.data_ptr(), lp)
-    with with_dev:
-        check(lib().dssm_gated_forward(ctypes.byref(inp), sp, _ptr(xx), _ptr(xo), y.data_ptr(),
-                                       kind, _ptr(ckpt), ws.data_ptr(), nbytes, st))
+        ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, (sp, kind), ckpt, "ckpt", dev, stream)
+    _launch(lib().dssm_gated_forward, dev, stream, ctypes.byref(inp), sp, xp, xo, y.data_ptr(),
+            kind, _ptr(ckpt), ws.data_ptr(), nbytes)
     return y, ckpt
 
 
@@ -750,19 +781,13 @@ def gated_step(u_t, r_t, i_t, log_re, x, x_out=None, lens=None, y=None, stream=N
     code, sb = _gated_rows(u_t, r_t, i_t, 2)
     B, H = u_t.shape
     dev = u_t.device
-    lr = _dev_f32(log_re, "log_re", H, dev)
-    xx = _dev_f32(x, "x", B * H, dev)
-    xo = xx if x_out is None else _dev_f32(x_out, "x_out", B * H, dev)
-    if y is None:
-        y = _empty(u_t.shape, u_t.dtype, dev, stream)
-    _plain(y, "y", u_t, "u_t")
-    shape = GatedShape(B, H, 1, code)
-    inp = GatedInputs(u_t.data_ptr(), r_t.data_ptr(), i_t.data_ptr(), sb, lr.data_ptr(),
-                      _lens_ptr(lens, B, dev))
-    with_dev, st = _launch_on(dev, stream)
-    with with_dev:
-        check(lib().dssm_gated_step(ctypes.byref(inp), ctypes.byref(shape), xx.data_ptr(),
-                                    xo.data_ptr(), y.data_ptr(), st))
+    inp = GatedInputs(u_t.data_ptr(), r_t.data_ptr(), i_t.data_ptr(), sb,
+                      _vec(log_re, "log_re", H, dev), _lens_ptr(lens, B, dev))
+    xp = _vec(x, "x", B * H, dev)
+    xo = xp if x_out is None else _vec(x_out, "x_out", B * H, dev)
+    y = _new(u_t, stream) if y is None else _plain(y, "y", u_t, "u_t")
+    _launch(lib().dssm_gated_step, dev, stream, ctypes.byref(inp),
+            ctypes.byref(GatedShape(B, H, 1, code)), xp, xo, y.data_ptr())
     return y
 
 
@@ -789,29 +814,24 @@ def gated_backward(dy, ckpt, kind, log_re, u=None, r=None, i=None, dx=None, lens
             raise ValueError("CKPT_STATE keeps states only: u, r and i are needed")
         for t, name in ((u, "u"), (r, "r"), (i, "i")):
             _like(t, name, dy, "dy")
-        sb = _one_stride([(u, "u"), (r, "r"), (i, "i")])
+        sb = _one_stride(u, r, i, ("u", "r", "i"))
     elif u is not None or r is not None or i is not None:
         raise ValueError("CKPT_INT8 holds u, r and i itself: pass none")
-    lr = _dev_f32(log_re, "log_re", H, dev)
-    dxx = None if dx is None else _dev_f32(dx, "dx", B * H, dev)
     out = {}
     for name, t in (("du", du), ("dr", dr), ("di", di)):
-        out[name] = _empty(dy.shape, dy.dtype, dev, stream) if t is None else _like(t, name, dy, "dy")
-    gsb = _one_stride([(out[k], k) for k in ("du", "dr", "di")])
+        out[name] = _new(dy, stream) if t is None else _like(t, name, dy, "dy")
+    gsb = _one_stride(out["du"], out["dr"], out["di"], ("du", "dr", "di"))
     out["dlog_re"] = _empty((H,), torch.float32, dev, stream)
     out["dx0"] = _empty((B, H), torch.float32, dev, stream)
-    shape = GatedShape(B, H, L, code)
-    sp = ctypes.byref(shape)
-    with_dev, st = _launch_on(dev, stream)
-    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, [sp], workspace, "workspace", dev, stream)
-    ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, [sp, kind], ckpt, "ckpt", dev, stream)
-    inp = GatedInputs(_ptr(u), _ptr(r), _ptr(i), sb, lr.data_ptr(), _lens_ptr(lens, B, dev))
+    sp = ctypes.byref(GatedShape(B, H, L, code))
+    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, (sp,), workspace, "workspace", dev, stream)
+    ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, (sp, kind), ckpt, "ckpt", dev, stream)
+    inp = GatedInputs(_ptr(u), _ptr(r), _ptr(i), sb, _vec(log_re, "log_re", H, dev),
+                      _lens_ptr(lens, B, dev))
     g = GatedGrads(out["du"].data_ptr(), out["dr"].data_ptr(), out["di"].data_ptr(), gsb,
                    out["dlog_re"].data_ptr(), out["dx0"].data_ptr())
-    with with_dev:
-        check(lib().dssm_gated_backward(ctypes.byref(inp), sp, kind, ckpt.data_ptr(),
-                                        dy.data_ptr(), _ptr(dxx), ctypes.byref(g), ws.data_ptr(),
-                                        nbytes, st))
+    _launch(lib().dssm_gated_backward, dev, stream, ctypes.byref(inp), sp, kind, ckpt.data_ptr(),
+            dy.data_ptr(), _opt_vec(dx, "dx", B * H, dev), ctypes.byref(g), ws.data_ptr(), nbytes)
     return out
 
 
@@ -839,10 +859,8 @@ def ckpt8_pack(x, blob=None, stream=None):
         raise ValueError("x must be contiguous")
     rows, L = _rows_of(x.shape)
     dev = x.device
-    blob, _ = _bytes(lib().dssm_ckpt8_size, [rows, L], blob, "blob", dev, stream)
-    with_dev, st = _launch_on(dev, stream)
-    with with_dev:
-        check(lib().dssm_ckpt8_pack(x.data_ptr(), rows, L, code, blob.data_ptr(), st))
+    blob, _ = _bytes(lib().dssm_ckpt8_size, (rows, L), blob, "blob", dev, stream)
+    _launch(lib().dssm_ckpt8_pack, dev, stream, x.data_ptr(), rows, L, code, blob.data_ptr())
     return blob
 
 
@@ -854,15 +872,13 @@ def ckpt8_unpack(blob, shape, dtype, x=None, stream=None):
     shape = tuple(shape)
     rows, L = _rows_of(shape)
     dev = blob.device
-    _bytes(lib().dssm_ckpt8_size, [rows, L], blob, "blob", dev, stream)
+    _bytes(lib().dssm_ckpt8_size, (rows, L), blob, "blob", dev, stream)
     if x is None:
         x = _empty(shape, dtype, dev, stream)
     code = _dtype_code(x, "x")
     if tuple(x.shape) != shape or x.dtype != dtype or x.device != dev or not x.is_contiguous():
         raise ValueError("x must be a contiguous %s tensor of %s on %s" % (dtype, shape, dev))
-    with_dev, st = _launch_on(dev, stream)
-    with with_dev:
-        check(lib().dssm_ckpt8_unpack(blob.data_ptr(), rows, L, code, x.data_ptr(), st))
+    _launch(lib().dssm_ckpt8_unpack, dev, stream, blob.data_ptr(), rows, L, code, x.data_ptr())
     return x
 
 
@@ -875,18 +891,18 @@ def _resnorm_dims(x, name):
 
 def _resnorm_params(w_post, scale, w_pre, H, dev, y, n):
     def vec(t, name, used):
-        return _dev_f32(t, name, H, dev) if used or t is not None else None
+        return _vec(t, name, H, dev) if used or t is not None else None
 
-    keep = (vec(w_post, "w_post", y), vec(scale, "scale", y), vec(w_pre, "w_pre", n))
-    return ResnormParams(*[_ptr(t) for t in keep]), keep
+    return ctypes.byref(ResnormParams(vec(w_post, "w_post", y), vec(scale, "scale", y),
+                                      vec(w_pre, "w_pre", n)))
 
 
 def _resnorm_forward(x, y, g, w_post, scale, w_pre, norm, eps, lens, o, n, stats, stream):
-    torch = _torch()
     code = _dtype_code(x, "x")
     B, H, L = _resnorm_dims(x, "x")
     dev = x.device
-    _plain(x, "x", x, "x")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if y is None and (g is not None or o is not None):
         raise ValueError("a gate or a stream output needs y")
     if y is None and w_pre is None:
@@ -894,23 +910,19 @@ def _resnorm_forward(x, y, g, w_post, scale, w_pre, norm, eps, lens, o, n, stats
     sg = 0
     if y is not None:
         _plain(y, "y", x, "x")
-        o = _empty(x.shape, x.dtype, dev, stream) if o is None else _plain(o, "o", x, "x")
+        o = _new(x, stream) if o is None else _plain(o, "o", x, "x")
         if g is not None:
             sg = _batch_stride(_like(g, "g", x, "x"), "g")
     if w_pre is not None:
-        n = _empty(x.shape, x.dtype, dev, stream) if n is None else _plain(n, "n", x, "x")
+        n = _new(x, stream) if n is None else _plain(n, "n", x, "x")
     elif n is not None:
         raise ValueError("n needs w_pre")
-    prm, keep = _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, n is not None)
     if stats is True:
-        stats = _empty((4 if norm == NORM_LAYER else 2, B, L), torch.float32, dev, stream)
-    shape = ResnormShape(B, H, L, code, int(norm), float(eps))
-    with_dev, st = _launch_on(dev, stream)
-    with with_dev:
-        check(lib().dssm_resnorm_forward(x.data_ptr(), _ptr(y), _ptr(g), sg, ctypes.byref(prm),
-                                         ctypes.byref(shape), _lens_ptr(lens, B, dev), _ptr(o),
-                                         _ptr(n), _ptr(stats), st))
-    del keep
+        stats = _empty((4 if norm == NORM_LAYER else 2, B, L), _torch().float32, dev, stream)
+    _launch(lib().dssm_resnorm_forward, dev, stream, x.data_ptr(), _ptr(y), _ptr(g), sg,
+            _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, n is not None),
+            ctypes.byref(ResnormShape(B, H, L, code, int(norm), float(eps))),
+            _lens_ptr(lens, B, dev), _ptr(o), _ptr(n), _ptr(stats))
     return o, n, stats
 
 
@@ -941,7 +953,8 @@ def resnorm_backward(o, y, g, stats, w_post, scale, w_pre, do, dn, norm=NORM_RMS
     code = _dtype_code(o, "o")
     B, H, L = _resnorm_dims(o, "o")
     dev = o.device
-    _plain(o, "o", o, "o")
+    if not o.is_contiguous():
+        raise ValueError("o must be contiguous")
     if y is None and g is not None:
         raise ValueError("a gate needs y")
     if dn is not None and w_pre is None:
@@ -950,33 +963,26 @@ def resnorm_backward(o, y, g, stats, w_post, scale, w_pre, do, dn, norm=NORM_RMS
         if t is not None:
             _plain(t, name, o, "o")
     sg = 0 if g is None else _batch_stride(_like(g, "g", o, "o"), "g")
-    rows = 4 if norm == NORM_LAYER else 2
-    st_ = _dev_f32(stats, "stats", rows * B * L, dev)
-    prm, keep = _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, dn is not None)
-    new = lambda: _empty(o.shape, o.dtype, dev, stream)
     vec = lambda: _empty((H,), torch.float32, dev, stream)
-    out = dict(dx=new(), dy=None if y is None else new(), dg=None, dw_post=None, dscale=None,
-               dw_pre=vec())
+    out = dict(dx=_new(o, stream), dy=None if y is None else _new(o, stream), dg=None,
+               dw_post=None, dscale=None, dw_pre=vec())
     sdg = 0
     if y is not None:
         out["dw_post"], out["dscale"] = vec(), vec()
     if g is not None:
-        out["dg"] = new() if dg is None else _like(dg, "dg", o, "o")
+        out["dg"] = _new(o, stream) if dg is None else _like(dg, "dg", o, "o")
         sdg = _batch_stride(out["dg"], "dg")
     elif dg is not None:
         raise ValueError("dg needs g")
-    shape = ResnormShape(B, H, L, code, int(norm), 0.0)
-    sp = ctypes.byref(shape)
-    with_dev, st = _launch_on(dev, stream)
-    ws, nbytes = _bytes(lib().dssm_resnorm_workspace_size, [sp], workspace, "workspace", dev,
+    sp = ctypes.byref(ResnormShape(B, H, L, code, int(norm), 0.0))
+    ws, nbytes = _bytes(lib().dssm_resnorm_workspace_size, (sp,), workspace, "workspace", dev,
                         stream)
     gr = ResnormGrads(_ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dg"]), sdg,
                       _ptr(out["dw_post"]), _ptr(out["dscale"]), _ptr(out["dw_pre"]))
-    with with_dev:
-        check(lib().dssm_resnorm_backward(o.data_ptr(), _ptr(y), _ptr(g), sg, st_.data_ptr(),
-                                          ctypes.byref(prm), sp, _lens_ptr(lens, B, dev), _ptr(do),
-                                          _ptr(dn), ctypes.byref(gr), ws.data_ptr(), nbytes, st))
-    del keep
+    _launch(lib().dssm_resnorm_backward, dev, stream, o.data_ptr(), _ptr(y), _ptr(g), sg,
+            _vec(stats, "stats", (4 if norm == NORM_LAYER else 2) * B * L, dev),
+            _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, dn is not None), sp,
+            _lens_ptr(lens, B, dev), _ptr(do), _ptr(dn), ctypes.byref(gr), ws.data_ptr(), nbytes)
     return out
 
 

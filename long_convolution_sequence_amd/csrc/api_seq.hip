@@ -315,6 +315,8 @@ static int check_resnorm(const dssm_resnorm_shape* s, bool* empty) {
     return fail(DSSM_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (s->H > kResnormMaxH)
     return fail(DSSM_ERR_UNSUPPORTED, "resnorm: H=%d exceeds %d", s->H, kResnormMaxH);
+  if (s->L > kResnormMaxL)
+    return fail(DSSM_ERR_UNSUPPORTED, "resnorm: L=%d exceeds %d", s->L, kResnormMaxL);
   // strips of four steps at least
   if ((long)s->B * ((s->L + 3) / 4) > kMaxStrips)
     return fail(DSSM_ERR_UNSUPPORTED, "resnorm: B*ceil(L/4)=%ld exceeds 2^22",

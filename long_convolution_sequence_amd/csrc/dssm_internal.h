@@ -309,6 +309,7 @@ hipError_t launch_ckpt8_unpack(const void* blob, long rows, int L, int dtype, vo
 // Residual norm (resnorm.hip)
 // ---------------------------------------------------------------------------
 constexpr int kResnormMaxH = 8192;
+constexpr int kResnormMaxL = 1 << 20;  // a workgroup's channels lie within 32 bits of bytes
 struct ResnormCall {
   const void *x, *y, *g;  // y null: only n = norm(x) w_pre;  g null: no gate
   long long stride_g;     // elements between batch rows of g

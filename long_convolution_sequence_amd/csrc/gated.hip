@@ -203,18 +203,11 @@ __device__ __forceinline__ int clamp8(int n) { return min(max(n, 0), 8); }
 // gradient), for the others 0.
 template <typename T>
 struct Raw {
-  typename VecOf<T, 8>::type v;
-  __device__ __forceinline__ void fetch(const T* p, int nv, T fill) {
-    if (nv == 8) {
-      v = *reinterpret_cast<const typename VecOf<T, 8>::type*>(p);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = k < nv ? p[k] : fill;
-    }
-  }
+  Packed<T, 8> v;
+  __device__ __forceinline__ void fetch(const T* p, int nv, T fill) { v.load(p, nv, fill); }
   __device__ __forceinline__ void get(float* out, int, float) const {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) out[k] = (float)v[k];
+    for (int k = 0; k < 8; ++k) out[k] = v[k];
   }
 };
 

@@ -32,390 +32,556 @@ struct Args {
   long long sg;
   const float *w_post, *scale, *w_pre;
   const int* lens;
-  int B, H, L, ntile;  // strips per batch row
+  int B, H, L;
+  int ntile, per;  // strips of a batch row, strips of a die
   float eps;
   void *o, *n;
   float* stats;
   const void *d_o, *d_n;
   void *dx, *dy, *dg;
   long long sdg;
-  float* part;         // [workgroups][3][H]
+  float* part;         // [workgroups][2][H]
 };
 
-// v summed over the LT lanes of one channel.
+// A value from another lane of its row of 16, by the data-parallel primitives.
+template <int CTRL>
+__device__ __forceinline__ float row_move(float x) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+
+// v added up over pairs of rows of 16 lanes, and over the wave's halves.
+__device__ __forceinline__ float rows_sum(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// v summed over the LT lanes of one channel; all of them get the sum.
 template <int LT>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < LT; o <<= 1) v += __shfl_xor(v, o);
+  if (LT >= 2) v += row_move<0xb1>(v);    // neighbours swapped
+  if (LT >= 4) v += row_move<0x4e>(v);    // pairs swapped
+  if (LT >= 8) v += row_move<0x141>(v);   // mirrored in 8 lanes, whose fours agree by now
+  if (LT >= 16) v += row_move<0x140>(v);  // mirrored in 16
   return v;
 }
 
-// v[0..VE) summed over the workgroup's lanes of the same strip column; every
-// thread gets the totals.  buf: [NT / 64][LT VE] floats.  Two barriers.
-template <int NT, int LT, int VE>
-__device__ __forceinline__ void strip_sum(float* v, float* buf) {
+// v summed over the lanes of a wave that hold the same steps (every LT-th).
+template <int LT>
+__device__ __forceinline__ float column_sum(float v) {
+  if (LT <= 1) v += row_move<0xb1>(v);
+  if (LT <= 2) v += row_move<0x4e>(v);   // the pairs' lanes keep their place
+  if (LT <= 4) v += row_move<0x124>(v);  // rotated by 4: with the next, every fourth of 16
+  if (LT <= 8) v += row_move<0x128>(v);  // rotated by 8
+  return halves_sum(rows_sum(v));
+}
+
+// N sets of VE values summed over the workgroup's lanes of the same strip
+// column; every thread gets the totals.  buf: [NT / 64][N LT VE] floats.  More
+// than four waves are added up by one thread per column, so that not every
+// thread reads every wave's sums.
+template <int NT, int LT, int VE, int N>
+__device__ __forceinline__ void strip_sum(float (*v)[VE], float* buf) {
+  constexpr int W = NT / 64, C = N * LT * VE;
 #pragma unroll
-  for (int o = LT; o < 64; o <<= 1)
+  for (int m = 0; m < N; ++m)
 #pragma unroll
-    for (int k = 0; k < VE; ++k) v[k] += __shfl_xor(v[k], o);
+    for (int k = 0; k < VE; ++k) v[m][k] = column_sum<LT>(v[m][k]);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lt = lane % LT;
   __syncthreads();  // the buffer's last readers are done
   if (lane < LT)
 #pragma unroll
-    for (int k = 0; k < VE; ++k) buf[wave * (LT * VE) + lt * VE + k] = v[k];
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int k = 0; k < VE; ++k) buf[wave * C + (m * LT + lt) * VE + k] = v[m][k];
   __syncthreads();
+  if (W > 4) {
+    if (threadIdx.x < C) {
+      float s = 0.f;
 #pragma unroll
-  for (int k = 0; k < VE; ++k) v[k] = 0.f;
-  for (int w = 0; w < NT / 64; ++w)
+      for (int w = 0; w < W; ++w) s += buf[w * C + threadIdx.x];
+      buf[threadIdx.x] = s;  // its own column: no other thread reads it before the barrier
+    }
+    __syncthreads();
+  }
 #pragma unroll
-    for (int k = 0; k < VE; ++k) v[k] += buf[w * (LT * VE) + lt * VE + k];
+  for (int m = 0; m < N; ++m)
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      float s = buf[(m * LT + lt) * VE + k];
+      if (W <= 4)
+#pragma unroll
+        for (int w = 1; w < W; ++w) s += buf[w * C + (m * LT + lt) * VE + k];
+      v[m][k] = s;
+    }
 }
 
-// Mean (layer norm) and factor of the columns held in h[KH], per step.
-template <typename T, bool LAYER, int NT, int LT, int VE, int KH, typename Vec>
+// Strips to workgroups: each of the 8 dies takes a run of neighbouring strips,
+// which share the ends of their 128-byte lines in its cache (workgroups go to
+// the dies in turn).  `per` strips to a die; the last dies' numbers run past n.
+__device__ __forceinline__ int strip_of_block(int block, int per) {
+  return (block & 7) * per + (block >> 3);
+}
+
+// Mean (layer norm) and factor of the columns held in a[KH], per step.
+template <bool LAYER, int NT, int LT, int VE, int KH, typename Vec>
 __device__ __forceinline__ void column_stats(const Vec* a, int H, int rs, float inv_h, float eps,
-                                             int nv, float* buf, float* mean, float* rstd) {
+                                             int nv, float* buf, float (*mean)[VE],
+                                             float (*rstd)[VE]) {
   constexpr int NR = NT / LT;
 #pragma unroll
-  for (int k = 0; k < VE; ++k) mean[k] = 0.f;
+  for (int k = 0; k < VE; ++k) mean[0][k] = 0.f;
   if (LAYER) {
 #pragma unroll
     for (int j = 0; j < KH; ++j)
+      if (rs + j * NR < H)
 #pragma unroll
-      for (int k = 0; k < VE; ++k) mean[k] += (float)a[j][k];
-    strip_sum<NT, LT, VE>(mean, buf);
+        for (int k = 0; k < VE; ++k) mean[0][k] += a[j][k];
+    strip_sum<NT, LT, VE, 1>(mean, buf);
 #pragma unroll
-    for (int k = 0; k < VE; ++k) mean[k] *= inv_h;
+    for (int k = 0; k < VE; ++k) mean[0][k] *= inv_h;
   }
 #pragma unroll
-  for (int k = 0; k < VE; ++k) rstd[k] = 0.f;
+  for (int k = 0; k < VE; ++k) rstd[0][k] = 0.f;
 #pragma unroll
   for (int j = 0; j < KH; ++j)
-    if (rs + j * NR < H)  // channels past H hold 0, which is off the mean
+    if (rs + j * NR < H)
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
-        const float d = (float)a[j][k] - mean[k];
-        rstd[k] = fmaf(d, d, rstd[k]);
+        const float d = a[j][k] - mean[0][k];
+        rstd[0][k] = fmaf(d, d, rstd[0][k]);
       }
-  strip_sum<NT, LT, VE>(rstd, buf);
+  strip_sum<NT, LT, VE, 1>(rstd, buf);
 #pragma unroll
   for (int k = 0; k < VE; ++k)
-    rstd[k] = k < nv ? __builtin_amdgcn_rsqf(fmaf(rstd[k], inv_h, eps)) : 0.f;
+    rstd[0][k] = k < nv ? __builtin_amdgcn_rsqf(fmaf(rstd[0][k], inv_h, eps)) : 0.f;
 }
 
-template <typename T, int VE>
-__device__ __forceinline__ typename VecOf<T, VE>::type load_vec(const T* p, int n) {
-  typename VecOf<T, VE>::type v;
-  if (n >= VE) {
-    v = *reinterpret_cast<const typename VecOf<T, VE>::type*>(p);
-  } else {
+// Where a lane's KH channels lie in a batch row's strip: channel rs + j NR at
+// a distance the workgroup shares (in scalar registers) plus the lane's own in
+// 32 bits, which a load adds by itself.  Lanes past the last channel take the
+// last one's place; they read it again and never count or store it.
+template <typename T, int NR, int KH>
+struct Rows {
+  uint32_t off[KH];
+  int H, L;
+  __device__ __forceinline__ Rows(int rs, int first, int H_, int L_) : H(H_), L(L_) {
 #pragma unroll
-    for (int k = 0; k < VE; ++k) v[k] = k < n ? p[k] : (T)0.f;
+    for (int j = 0; j < KH; ++j)
+      off[j] = ((uint32_t)(min(rs + j * NR, H - 1) - min(j * NR, H - 1)) * (uint32_t)L +
+                (uint32_t)first) * (uint32_t)sizeof(T);
   }
-  return v;
-}
-
-template <typename T, int VE>
-__device__ __forceinline__ void store_vec(T* p, int n, typename VecOf<T, VE>::type v) {
-  if (n >= VE) {
-    *reinterpret_cast<typename VecOf<T, VE>::type*>(p) = v;
-  } else {
+  // strip: the strip's first step in the batch row's first channel
+  __device__ __forceinline__ const T* at(const T* strip, int j) const {
+    const char* row = reinterpret_cast<const char*>(strip + (size_t)min(j * NR, H - 1) * L);
+    return reinterpret_cast<const T*>(row + off[j]);
+  }
+  __device__ __forceinline__ T* at(T* strip, int j) const {
+    return const_cast<T*>(at(const_cast<const T*>(strip), j));
+  }
+  // A whole strip is read without a guard; of one that ends early `nv` of the
+  // lane's steps are live, the others 0.
+  template <int VE>
+  __device__ __forceinline__ void load_row(Packed<T, VE>& v, const T* strip, int j, int nv,
+                                           bool whole) const {
+    if (whole)
+      v.load(at(strip, j));
+    else
+      v.load(at(strip, j), nv, (T)0.f);
+  }
+  template <int VE>
+  __device__ __forceinline__ void load(Packed<T, VE>* v, const T* strip, int nv, bool whole) const {
+    if (whole) {
 #pragma unroll
-    for (int k = 0; k < VE; ++k)
-      if (k < n) p[k] = v[k];
+      for (int j = 0; j < KH; ++j) v[j].load(at(strip, j));
+    } else {
+#pragma unroll
+      for (int j = 0; j < KH; ++j) v[j].load(at(strip, j), nv, (T)0.f);
+    }
   }
+};
+
+template <typename T, int VE, int KH>
+__device__ __forceinline__ void no_rows(Packed<T, VE>* v) {
+#pragma unroll
+  for (int j = 0; j < KH; ++j)
+#pragma unroll
+    for (int k = 0; k < Packed<T, VE>::W; ++k) v[j].w[k] = 0;
 }
 
+// With up to four channels to a lane all of a strip's inputs are asked for
+// before the first sum over channels is formed, so that the sums' barriers wait
+// for memory once; with eight only y has the registers.
 template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
 __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
-  typedef typename VecOf<T, VE>::type Vec;
+  typedef Packed<T, VE> Vec;
   constexpr int NR = NT / LT;
   __shared__ float buf[(NT / 64) * LT * VE];
-  const int b = blockIdx.x / p.ntile;
+  const int strip = strip_of_block(blockIdx.x, p.per);
+  if (strip >= p.B * p.ntile) return;
+  const int b = __builtin_amdgcn_readfirstlane(strip / p.ntile);
   const int lt = threadIdx.x % LT, rs = threadIdx.x / LT;
-  const int t = (blockIdx.x - b * p.ntile) * (LT * VE) + lt * VE;
+  const int t0 = (strip - b * p.ntile) * (LT * VE), t = t0 + lt * VE;
   const int len = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
   const int nv = min(max(len - t, 0), VE), ns = min(max(p.L - t, 0), VE);
+  const bool whole = t0 + LT * VE <= len;
   const float inv_h = 1.f / (float)p.H;
-  const size_t base = (size_t)b * p.H * p.L + t;
-  const T* x = static_cast<const T*>(p.x) + base;
+  const size_t base = (size_t)b * p.H * p.L + t0;
   const size_t plane = (size_t)p.B * p.L;
   const size_t at = (size_t)b * p.L + t;
+  const Rows<T, NR, KH> rows(rs, lt * VE, p.H, p.L);
+  const T* x = static_cast<const T*>(p.x) + base;
   Vec a[KH];
-  float mean[VE], rstd[VE];
+  float mean[1][VE], rstd[1][VE];
   if (p.y) {
-    const T* y = static_cast<const T*>(p.y) + base;
-    const T* g = static_cast<const T*>(p.g) + (p.g ? (size_t)(b * p.sg) + t : 0);
-#pragma unroll
-    for (int j = 0; j < KH; ++j) {
-      const int h = rs + j * NR;
-      a[j] = load_vec<T, VE>(y + (size_t)h * p.L, h < p.H ? nv : 0);
+    Vec xv[KH], gv[KH];
+    const T* g = static_cast<const T*>(p.g) + (p.g ? (size_t)(b * p.sg) + t0 : 0);
+    rows.load(a, static_cast<const T*>(p.y) + base, nv, whole);
+    if (KH <= 4) {
+      if (p.g) rows.load(gv, g, nv, whole);
+      rows.load(xv, x, nv, whole);
     }
-    column_stats<T, LAYER, NT, LT, VE, KH>(a, p.H, rs, inv_h, p.eps, nv, buf, mean, rstd);
+    column_stats<LAYER, NT, LT, VE, KH>(a, p.H, rs, inv_h, p.eps, nv, buf, mean, rstd);
+#pragma unroll
+    for (int j = 0; j < KH; ++j) a[j].refresh();
     if (p.stats && rs == 0) {
-      if (LAYER) store_n<float, VE>(p.stats + at, ns, mean);
-      store_n<float, VE>(p.stats + (LAYER ? plane : 0) + at, ns, rstd);
+      if (LAYER) store_n<float, VE>(p.stats + at, ns, mean[0]);
+      store_n<float, VE>(p.stats + (LAYER ? plane : 0) + at, ns, rstd[0]);
     }
 #pragma unroll
     for (int j = 0; j < KH; ++j) {
       const int h = rs + j * NR;
       const bool in = h < p.H;
-      const Vec xv = load_vec<T, VE>(x + (size_t)h * p.L, in ? nv : 0);
-      float c = in ? p.w_post[h] * p.scale[h] : 0.f;
-      float gv[VE];
-#pragma unroll
-      for (int k = 0; k < VE; ++k) gv[k] = 1.f;
-      if (p.g) {
-        const Vec gr = load_vec<T, VE>(g + (size_t)h * p.L, in ? nv : 0);
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          float rest;
-          gv[k] = (float)gr[k] * sigmoid_pair((float)gr[k], &rest);
-        }
+      const float c = in ? p.w_post[h] * p.scale[h] : 0.f;
+      if (KH > 4) {
+        if (p.g) rows.load_row(gv[j], g, j, nv, whole);
+        rows.load_row(xv[j], x, j, nv, whole);
       }
+      float out[VE];
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
-        const float v = ((float)a[j][k] - mean[k]) * rstd[k];
-        a[j][k] = (T)(k < nv ? fmaf(v * c, gv[k], (float)xv[k]) : 0.f);
+        float silu = 1.f;
+        if (p.g)
+          silu = gv[j][k] * __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gv[j][k]));
+        const float v = (a[j][k] - mean[0][k]) * rstd[0][k];
+        // behind a row's end everything read is 0, and so is the factor
+        out[k] = fmaf(v * c, silu, xv[j][k]);
       }
-      if (in) store_vec<T, VE>(static_cast<T*>(p.o) + base + (size_t)h * p.L, ns, a[j]);
+      a[j].set(out);
+      if (in) a[j].store(rows.at(static_cast<T*>(p.o) + base, j), ns);
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < KH; ++j) {
-      const int h = rs + j * NR;
-      a[j] = load_vec<T, VE>(x + (size_t)h * p.L, h < p.H ? nv : 0);
-    }
+    rows.load(a, x, nv, whole);
   }
   if (!p.n) return;
   // the norm before the next block is of the stream as it is stored
-  column_stats<T, LAYER, NT, LT, VE, KH>(a, p.H, rs, inv_h, p.eps, nv, buf, mean, rstd);
+  column_stats<LAYER, NT, LT, VE, KH>(a, p.H, rs, inv_h, p.eps, nv, buf, mean, rstd);
   if (p.stats && rs == 0) {
-    if (LAYER) store_n<float, VE>(p.stats + 2 * plane + at, ns, mean);
-    store_n<float, VE>(p.stats + (LAYER ? 3 : 1) * plane + at, ns, rstd);
+    if (LAYER) store_n<float, VE>(p.stats + 2 * plane + at, ns, mean[0]);
+    store_n<float, VE>(p.stats + (LAYER ? 3 : 1) * plane + at, ns, rstd[0]);
   }
 #pragma unroll
   for (int j = 0; j < KH; ++j) {
     const int h = rs + j * NR;
     if (h >= p.H) continue;
     const float w = p.w_pre[h];
-    Vec out;
+    float out[VE];
 #pragma unroll
-    for (int k = 0; k < VE; ++k)
-      out[k] = (T)(k < nv ? ((float)a[j][k] - mean[k]) * rstd[k] * w : 0.f);
-    store_vec<T, VE>(static_cast<T*>(p.n) + base + (size_t)h * p.L, ns, out);
+    for (int k = 0; k < VE; ++k) out[k] = (a[j][k] - mean[0][k]) * rstd[0][k] * w;
+    store_n<T, VE>(rows.at(static_cast<T*>(p.n) + base, j), ns, out);
   }
 }
 
-// Strips w, w + gridDim.x, ... of one workgroup.  Its sums over b, t stay in
-// LDS until the end: a channel is always the same LT lanes'.
-template <typename T, bool LAYER, int NT, int LT, int VE>
+// Strips of one workgroup, one after another.  All five inputs of a strip are
+// held in registers, so memory is read once; the sums over b, t stay in the
+// registers of the channel's lanes until the end.  With oh = o ro - mo ro and
+// so on, the factors that a column shares are formed once per strip.
+template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
 __global__ __launch_bounds__(NT) void resnorm_bwd_kernel(Args p) {
-  constexpr int NR = NT / LT;
-  __shared__ float buf[(NT / 64) * LT * VE];
-  __shared__ float sums[3 * kResnormMaxH / LT];  // [3][H]
+  typedef Packed<T, VE> Vec;
+  constexpr int NR = NT / LT, N = LAYER ? 2 : 1;
+  __shared__ float buf[(NT / 64) * N * LT * VE];
   const int lt = threadIdx.x % LT, rs = threadIdx.x / LT;
   const int H = p.H;
   const float inv_h = 1.f / (float)H;
   const size_t plane = (size_t)p.B * p.L;
-  for (int h = rs; h < H; h += NR)
-    if (lt == 0) sums[h] = sums[H + h] = sums[2 * H + h] = 0.f;
+  const Rows<T, NR, KH> rows(rs, lt * VE, H, p.L);
+  float a_v[KH], a_n[KH];  // sums of t yh silu(g) and of dn oh
+#pragma unroll
+  for (int j = 0; j < KH; ++j) a_v[j] = a_n[j] = 0.f;
   const int total = p.B * p.ntile;
-  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const int b = tile / p.ntile;
-    const int t = (tile - b * p.ntile) * (LT * VE) + lt * VE;
+  for (int block = blockIdx.x; block < 8 * p.per; block += gridDim.x) {
+    const int strip = strip_of_block(block, p.per);
+    if (strip >= total) continue;
+    const int b = __builtin_amdgcn_readfirstlane(strip / p.ntile);
+    const int t0 = (strip - b * p.ntile) * (LT * VE), t = t0 + lt * VE;
     const int len = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
     const int nv = min(max(len - t, 0), VE), ns = min(max(p.L - t, 0), VE);
-    const size_t base = (size_t)b * H * p.L + t;
+    const bool whole = t0 + LT * VE <= len;
+    const size_t base = (size_t)b * H * p.L + t0;
     const size_t at = (size_t)b * p.L + t;
-    const T* o = static_cast<const T*>(p.x) + base;
-    const T* dn = p.d_n ? static_cast<const T*>(p.d_n) + base : nullptr;
-    const T* dout = p.d_o ? static_cast<const T*>(p.d_o) + base : nullptr;
-    float mo[VE], ro[VE], s1[VE], s0[VE];
-#pragma unroll
-    for (int k = 0; k < VE; ++k) mo[k] = ro[k] = s1[k] = s0[k] = 0.f;
-    if (dn) {
-      if (LAYER) load_n<float, VE>(p.stats + 2 * plane + at, nv, mo);
-      load_n<float, VE>(p.stats + (LAYER ? 3 : 1) * plane + at, nv, ro);
-      for (int h = rs; h < H; h += NR) {
-        const float w = p.w_pre[h];
-        float ov[VE], dv[VE], sum = 0.f;
-        load_n<T, VE>(o + (size_t)h * p.L, nv, ov);
-        load_n<T, VE>(dn + (size_t)h * p.L, nv, dv);
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          const float oh = (ov[k] - mo[k]) * ro[k];
-          const float P = dv[k] * w;
-          s1[k] = fmaf(P, oh, s1[k]);
-          if (LAYER) s0[k] += P;
-          sum = fmaf(dv[k], oh, sum);  // past the end dv is 0
-        }
-        sum = lanes_sum<LT>(sum);
-        if (lt == 0) sums[2 * H + h] += sum;
-      }
-      strip_sum<NT, LT, VE>(s1, buf);
-      if (LAYER) strip_sum<NT, LT, VE>(s0, buf);
-#pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        s1[k] *= inv_h;
-        s0[k] *= inv_h;
-      }
-    }
-    // t of one channel's steps
-    auto stream = [&](int h, float* tv) {
-#pragma unroll
-      for (int k = 0; k < VE; ++k) tv[k] = 0.f;
-      if (dout) load_n<T, VE>(dout + (size_t)h * p.L, nv, tv);
-      if (dn) {
-        const float w = p.w_pre[h];
-        float ov[VE], dv[VE];
-        load_n<T, VE>(o + (size_t)h * p.L, nv, ov);
-        load_n<T, VE>(dn + (size_t)h * p.L, nv, dv);
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-          const float oh = (ov[k] - mo[k]) * ro[k];
-          float q = fmaf(dv[k], w, -oh * s1[k]);
-          if (LAYER) q -= s0[k];
-          tv[k] = fmaf(ro[k], q, tv[k]);
-        }
-      }
+    Vec ov[KH], nn[KH], dv[KH], yv[KH], gv[KH];
+    const auto load = [&](Vec* v, const void* q, size_t off) {
+      if (q)
+        rows.load(v, static_cast<const T*>(q) + off, nv, whole);
+      else
+        no_rows<T, VE, KH>(v);
     };
-    if (!p.y) {
-      for (int h = rs; h < H; h += NR) {
-        float tv[VE];
-        stream(h, tv);
-        store_n<T, VE>(static_cast<T*>(p.dx) + base + (size_t)h * p.L, ns, tv);
-      }
-      continue;
-    }
-    const T* y = static_cast<const T*>(p.y) + base;
-    const T* g = static_cast<const T*>(p.g) + (p.g ? (size_t)(b * p.sg) + t : 0);
-    float my[VE], ry[VE], r1[VE], r0[VE];
+    load(ov, p.d_n ? p.x : nullptr, base);
+    load(nn, p.d_n, base);
+    // factor and (layer norm) -mean factor of o and of y; past the end 0
+    float ro[VE], mo[VE], ry[VE], my[VE];
+    load_n<float, VE>(p.stats + (LAYER ? 3 : 1) * plane + at, p.d_n ? nv : 0, ro);
+    load_n<float, VE>(p.stats + 2 * plane + at, LAYER && p.d_n ? nv : 0, mo);
+    load(dv, p.d_o, base);
+    load(yv, p.y, base);
+    load(gv, p.g, (size_t)(b * p.sg) + t0);
+    load_n<float, VE>(p.stats + (LAYER ? plane : 0) + at, p.y ? nv : 0, ry);
+    load_n<float, VE>(p.stats + at, LAYER && p.y ? nv : 0, my);
+    float s[N][VE];
 #pragma unroll
-    for (int k = 0; k < VE; ++k) my[k] = r1[k] = r0[k] = 0.f;
-    if (LAYER) load_n<float, VE>(p.stats + at, nv, my);
-    load_n<float, VE>(p.stats + (LAYER ? plane : 0) + at, nv, ry);
-    for (int h = rs; h < H; h += NR) {
-      const float wp = p.w_post[h], sc = p.scale[h];
-      float tv[VE], yv[VE], gv[VE], dgv[VE];
-      stream(h, tv);
-      load_n<T, VE>(y + (size_t)h * p.L, nv, yv);
-      if (p.g) load_n<T, VE>(g + (size_t)h * p.L, nv, gv);
-      float sv = 0.f;
+    for (int m = 0; m < N; ++m)
 #pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        float rest, silu = 1.f, dsilu = 0.f;
-        if (p.g) {
-          const float s = sigmoid_pair(gv[k], &rest);
-          silu = gv[k] * s;
-          dsilu = s * fmaf(gv[k], rest, 1.f);
+      for (int k = 0; k < VE; ++k) s[m][k] = 0.f;
+    if (p.d_n) {
+#pragma unroll
+      for (int k = 0; k < VE; ++k) mo[k] *= -ro[k];
+#pragma unroll
+      for (int j = 0; j < KH; ++j) {
+        const int h = rs + j * NR;
+        const float w = h < H ? p.w_pre[h] : 0.f;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          const float oh = LAYER ? fmaf(ov[j][k], ro[k], mo[k]) : ov[j][k] * ro[k];
+          const float m = nn[j][k] * oh;
+          a_n[j] += m;
+          s[0][k] = fmaf(w, m, s[0][k]);
+          if (LAYER) s[N - 1][k] = fmaf(w, nn[j][k], s[N - 1][k]);
         }
-        const float yh = (yv[k] - my[k]) * ry[k];  // past the end the factor is 0
-        const float ty = tv[k] * yh;
-        sv = fmaf(ty, silu, sv);
-        dgv[k] = ty * (wp * sc) * dsilu;
-        const float R = tv[k] * (sc * wp) * silu;
-        r1[k] = fmaf(R, yh, r1[k]);
-        if (LAYER) r0[k] += R;
       }
-      store_n<T, VE>(static_cast<T*>(p.dx) + base + (size_t)h * p.L, ns, tv);
-      if (p.dg)
-        store_n<T, VE>(static_cast<T*>(p.dg) + (size_t)(b * p.sdg) + t + (size_t)h * p.L, ns, dgv);
-      sv = lanes_sum<LT>(sv);
-      if (lt == 0) {
-        sums[h] = fmaf(sv, sc, sums[h]);
-        sums[H + h] = fmaf(sv, wp, sums[H + h]);
-      }
+      strip_sum<NT, LT, VE, N>(s, buf);
     }
-    strip_sum<NT, LT, VE>(r1, buf);
-    if (LAYER) strip_sum<NT, LT, VE>(r0, buf);
-    for (int h = rs; h < H; h += NR) {
-      const float c = p.w_post[h] * p.scale[h];
-      float tv[VE], yv[VE], gv[VE], out[VE];
-      stream(h, tv);
-      load_n<T, VE>(y + (size_t)h * p.L, nv, yv);
-      if (p.g) load_n<T, VE>(g + (size_t)h * p.L, nv, gv);
+    // t = do + ro w dn - c1 oh - c0
+    float c1[VE], c0[VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      c1[k] = -ro[k] * s[0][k] * inv_h;
+      c0[k] = -ro[k] * s[N - 1][k] * inv_h;
+      if (LAYER) my[k] *= -ry[k];
+    }
+#pragma unroll
+    for (int j = 0; j < KH; ++j) {
+      ov[j].refresh();
+      nn[j].refresh();
+    }
+    float R[KH][VE], r[N][VE];
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int k = 0; k < VE; ++k) r[m][k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KH; ++j) {
+      const int h = rs + j * NR;
+      const bool in = h < H;
+      const float w = in && p.d_n ? p.w_pre[h] : 0.f;
+      float tv[VE];
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
-        float rest;
-        const float silu = p.g ? gv[k] * sigmoid_pair(gv[k], &rest) : 1.f;
-        const float yh = (yv[k] - my[k]) * ry[k];
-        float q = fmaf(tv[k] * c, silu, -yh * (r1[k] * inv_h));
-        if (LAYER) q -= r0[k] * inv_h;
-        out[k] = ry[k] * q;
+        const float oh = LAYER ? fmaf(ov[j][k], ro[k], mo[k]) : ov[j][k] * ro[k];
+        tv[k] = fmaf(nn[j][k], w * ro[k], dv[j][k]);
+        tv[k] = fmaf(c1[k], oh, tv[k]);
+        if (LAYER) tv[k] += c0[k];
       }
-      store_n<T, VE>(static_cast<T*>(p.dy) + base + (size_t)h * p.L, ns, out);
+      if (in) store_n<T, VE>(rows.at(static_cast<T*>(p.dx) + base, j), ns, tv);
+      if (!p.y) continue;
+      const float c = in ? p.w_post[h] * p.scale[h] : 0.f;
+      float dgv[VE];
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        float silu = 1.f, dsilu = 0.f;
+        if (p.g) {
+          const float gk = gv[j][k];
+          const float sg = __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gk));
+          silu = gk * sg;
+          dsilu = fmaf(-silu, sg, silu + sg);  // sg (1 + g (1 - sg))
+        }
+        const float yh = LAYER ? fmaf(yv[j][k], ry[k], my[k]) : yv[j][k] * ry[k];
+        const float ty = tv[k] * yh;
+        const float v = ty * silu;
+        a_v[j] += v;
+        r[0][k] = fmaf(c, v, r[0][k]);
+        R[j][k] = tv[k] * silu * c;
+        if (LAYER) r[N - 1][k] += R[j][k];
+        dgv[k] = ty * dsilu * c;
+      }
+      if (in && p.dg)
+        store_n<T, VE>(rows.at(static_cast<T*>(p.dg) + (size_t)(b * p.sdg) + t0, j), ns, dgv);
+    }
+    if (!p.y) continue;
+#pragma unroll
+    for (int j = 0; j < KH; ++j) yv[j].refresh();
+    strip_sum<NT, LT, VE, N>(r, buf);
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      c1[k] = -ry[k] * r[0][k] * inv_h;
+      c0[k] = -ry[k] * r[N - 1][k] * inv_h;
+    }
+#pragma unroll
+    for (int j = 0; j < KH; ++j) {
+      const int h = rs + j * NR;
+      if (h >= H) continue;
+      float out[VE];
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        const float yh = LAYER ? fmaf(yv[j][k], ry[k], my[k]) : yv[j][k] * ry[k];
+        out[k] = fmaf(c1[k], yh, R[j][k] * ry[k]);
+        if (LAYER) out[k] += c0[k];
+      }
+      store_n<T, VE>(rows.at(static_cast<T*>(p.dy) + base, j), ns, out);
     }
   }
-  float* part = p.part + (size_t)blockIdx.x * 3 * H;
-  for (int h = rs; h < H; h += NR)
-    if (lt == 0) {
-      part[h] = sums[h];
-      part[H + h] = sums[H + h];
-      part[2 * H + h] = sums[2 * H + h];
+  float* part = p.part + (size_t)blockIdx.x * 2 * H;
+#pragma unroll
+  for (int j = 0; j < KH; ++j) {
+    const int h = rs + j * NR;
+    const float v = lanes_sum<LT>(a_v[j]), n = lanes_sum<LT>(a_n[j]);
+    if (lt == 0 && h < H) {
+      part[h] = v;
+      part[H + h] = n;
     }
+  }
 }
 
-// The workgroups' sums, in order and in float64: 16 channels by 16 slices of
-// the workgroups to a block.
-__global__ __launch_bounds__(256) void resnorm_sum_kernel(const float* __restrict__ part, int G,
-                                                          int n, int H, float* dw_post,
-                                                          float* dscale, float* dw_pre) {
-  __shared__ double s[16][17];
+// The workgroups' sums, in order and in float64: 16 channels by 64 slices of
+// the workgroups to a block.  With V = sum t yh silu(g): dw_post = scale V,
+// dscale = w_post V.
+__global__ __launch_bounds__(1024) void resnorm_sum_kernel(const float* __restrict__ part, int G,
+                                                           int H, const float* w_post,
+                                                           const float* scale, float* dw_post,
+                                                           float* dscale, float* dw_pre) {
+  __shared__ double s[64][17];
   const int c = threadIdx.x & 15, z = threadIdx.x >> 4;
   const int k = blockIdx.x * 16 + c;
   double v = 0.0;
-  if (k < n)
-    for (int w = z; w < G; w += 16) v += (double)part[(size_t)w * n + k];
+  if (k < 2 * H) {
+#pragma unroll 4
+    for (int w = z; w < G; w += 64) v += (double)part[(size_t)w * 2 * H + k];
+  }
   s[z][c] = v;
   __syncthreads();
-  if (z == 0 && k < n) {
-    double t = 0.0;
+  if (threadIdx.x < 256) {  // 16 slices' sums at a time, then these
+    v = 0.0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) t += s[j][c];
-    float* out = k < H ? dw_post : k < 2 * H ? dscale : dw_pre;
-    if (out) out[k % H] = (float)t;
+    for (int j = 0; j < 4; ++j) v += s[z * 4 + j][c];
+  }
+  __syncthreads();
+  if (threadIdx.x < 256) s[z][c] = v;
+  __syncthreads();
+  if (z == 0 && k < 2 * H) {
+    v = 0.0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v += s[j][c];
+    if (k >= H) {
+      if (dw_pre) dw_pre[k - H] = (float)v;
+    } else {
+      if (dw_post) dw_post[k] = (float)(G ? v * (double)scale[k] : 0.0);
+      if (dscale) dscale[k] = (float)(G ? v * (double)w_post[k] : 0.0);
+    }
   }
 }
 
 constexpr int kMaxGroups = 512;  // workgroups of the backward pass
 
-// Steps to a lane, lanes to a row segment: 128 bytes of each row at a time
-// while the forward pass holds the strip's H channels in registers, shorter
-// segments for more channels; a single step takes its channels side by side.
-struct Strip {
-  int lt, ve;
+// Threads, lanes to a row segment, bytes of a lane's steps and channels to a
+// lane.  A strip's inputs stay in registers, so more channels mean shorter
+// segments of each row, which memory serves less well (forward, bf16, 2^25
+// elements: 76-86 us with 128 bytes up to 512 channels, 97 with 64 and 119
+// with 32; backward 136-145 with 256 or 128 bytes, 170 with 64).
+struct Form {
+  int nt, lt, kh;
 };
 
-Strip strip_of(int H, int L, int dtype) {
-  if (L == 1) return {1, 1};
-  const int ve = dtype == 0 ? 4 : 8;
-  return {H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1, ve};
+Form fwd_form(int H, int L) {
+  if (L == 1) return H <= 1024 ? Form{256, 1, 4} : Form{1024, 1, 8};
+  if (H <= 512) return {H <= 128 ? 256 : H <= 256 ? 512 : 1024, 8, 4};
+  return {1024, H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1, 8};
 }
 
-int strips(const Strip& s, int L) { return (L + s.lt * s.ve - 1) / (s.lt * s.ve); }
+Form bwd_form(int H, int L) {
+  if (L == 1) return H <= 1024 ? Form{256, 1, 4} : Form{1024, 1, 8};
+  if (H <= 2048) return {512, H <= 128 ? 16 : H <= 256 ? 8 : H <= 512 ? 4 : H <= 1024 ? 2 : 1, 4};
+  return {1024, 1, H <= 4096 ? 4 : 8};
+}
+
+// Steps of a strip.
+int strip_steps(const Form& f, int L, int dtype) { return f.lt * (L == 1 ? 1 : dtype == 0 ? 4 : 8); }
+
+int strips(const Form& f, int L, int dtype) {
+  const int n = strip_steps(f, L, dtype);
+  return (L + n - 1) / n;
+}
 
 int groups_of(int B, int H, int L, int dtype) {
-  return (int)std::min<long>((long)B * strips(strip_of(H, L, dtype), L), kMaxGroups);
+  const long n = (long)B * strips(bwd_form(H, L), L, dtype);
+  return (int)std::min<long>((n + 7) / 8 * 8, kMaxGroups);
 }
 
 template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
 void fwd_start(const Args& a, hipStream_t st) {
-  hipLaunchKernelGGL((resnorm_fwd_kernel<T, LAYER, NT, LT, VE, KH>),
-                     dim3((unsigned)(a.B * a.ntile)), dim3(NT), 0, st, a);
+  hipLaunchKernelGGL((resnorm_fwd_kernel<T, LAYER, NT, LT, VE, KH>), dim3(8u * a.per), dim3(NT), 0,
+                     st, a);
 }
 
-template <typename T, bool LAYER, int LT, int VE>
+template <typename T, bool LAYER>
+void fwd_run(const Args& a, const Form& f, hipStream_t st) {
+  constexpr int VE = 16 / sizeof(T);
+  if (a.L == 1)
+    f.nt == 256 ? fwd_start<T, LAYER, 256, 1, 1, 4>(a, st)
+                : fwd_start<T, LAYER, 1024, 1, 1, 8>(a, st);
+  else if (f.kh == 4)
+    f.nt == 256   ? fwd_start<T, LAYER, 256, 8, VE, 4>(a, st)
+    : f.nt == 512 ? fwd_start<T, LAYER, 512, 8, VE, 4>(a, st)
+                  : fwd_start<T, LAYER, 1024, 8, VE, 4>(a, st);
+  else
+    f.lt == 8   ? fwd_start<T, LAYER, 1024, 8, VE, 8>(a, st)
+    : f.lt == 4 ? fwd_start<T, LAYER, 1024, 4, VE, 8>(a, st)
+    : f.lt == 2 ? fwd_start<T, LAYER, 1024, 2, VE, 8>(a, st)
+                : fwd_start<T, LAYER, 1024, 1, VE, 8>(a, st);
+}
+
+template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
 void bwd_start(const Args& a, int groups, hipStream_t st) {
-  hipLaunchKernelGGL((resnorm_bwd_kernel<T, LAYER, 512, LT, VE>), dim3((unsigned)groups),
-                     dim3(512), 0, st, a);
+  hipLaunchKernelGGL((resnorm_bwd_kernel<T, LAYER, NT, LT, VE, KH>), dim3((unsigned)groups),
+                     dim3(NT), 0, st, a);
+}
+
+template <typename T, bool LAYER>
+void bwd_run(const Args& a, const Form& f, int groups, hipStream_t st) {
+  constexpr int VE = 16 / sizeof(T);
+  if (a.L == 1)
+    f.nt == 256 ? bwd_start<T, LAYER, 256, 1, 1, 4>(a, groups, st)
+                : bwd_start<T, LAYER, 1024, 1, 1, 8>(a, groups, st);
+  else if (f.nt == 512)
+    f.lt == 16  ? bwd_start<T, LAYER, 512, 16, VE, 4>(a, groups, st)
+    : f.lt == 8 ? bwd_start<T, LAYER, 512, 8, VE, 4>(a, groups, st)
+    : f.lt == 4 ? bwd_start<T, LAYER, 512, 4, VE, 4>(a, groups, st)
+    : f.lt == 2 ? bwd_start<T, LAYER, 512, 2, VE, 4>(a, groups, st)
+                : bwd_start<T, LAYER, 512, 1, VE, 4>(a, groups, st);
+  else
+    f.kh == 4 ? bwd_start<T, LAYER, 1024, 1, VE, 4>(a, groups, st)
+              : bwd_start<T, LAYER, 1024, 1, VE, 8>(a, groups, st);
 }
 
 template <typename T, bool LAYER>
 hipError_t run(const ResnormCall& c, int dtype, bool backward, hipStream_t st) {
-  constexpr int VE = 16 / sizeof(T);
-  const Strip s = strip_of(c.H, c.L, dtype);
+  const Form f = backward ? bwd_form(c.H, c.L) : fwd_form(c.H, c.L);
   Args a{};
   a.x = c.x;
   a.y = c.y;
@@ -428,7 +594,8 @@ hipError_t run(const ResnormCall& c, int dtype, bool backward, hipStream_t st) {
   a.B = c.B;
   a.H = c.H;
   a.L = c.L;
-  a.ntile = strips(s, c.L);
+  a.ntile = strips(f, c.L, dtype);
+  a.per = (c.B * a.ntile + 7) / 8;
   a.eps = c.eps;
   a.o = c.o;
   a.n = c.n;
@@ -441,30 +608,15 @@ hipError_t run(const ResnormCall& c, int dtype, bool backward, hipStream_t st) {
   a.sdg = c.stride_dg;
   a.part = static_cast<float*>(c.ws);
   if (!backward) {
-    if (s.ve == 1)
-      c.H <= 2048 ? fwd_start<T, LAYER, 256, 1, 1, 8>(a, st)
-                  : fwd_start<T, LAYER, 1024, 1, 1, 8>(a, st);
-    else if (s.lt == 8)
-      c.H <= 128   ? fwd_start<T, LAYER, 256, 8, VE, 4>(a, st)
-      : c.H <= 512 ? fwd_start<T, LAYER, 512, 8, VE, 8>(a, st)
-                   : fwd_start<T, LAYER, 1024, 8, VE, 8>(a, st);
-    else
-      s.lt == 4   ? fwd_start<T, LAYER, 1024, 4, VE, 8>(a, st)
-      : s.lt == 2 ? fwd_start<T, LAYER, 1024, 2, VE, 8>(a, st)
-                  : fwd_start<T, LAYER, 1024, 1, VE, 8>(a, st);
+    fwd_run<T, LAYER>(a, f, st);
     return hipGetLastError();
   }
   const int groups = groups_of(c.B, c.H, c.L, dtype);
-  if (s.ve == 1) bwd_start<T, LAYER, 1, 1>(a, groups, st);
-  else if (s.lt == 8) bwd_start<T, LAYER, 8, VE>(a, groups, st);
-  else if (s.lt == 4) bwd_start<T, LAYER, 4, VE>(a, groups, st);
-  else if (s.lt == 2) bwd_start<T, LAYER, 2, VE>(a, groups, st);
-  else bwd_start<T, LAYER, 1, VE>(a, groups, st);
+  bwd_run<T, LAYER>(a, f, groups, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int n = 3 * c.H;
-  hipLaunchKernelGGL(resnorm_sum_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, st, a.part,
-                     groups, n, c.H, c.dw_post, c.dscale, c.dw_pre);
+  hipLaunchKernelGGL(resnorm_sum_kernel, dim3((unsigned)((2 * c.H + 15) / 16)), dim3(1024), 0, st,
+                     a.part, groups, c.H, c.w_post, c.scale, c.dw_post, c.dscale, c.dw_pre);
   return hipGetLastError();
 }
 
@@ -484,7 +636,7 @@ hipError_t run_type(const ResnormCall& c, int dtype, bool backward, hipStream_t 
 }  // namespace
 
 size_t resnorm_workspace(int B, int H, int L, int dtype) {
-  return align_up((size_t)groups_of(B, H, L, dtype) * 3 * H * sizeof(float), 256);
+  return align_up((size_t)groups_of(B, H, L, dtype) * 2 * H * sizeof(float), 256);
 }
 
 hipError_t launch_resnorm_forward(const ResnormCall& c, int dtype, hipStream_t st) {
@@ -494,10 +646,9 @@ hipError_t launch_resnorm_forward(const ResnormCall& c, int dtype, hipStream_t s
 // B = 0 or L = 0: no strips, so the sums are zero.
 hipError_t launch_resnorm_backward(const ResnormCall& c, int dtype, hipStream_t st) {
   if (c.B == 0 || c.L == 0) {
-    const int n = 3 * c.H;
-    hipLaunchKernelGGL(resnorm_sum_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, st,
-                       static_cast<const float*>(nullptr), 0, n, c.H, c.dw_post, c.dscale,
-                       c.dw_pre);
+    hipLaunchKernelGGL(resnorm_sum_kernel, dim3((unsigned)((2 * c.H + 15) / 16)), dim3(1024), 0, st,
+                       static_cast<const float*>(nullptr), 0, c.H, c.w_post, c.scale, c.dw_post,
+                       c.dscale, c.dw_pre);
     return hipGetLastError();
   }
   return run_type(c, dtype, true, st);

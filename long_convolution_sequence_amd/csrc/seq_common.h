@@ -51,6 +51,99 @@ __device__ __forceinline__ void store_n(T* p, int n, const float* in) {
   }
 }
 
+// N consecutive elements as they lie in memory, in 32-bit words.  Words and not
+// elements: where a guarded load meets a whole one, elements would each take a
+// register of their own.
+template <typename T, int N>
+struct Packed {
+  static constexpr int W = (N * (int)sizeof(T) + 3) / 4;
+  uint32_t w[W];
+
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N * sizeof(T) >= 4) {
+      const typename VecOf<T, N>::type v = *reinterpret_cast<const typename VecOf<T, N>::type*>(p);
+      __builtin_memcpy(w, &v, sizeof(w));
+    } else {
+      w[0] = bits(p[0]);
+    }
+  }
+  // elements at or past `n` are not read and are `fill`
+  __device__ __forceinline__ void load(const T* p, int n, T fill) {
+    if (n >= N) {
+      load(p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] = 0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) put(k, bits(k < n ? p[k] : fill));
+    }
+  }
+  __device__ __forceinline__ float operator[](int k) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[k]);
+    } else {
+      const uint16_t h = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+      return (float)__builtin_bit_cast(T, h);
+    }
+  }
+  // rounded to nearest even once
+  __device__ __forceinline__ void set(const float* x) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) w[k] = __float_as_uint(x[k]);
+    } else if constexpr (N == 1) {
+      w[0] = bits((T)x[0]);
+    } else {
+      typedef T two __attribute__((ext_vector_type(2)));
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) {
+        const two v = {(T)x[2 * k], (T)x[2 * k + 1]};
+        w[k] = __builtin_bit_cast(uint32_t, v);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int n) const {
+    if (n >= N) {
+      typename VecOf<T, N>::type v;
+      if constexpr (N * sizeof(T) >= 4) {
+        __builtin_memcpy(&v, w, sizeof(w));
+        *reinterpret_cast<typename VecOf<T, N>::type*>(p) = v;
+      } else {
+        p[0] = __builtin_bit_cast(T, (uint16_t)w[0]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < n) {
+          if constexpr (sizeof(T) == 4)
+            p[k] = __builtin_bit_cast(T, w[k]);
+          else
+            p[k] = __builtin_bit_cast(T, (uint16_t)(w[k / 2] >> (16 * (k & 1))));
+        }
+    }
+  }
+  // The compiler forgets what it derived from the words before (their values in
+  // float32, twice the registers) and derives it again.
+  __device__ __forceinline__ void refresh() {
+#pragma unroll
+    for (int k = 0; k < W; ++k) asm volatile("" : "+v"(w[k]));
+  }
+
+ private:
+  static __device__ __forceinline__ uint32_t bits(T x) {
+    if constexpr (sizeof(T) == 4)
+      return __builtin_bit_cast(uint32_t, x);
+    else
+      return __builtin_bit_cast(uint16_t, x);
+  }
+  __device__ __forceinline__ void put(int k, uint32_t b) {
+    if constexpr (sizeof(T) == 4)
+      w[k] = b;
+    else
+      w[k / 2] |= b << (16 * (k & 1));
+  }
+};
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 constexpr float kLog2e = 1.44269504088896340736f;
