@@ -189,14 +189,6 @@ struct Rows {
   // A whole strip is read without a guard; of one that ends early `nv` of the
   // lane's steps are live, the others 0.
   template <int VE>
-  __device__ __forceinline__ void load_row(Packed<T, VE>& v, const T* strip, int j, int nv,
-                                           bool whole) const {
-    if (whole)
-      v.load(at(strip, j));
-    else
-      v.load(at(strip, j), nv, (T)0.f);
-  }
-  template <int VE>
   __device__ __forceinline__ void load(Packed<T, VE>* v, const T* strip, int nv, bool whole) const {
     if (whole) {
 #pragma unroll
@@ -216,9 +208,8 @@ __device__ __forceinline__ void no_rows(Packed<T, VE>* v) {
     for (int k = 0; k < Packed<T, VE>::W; ++k) v[j].w[k] = 0;
 }
 
-// With up to four channels to a lane all of a strip's inputs are asked for
-// before the first sum over channels is formed, so that the sums' barriers wait
-// for memory once; with eight only y has the registers.
+// The whole strip in registers: all inputs are asked for before the first sum
+// over channels is formed, so that the sums' barriers wait for memory once.
 template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
 __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
   typedef Packed<T, VE> Vec;
@@ -244,10 +235,8 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
     Vec xv[KH], gv[KH];
     const T* g = static_cast<const T*>(p.g) + (p.g ? (size_t)(b * p.sg) + t0 : 0);
     rows.load(a, static_cast<const T*>(p.y) + base, nv, whole);
-    if (KH <= 4) {
-      if (p.g) rows.load(gv, g, nv, whole);
-      rows.load(xv, x, nv, whole);
-    }
+    if (p.g) rows.load(gv, g, nv, whole);
+    rows.load(xv, x, nv, whole);
     column_stats<LAYER, NT, LT, VE, KH>(a, p.H, rs, inv_h, p.eps, nv, buf, mean, rstd);
 #pragma unroll
     for (int j = 0; j < KH; ++j) a[j].refresh();
@@ -260,10 +249,6 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
       const int h = rs + j * NR;
       const bool in = h < p.H;
       const float c = in ? p.w_post[h] * p.scale[h] : 0.f;
-      if (KH > 4) {
-        if (p.g) rows.load_row(gv[j], g, j, nv, whole);
-        rows.load_row(xv[j], x, j, nv, whole);
-      }
       float out[VE];
 #pragma unroll
       for (int k = 0; k < VE; ++k) {
@@ -296,6 +281,193 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
 #pragma unroll
     for (int k = 0; k < VE; ++k) out[k] = (a[j][k] - mean[0][k]) * rstd[0][k] * w;
     store_n<T, VE>(rows.at(static_cast<T*>(p.n) + base, j), ns, out);
+  }
+}
+
+// One strip of a workgroup that loops over its channels.
+template <typename T, int NT, int LT, int VE>
+struct WideStrip {
+  typedef Packed<T, VE> Vec;
+  static constexpr int NR = NT / LT;
+  int b, t0, t, nv, ns, H, L, lt, rs;
+  bool whole;
+  size_t base, at, plane;
+  __device__ __forceinline__ WideStrip(const Args& p, int strip) {
+    b = __builtin_amdgcn_readfirstlane(strip / p.ntile);
+    lt = threadIdx.x % LT;
+    rs = threadIdx.x / LT;
+    t0 = (strip - b * p.ntile) * (LT * VE);
+    t = t0 + lt * VE;
+    H = p.H;
+    L = p.L;
+    const int len = p.lens ? min(max(p.lens[b], 0), L) : L;
+    nv = min(max(len - t, 0), VE);
+    ns = min(max(L - t, 0), VE);
+    whole = t0 + LT * VE <= len;
+    base = (size_t)b * H * L + t0;
+    plane = (size_t)p.B * L;
+    at = (size_t)b * L + t;
+  }
+  // the lane's steps of channel rs + j NR (past the end, the last one's place)
+  __device__ __forceinline__ const T* spot(const T* strip, int j) const {
+    const int first = min(j * NR, H - 1);
+    const uint32_t off = ((uint32_t)(min(rs + j * NR, H - 1) - first) * (uint32_t)L +
+                          (uint32_t)(lt * VE)) * (uint32_t)sizeof(T);
+    return reinterpret_cast<const T*>(reinterpret_cast<const char*>(strip + (size_t)first * L) +
+                                      off);
+  }
+  __device__ __forceinline__ T* spot(T* strip, int j) const {
+    return const_cast<T*>(spot(const_cast<const T*>(strip), j));
+  }
+  __device__ __forceinline__ void get(Vec& v, const T* strip, int j) const {
+    if (whole)
+      v.load(spot(strip, j));
+    else
+      v.load(spot(strip, j), nv, (T)0.f);
+  }
+  // nothing where there is no such tensor
+  __device__ __forceinline__ void get_any(Vec& v, const T* strip, int j) const {
+    if (strip)
+      get(v, strip, j);
+    else
+#pragma unroll
+      for (int k = 0; k < Vec::W; ++k) v.w[k] = 0;
+  }
+};
+
+// The forward pass for more channels than the registers hold: y is read once
+// for its sums and, still in a cache, again; o is read back for its own.  Loops
+// over the channels, U of them in flight; a few registers per lane, so that
+// a compute unit holds more waves, and longer segments of each row (bf16, 2^25
+// elements, 1024 channels: 81 us against 87 with the strip in registers; 2048
+// channels: 90 against 106).
+template <typename T, bool LAYER, int NT, int LT, int VE, int U>
+__global__ __launch_bounds__(NT) void resnorm_fwd_wide_kernel(Args p) {
+  typedef Packed<T, VE> Vec;
+  constexpr int NR = NT / LT;
+  __shared__ float buf[(NT / 64) * LT * VE];
+  const int strip = strip_of_block(blockIdx.x, p.per);
+  if (strip >= p.B * p.ntile) return;
+  const WideStrip<T, NT, LT, VE> at(p, strip);
+  const int rs = at.rs, H = at.H, nv = at.nv, ns = at.ns;
+  const float inv_h = 1.f / (float)H;
+  const int nj = (H + NR - 1) / NR;
+  const T* x = static_cast<const T*>(p.x) + at.base;
+  T* o = static_cast<T*>(p.o) + at.base;
+  // A lane's channels one by one: their sum of squares, or for the layer norm
+  // their mean and the squares' sum about it, whatever the first ones were
+  // (Welford's update); the lanes' are then joined about the column's mean.
+  float mean[VE], rstd[VE], s[1][VE], m[1][VE];
+  float count = 0.f;
+  const auto clear = [&]() {
+    count = 0.f;
+#pragma unroll
+    for (int k = 0; k < VE; ++k) s[0][k] = m[0][k] = 0.f;
+  };
+  const auto take = [&](bool in, const Vec& v) {
+    if (!in) return;
+    if (LAYER) {
+      count += 1.f;
+      const float inv = __builtin_amdgcn_rcpf(count);
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        const float d = v[k] - m[0][k];
+        m[0][k] = fmaf(d, inv, m[0][k]);
+        s[0][k] = fmaf(d, v[k] - m[0][k], s[0][k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < VE; ++k) s[0][k] = fmaf(v[k], v[k], s[0][k]);
+    }
+  };
+  const auto finish = [&]() {
+#pragma unroll
+    for (int k = 0; k < VE; ++k) mean[k] = 0.f;
+    if (LAYER) {
+      float t[1][VE];
+#pragma unroll
+      for (int k = 0; k < VE; ++k) t[0][k] = count * m[0][k];
+      strip_sum<NT, LT, VE, 1>(t, buf);
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        mean[k] = t[0][k] * inv_h;
+        const float d = m[0][k] - mean[k];
+        s[0][k] = fmaf(count * d, d, s[0][k]);
+      }
+    }
+    strip_sum<NT, LT, VE, 1>(s, buf);
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+      rstd[k] = k < nv ? __builtin_amdgcn_rsqf(fmaf(s[0][k], inv_h, p.eps)) : 0.f;
+  };
+  clear();
+  const T* first = p.y ? static_cast<const T*>(p.y) + at.base : x;
+  for (int j0 = 0; j0 < nj; j0 += U) {
+    Vec v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) at.get(v[u], first, j0 + u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) take(rs + (j0 + u) * NR < H, v[u]);
+  }
+  finish();
+  const T* stream = first;
+  if (p.y) {
+    if (p.stats && rs == 0) {
+      if (LAYER) store_n<float, VE>(p.stats + at.at, ns, mean);
+      store_n<float, VE>(p.stats + (LAYER ? at.plane : 0) + at.at, ns, rstd);
+    }
+    const T* g = static_cast<const T*>(p.g) + (p.g ? (size_t)(at.b * p.sg) + at.t0 : 0);
+    clear();
+    for (int j0 = 0; j0 < nj; j0 += U) {
+      Vec yv[U], xv[U], gv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        at.get(yv[u], first, j0 + u);
+        at.get(xv[u], x, j0 + u);
+        if (p.g) at.get(gv[u], g, j0 + u);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = rs + (j0 + u) * NR;
+        const bool in = h < H;
+        const float c = in ? p.w_post[h] * p.scale[h] : 0.f;
+        float out[VE];
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          float silu = 1.f;
+          if (p.g) silu = gv[u][k] * __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gv[u][k]));
+          const float v = (yv[u][k] - mean[k]) * rstd[k];
+          out[k] = fmaf(v * c, silu, xv[u][k]);
+        }
+        Vec ov;
+        ov.set(out);
+        if (in) ov.store(at.spot(o, j0 + u), ns);
+        take(in, ov);
+      }
+    }
+    if (!p.n) return;
+    finish();
+    stream = o;
+  }
+  if (p.stats && rs == 0) {
+    if (LAYER) store_n<float, VE>(p.stats + 2 * at.plane + at.at, ns, mean);
+    store_n<float, VE>(p.stats + (LAYER ? 3 : 1) * at.plane + at.at, ns, rstd);
+  }
+  T* n = static_cast<T*>(p.n) + at.base;
+  for (int j0 = 0; j0 < nj; j0 += U) {
+    Vec v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) at.get(v[u], stream, j0 + u);  // a lane's own stores
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = rs + (j0 + u) * NR;
+      if (h >= H) continue;
+      const float c = p.w_pre[h];
+      float out[VE];
+#pragma unroll
+      for (int k = 0; k < VE; ++k) out[k] = (v[u][k] - mean[k]) * rstd[k] * c;
+      store_n<T, VE>(at.spot(n, j0 + u), ns, out);
+    }
   }
 }
 
@@ -459,6 +631,175 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_kernel(Args p) {
   }
 }
 
+// The backward pass for more channels than the registers hold.  The second
+// norm's sums need t, which needs the first norm's; but t is a combination of
+// do, dn, oh and 1 whose weights a column shares, so one reading of the inputs
+// gives sums from which both norms' follow (with k = scale silu(g) w_post):
+//   sum R yh = sum do k yh + ro (sum P k yh - mean(P oh) sum oh k yh - mean(P) sum k yh)
+//   sum R    = sum do k    + ro (sum P k    - mean(P oh) sum oh k    - mean(P) sum k)
+// and a second reading, still in a cache, writes the gradients.
+template <typename T, bool LAYER, int NT, int LT, int VE, int U>
+__global__ __launch_bounds__(NT) void resnorm_bwd_wide_kernel(Args p) {
+  typedef Packed<T, VE> Vec;
+  constexpr int NR = NT / LT, N = LAYER ? 10 : 4;
+  __shared__ float buf[(NT / 64) * N * LT * VE];
+  extern __shared__ float sums[];  // [2][H]: t yh silu(g), dn oh; a channel is always the same lanes'
+  const int H = p.H;
+  const float inv_h = 1.f / (float)H;
+  const int nj = (H + NR - 1) / NR;
+  for (int h = threadIdx.x / LT; h < H; h += NR)
+    if (threadIdx.x % LT == 0) sums[h] = sums[H + h] = 0.f;
+  const int total = p.B * p.ntile;
+  for (int block = blockIdx.x; block < 8 * p.per; block += gridDim.x) {
+    const int strip = strip_of_block(block, p.per);
+    if (strip >= total) continue;
+    const WideStrip<T, NT, LT, VE> at(p, strip);
+    const int ns = at.ns;
+    const auto input = [&](const void* q, size_t off) {
+      return q ? static_cast<const T*>(q) + off : nullptr;
+    };
+    const T* o = input(p.d_n ? p.x : nullptr, at.base);
+    const T* dn = input(p.d_n, at.base);
+    const T* dout = input(p.d_o, at.base);
+    const T* y = input(p.y, at.base);
+    const T* g = input(p.g, (size_t)(at.b * p.sg) + at.t0);
+    // factor and (layer norm) -mean factor of o and of y; past the end 0
+    float ro[VE], mo[VE], ry[VE], my[VE];
+    load_n<float, VE>(p.stats + (LAYER ? 3 : 1) * at.plane + at.at, dn ? at.nv : 0, ro);
+    load_n<float, VE>(p.stats + 2 * at.plane + at.at, LAYER && dn ? at.nv : 0, mo);
+    load_n<float, VE>(p.stats + (LAYER ? at.plane : 0) + at.at, y ? at.nv : 0, ry);
+    load_n<float, VE>(p.stats + at.at, LAYER && y ? at.nv : 0, my);
+    float s[N][VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      mo[k] *= -ro[k];
+      my[k] *= -ry[k];
+    }
+#pragma unroll
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int k = 0; k < VE; ++k) s[m][k] = 0.f;
+    for (int j0 = 0; j0 < nj; j0 += U) {
+      Vec ov[U], nn[U], dv[U], yv[U], gv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        at.get_any(ov[u], o, j0 + u);
+        at.get_any(nn[u], dn, j0 + u);
+        at.get_any(dv[u], dout, j0 + u);
+        at.get_any(yv[u], y, j0 + u);
+        at.get_any(gv[u], g, j0 + u);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = at.rs + (j0 + u) * NR;
+        const bool in = h < H;
+        const float w = in && dn ? p.w_pre[h] : 0.f;
+        const float c = in && y ? p.w_post[h] * p.scale[h] : 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          const float oh = LAYER ? fmaf(ov[u][k], ro[k], mo[k]) : ov[u][k] * ro[k];
+          const float m = nn[u][k] * oh;
+          sum += m;
+          s[0][k] = fmaf(w, m, s[0][k]);
+          const float P = nn[u][k] * w;
+          float q = c;
+          if (g) q *= gv[u][k] * __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gv[u][k]));
+          const float yh = LAYER ? fmaf(yv[u][k], ry[k], my[k]) : yv[u][k] * ry[k];
+          const float e = q * yh;
+          s[1][k] = fmaf(dv[u][k], e, s[1][k]);
+          s[2][k] = fmaf(P, e, s[2][k]);
+          s[3][k] = fmaf(oh, e, s[3][k]);
+          if (LAYER) {
+            s[N - 6][k] += P;
+            s[N - 5][k] += e;
+            s[N - 4][k] = fmaf(dv[u][k], q, s[N - 4][k]);
+            s[N - 3][k] = fmaf(P, q, s[N - 3][k]);
+            s[N - 2][k] = fmaf(oh, q, s[N - 2][k]);
+            s[N - 1][k] += q;
+          }
+        }
+        sum = lanes_sum<LT>(sum);
+        if (at.lt == 0 && in) sums[H + h] += sum;
+      }
+    }
+    strip_sum<NT, LT, VE, N>(s, buf);
+    float c1[VE], c0[VE], d1[VE], d0[VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      const float a = s[0][k] * inv_h, b = LAYER ? s[N - 6][k] * inv_h : 0.f;
+      c1[k] = -ro[k] * a;
+      c0[k] = -ro[k] * b;
+      float r1 = fmaf(-a, s[3][k], s[2][k]), r0 = 0.f;
+      if (LAYER) {
+        r1 = fmaf(-b, s[N - 5][k], r1);
+        r0 = fmaf(-a, s[N - 2][k], s[N - 3][k]);
+        r0 = fmaf(-b, s[N - 1][k], r0);
+        r0 = fmaf(ro[k], r0, s[N - 4][k]);
+      }
+      r1 = fmaf(ro[k], r1, s[1][k]);
+      d1[k] = -ry[k] * r1 * inv_h;
+      d0[k] = -ry[k] * r0 * inv_h;
+    }
+    T* dx = static_cast<T*>(p.dx) + at.base;
+    T* dy = static_cast<T*>(p.dy) + at.base;
+    T* dg = static_cast<T*>(p.dg) + (size_t)(at.b * p.sdg) + at.t0;
+    for (int j0 = 0; j0 < nj; j0 += U) {
+      Vec ov[U], nn[U], dv[U], yv[U], gv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        at.get_any(ov[u], o, j0 + u);
+        at.get_any(nn[u], dn, j0 + u);
+        at.get_any(dv[u], dout, j0 + u);
+        at.get_any(yv[u], y, j0 + u);
+        at.get_any(gv[u], g, j0 + u);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = at.rs + (j0 + u) * NR;
+        const bool in = h < H;
+        const float w = in && dn ? p.w_pre[h] : 0.f;
+        const float c = in && y ? p.w_post[h] * p.scale[h] : 0.f;
+        float tv[VE], dgv[VE], dyv[VE], sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          const float oh = LAYER ? fmaf(ov[u][k], ro[k], mo[k]) : ov[u][k] * ro[k];
+          float tk = fmaf(nn[u][k], w * ro[k], dv[u][k]);
+          tk = fmaf(c1[k], oh, tk);
+          if (LAYER) tk += c0[k];
+          float silu = 1.f, dsilu = 0.f;
+          if (g) {
+            const float gk = gv[u][k];
+            const float sg = __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gk));
+            silu = gk * sg;
+            dsilu = fmaf(-silu, sg, silu + sg);  // sg (1 + g (1 - sg))
+          }
+          const float yh = LAYER ? fmaf(yv[u][k], ry[k], my[k]) : yv[u][k] * ry[k];
+          const float ty = tk * yh;
+          sum = fmaf(ty, silu, sum);
+          dgv[k] = ty * dsilu * c;
+          dyv[k] = fmaf(d1[k], yh, tk * silu * c * ry[k]);
+          if (LAYER) dyv[k] += d0[k];
+          tv[k] = tk;
+        }
+        if (in) {
+          store_n<T, VE>(at.spot(dx, j0 + u), ns, tv);
+          if (y) store_n<T, VE>(at.spot(dy, j0 + u), ns, dyv);
+          if (g) store_n<T, VE>(at.spot(dg, j0 + u), ns, dgv);
+        }
+        sum = lanes_sum<LT>(sum);
+        if (at.lt == 0 && in) sums[h] += sum;
+      }
+    }
+  }
+  float* part = p.part + (size_t)blockIdx.x * 2 * H;
+  for (int h = threadIdx.x / LT; h < H; h += NR)
+    if (threadIdx.x % LT == 0) {
+      part[h] = sums[h];
+      part[H + h] = sums[H + h];
+    }
+}
+
 // The workgroups' sums, in order and in float64: 16 channels by 64 slices of
 // the workgroups to a block.  With V = sum t yh silu(g): dw_post = scale V,
 // dscale = w_post V.
@@ -499,89 +840,107 @@ __global__ __launch_bounds__(1024) void resnorm_sum_kernel(const float* __restri
 
 constexpr int kMaxGroups = 512;  // workgroups of the backward pass
 
-// Threads, lanes to a row segment, bytes of a lane's steps and channels to a
-// lane.  A strip's inputs stay in registers, so more channels mean shorter
-// segments of each row, which memory serves less well (forward, bf16, 2^25
-// elements: 76-86 us with 128 bytes up to 512 channels, 97 with 64 and 119
-// with 32; backward 136-145 with 256 or 128 bytes, 170 with 64).
+// How a call is laid out: lanes to a row segment and steps to a lane, held in
+// registers (threads, channels to a lane) or looped over.
+//
+// Held, the strip's channels set the segments' length, which memory wants long
+// (backward, bf16, 2^25 elements: 136-145 us with 256 or 128 bytes for up to
+// 256 channels, 170 with 64, 200 with 32); looped, it is free, at the price of
+// reading inputs again from a cache.  Forward: held up to 512 channels (83 us
+// against 88 at 512; 87 against 81 at 1024).  Backward: held up to 1024 (200
+// against 209 there; 255 against 213 at 2048, 600 against 266 at 4096).
+// Looped strips are as wide as leaves one for every compute unit.  A single
+// step takes its channels side by side.
 struct Form {
-  int nt, lt, kh;
+  int nt, lt, ve, kh;  // kh 0: looped
 };
 
-Form fwd_form(int H, int L) {
-  if (L == 1) return H <= 1024 ? Form{256, 1, 4} : Form{1024, 1, 8};
-  if (H <= 512) return {H <= 128 ? 256 : H <= 256 ? 512 : 1024, 8, 4};
-  return {1024, H <= 1024 ? 8 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1, 8};
+int strips(const Form& f, int L) { return (L + f.lt * f.ve - 1) / (f.lt * f.ve); }
+
+Form widest(int B, int L, int ve, int least) {
+  Form f{1024, 16, ve, 0};
+  while (f.lt > least && (long)B * strips(f, L) < 256) f.lt /= 2;
+  return f;
 }
 
-Form bwd_form(int H, int L) {
-  if (L == 1) return H <= 1024 ? Form{256, 1, 4} : Form{1024, 1, 8};
-  if (H <= 2048) return {512, H <= 128 ? 16 : H <= 256 ? 8 : H <= 512 ? 4 : H <= 1024 ? 2 : 1, 4};
-  return {1024, 1, H <= 4096 ? 4 : 8};
+Form fwd_form(int B, int H, int L, int dtype) {
+  if (L == 1) return H <= 1024 ? Form{256, 1, 1, 4} : Form{1024, 1, 1, 8};
+  const int ve = dtype == 0 ? 4 : 8;
+  return H <= 512 ? Form{H <= 128 ? 256 : H <= 256 ? 512 : 1024, 8, ve, 4} : widest(B, L, ve, 2);
 }
 
-// Steps of a strip.
-int strip_steps(const Form& f, int L, int dtype) { return f.lt * (L == 1 ? 1 : dtype == 0 ? 4 : 8); }
-
-int strips(const Form& f, int L, int dtype) {
-  const int n = strip_steps(f, L, dtype);
-  return (L + n - 1) / n;
+Form bwd_form(int B, int H, int L, int dtype) {
+  if (L == 1) return H <= 1024 ? Form{256, 1, 1, 4} : Form{1024, 1, 1, 8};
+  const int ve = dtype == 0 ? 4 : 8;
+  return H <= 1024 ? Form{512, H <= 128 ? 16 : H <= 256 ? 8 : H <= 512 ? 4 : 2, ve, 4}
+                   : widest(B, L, 4, 4);
 }
 
 int groups_of(int B, int H, int L, int dtype) {
-  const long n = (long)B * strips(bwd_form(H, L), L, dtype);
+  const long n = (long)B * strips(bwd_form(B, H, L, dtype), L);
   return (int)std::min<long>((n + 7) / 8 * 8, kMaxGroups);
 }
 
 template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
-void fwd_start(const Args& a, hipStream_t st) {
+void fwd_held(const Args& a, hipStream_t st) {
   hipLaunchKernelGGL((resnorm_fwd_kernel<T, LAYER, NT, LT, VE, KH>), dim3(8u * a.per), dim3(NT), 0,
                      st, a);
+}
+
+template <typename T, bool LAYER, int LT>
+void fwd_wide(const Args& a, hipStream_t st) {
+  hipLaunchKernelGGL((resnorm_fwd_wide_kernel<T, LAYER, 1024, LT, 16 / (int)sizeof(T), 4>),
+                     dim3(8u * a.per), dim3(1024), 0, st, a);
 }
 
 template <typename T, bool LAYER>
 void fwd_run(const Args& a, const Form& f, hipStream_t st) {
   constexpr int VE = 16 / sizeof(T);
   if (a.L == 1)
-    f.nt == 256 ? fwd_start<T, LAYER, 256, 1, 1, 4>(a, st)
-                : fwd_start<T, LAYER, 1024, 1, 1, 8>(a, st);
-  else if (f.kh == 4)
-    f.nt == 256   ? fwd_start<T, LAYER, 256, 8, VE, 4>(a, st)
-    : f.nt == 512 ? fwd_start<T, LAYER, 512, 8, VE, 4>(a, st)
-                  : fwd_start<T, LAYER, 1024, 8, VE, 4>(a, st);
+    f.nt == 256 ? fwd_held<T, LAYER, 256, 1, 1, 4>(a, st) : fwd_held<T, LAYER, 1024, 1, 1, 8>(a, st);
+  else if (f.kh)
+    f.nt == 256   ? fwd_held<T, LAYER, 256, 8, VE, 4>(a, st)
+    : f.nt == 512 ? fwd_held<T, LAYER, 512, 8, VE, 4>(a, st)
+                  : fwd_held<T, LAYER, 1024, 8, VE, 4>(a, st);
   else
-    f.lt == 8   ? fwd_start<T, LAYER, 1024, 8, VE, 8>(a, st)
-    : f.lt == 4 ? fwd_start<T, LAYER, 1024, 4, VE, 8>(a, st)
-    : f.lt == 2 ? fwd_start<T, LAYER, 1024, 2, VE, 8>(a, st)
-                : fwd_start<T, LAYER, 1024, 1, VE, 8>(a, st);
+    f.lt == 16  ? fwd_wide<T, LAYER, 16>(a, st)
+    : f.lt == 8 ? fwd_wide<T, LAYER, 8>(a, st)
+    : f.lt == 4 ? fwd_wide<T, LAYER, 4>(a, st)
+                : fwd_wide<T, LAYER, 2>(a, st);
 }
 
 template <typename T, bool LAYER, int NT, int LT, int VE, int KH>
-void bwd_start(const Args& a, int groups, hipStream_t st) {
+void bwd_held(const Args& a, int groups, hipStream_t st) {
   hipLaunchKernelGGL((resnorm_bwd_kernel<T, LAYER, NT, LT, VE, KH>), dim3((unsigned)groups),
                      dim3(NT), 0, st, a);
+}
+
+template <typename T, bool LAYER, int LT>
+void bwd_wide(const Args& a, int groups, hipStream_t st) {
+  hipLaunchKernelGGL((resnorm_bwd_wide_kernel<T, LAYER, 1024, LT, 4, 2>), dim3((unsigned)groups),
+                     dim3(1024), 2 * a.H * sizeof(float), st, a);
 }
 
 template <typename T, bool LAYER>
 void bwd_run(const Args& a, const Form& f, int groups, hipStream_t st) {
   constexpr int VE = 16 / sizeof(T);
   if (a.L == 1)
-    f.nt == 256 ? bwd_start<T, LAYER, 256, 1, 1, 4>(a, groups, st)
-                : bwd_start<T, LAYER, 1024, 1, 1, 8>(a, groups, st);
-  else if (f.nt == 512)
-    f.lt == 16  ? bwd_start<T, LAYER, 512, 16, VE, 4>(a, groups, st)
-    : f.lt == 8 ? bwd_start<T, LAYER, 512, 8, VE, 4>(a, groups, st)
-    : f.lt == 4 ? bwd_start<T, LAYER, 512, 4, VE, 4>(a, groups, st)
-    : f.lt == 2 ? bwd_start<T, LAYER, 512, 2, VE, 4>(a, groups, st)
-                : bwd_start<T, LAYER, 512, 1, VE, 4>(a, groups, st);
+    f.nt == 256 ? bwd_held<T, LAYER, 256, 1, 1, 4>(a, groups, st)
+                : bwd_held<T, LAYER, 1024, 1, 1, 8>(a, groups, st);
+  else if (f.kh)
+    f.lt == 16  ? bwd_held<T, LAYER, 512, 16, VE, 4>(a, groups, st)
+    : f.lt == 8 ? bwd_held<T, LAYER, 512, 8, VE, 4>(a, groups, st)
+    : f.lt == 4 ? bwd_held<T, LAYER, 512, 4, VE, 4>(a, groups, st)
+                : bwd_held<T, LAYER, 512, 2, VE, 4>(a, groups, st);
   else
-    f.kh == 4 ? bwd_start<T, LAYER, 1024, 1, VE, 4>(a, groups, st)
-              : bwd_start<T, LAYER, 1024, 1, VE, 8>(a, groups, st);
+    f.lt == 16  ? bwd_wide<T, LAYER, 16>(a, groups, st)
+    : f.lt == 8 ? bwd_wide<T, LAYER, 8>(a, groups, st)
+                : bwd_wide<T, LAYER, 4>(a, groups, st);
 }
 
 template <typename T, bool LAYER>
 hipError_t run(const ResnormCall& c, int dtype, bool backward, hipStream_t st) {
-  const Form f = backward ? bwd_form(c.H, c.L) : fwd_form(c.H, c.L);
+  const Form f = backward ? bwd_form(c.B, c.H, c.L, dtype) : fwd_form(c.B, c.H, c.L, dtype);
   Args a{};
   a.x = c.x;
   a.y = c.y;
@@ -594,7 +953,7 @@ hipError_t run(const ResnormCall& c, int dtype, bool backward, hipStream_t st) {
   a.B = c.B;
   a.H = c.H;
   a.L = c.L;
-  a.ntile = strips(f, c.L, dtype);
+  a.ntile = strips(f, c.L);
   a.per = (c.B * a.ntile + 7) / 8;
   a.eps = c.eps;
   a.o = c.o;

@@ -23,6 +23,8 @@ SHAPES = [
     (1, 2050, 21, "f32", False, False), (1, 4096, 18, "bf16", False, False),
     (1, 4100, 9, "f16", True, False), (1, 8192, 11, "f32", False, False),
     (4, 24, 3000, "bf16", False, True),
+    # strips as wide as they get where channels are looped over
+    (5, 514, 6700, "f16", True, True), (4, 1030, 4100, "bf16", False, False),
 ]
 IDS = ["B%dH%dL%d-%s-%s%s" % (b, h, l, t, "layer" if n else "rms", "-ragged" if r else "")
        for b, h, l, t, n, r in SHAPES]
@@ -134,6 +136,29 @@ def test_bad_columns_stay_their_own():
     lens = torch.tensor([3, 0], dtype=torch.int32, device="cuda")
     _, n = bd.resnorm_forward(x, None, None, None, None, s["w_pre"], eps=0.0, lens=lens)
     assert torch.isfinite(n).all() and not n[0, :, 3:].any() and not n[1].any()
+
+
+@pytest.mark.parametrize("H", [40, 600])
+def test_layer_norm_far_from_zero_and_with_outliers(H):
+    """Means a thousand times the spread, and a channel (the first, the last) a
+    thousand times the others: no digits of the variance are lost beyond those
+    of float32 values of that size."""
+    torch = torch_()
+    for case in ("mean", "first", "last"):
+        s = prepared(2, H, 40, "f32", True, False, seed=H)
+        for t in (s["x"], s["y"]):
+            if case == "mean":
+                t += 1000.0
+            else:
+                t[:, 0 if case == "first" else -1] *= 1000.0
+        w = (s["w_post"], s["scale"], s["w_pre"])
+        o, n = bd.resnorm_forward(s["x"], s["y"], s["g"], *w, norm=bd.NORM_LAYER, eps=EPS)
+        a = [np64(t) for t in (s["x"], s["y"], s["g"]) + w[:2]] + [True, EPS]
+        close(o, oracle.resnorm_stream(*a), oracle.resnorm_stream(*a, magnitude=True), c_norm(H),
+              "f32", "o")
+        a = [np64(o), np64(w[2]), True, EPS]
+        close(n, oracle.resnorm_out(*a), oracle.resnorm_out(*a, magnitude=True), c_norm(H), "f32",
+              "n")
 
 
 def test_no_steps():
