@@ -6,6 +6,7 @@ library is missing or a call fails, an exception is raised -- there is no
 fallback path.
 """
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -718,19 +719,45 @@ def _launch(fn, device, stream, *args):
         check(status)
 
 
-def _bytes(fn, args, given, name, device, stream):
-    """A workspace or checkpoint of the size fn reports: the caller's, or new."""
-    torch = _torch()
+@functools.lru_cache(maxsize=256)
+def _gated_bytes(B, H, L, code, kind):
+    """Bytes of a checkpoint of `kind`, or (kind None) of the workspace."""
     need = ctypes.c_size_t(0)
-    check(fn(*args, ctypes.byref(need)))
+    shape = GatedShape(B, H, L, code)
+    if kind is None:
+        check(lib().dssm_gated_workspace_size(ctypes.byref(shape), ctypes.byref(need)))
+    else:
+        check(lib().dssm_gated_ckpt_size(ctypes.byref(shape), kind, ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=256)
+def _resnorm_bytes(B, H, L, code, norm):
+    """Bytes of workspace of the residual norm's backward pass."""
+    need = ctypes.c_size_t(0)
+    shape = ResnormShape(B, H, L, code, norm, 0.0)
+    check(lib().dssm_resnorm_workspace_size(ctypes.byref(shape), ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=256)
+def _ckpt8_bytes(rows, L):
+    need = ctypes.c_size_t(0)
+    check(lib().dssm_ckpt8_size(rows, L, ctypes.byref(need)))
+    return need.value
+
+
+def _buffer(need, given, name, device, stream):
+    """A workspace or checkpoint of `need` bytes: the caller's, or new."""
+    torch = _torch()
     if given is None:
-        given = _empty((max(need.value, 256),), torch.uint8, device, stream)
-        return given, max(need.value, 256)
+        need = max(need, 256)
+        return _empty((need,), torch.uint8, device, stream), need
     if not isinstance(given, torch.Tensor) or given.device != device or not given.is_contiguous():
         raise ValueError("%s must be a contiguous tensor on %s" % (name, device))
     n = given.numel() * given.element_size()
-    if n < need.value and name != "workspace":  # a workspace's size the library checks itself
-        raise ValueError("%s has %d bytes, needs %d" % (name, n, need.value))
+    if n < need and name != "workspace":  # a workspace's size the library checks itself
+        raise ValueError("%s has %d bytes, needs %d" % (name, n, need))
     return given, n
 
 
@@ -753,9 +780,9 @@ def _gated_forward(u, r, i, log_re, kind, x, x_out, lens, y, ckpt, workspace, st
     xo = xp if x_out is None else _vec(x_out, "x_out", B * H, dev)
     y = _new(u, stream) if y is None else _plain(y, "y", u, "u")
     sp = ctypes.byref(GatedShape(B, H, L, code))
-    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, (sp,), workspace, "workspace", dev, stream)
+    ws, nbytes = _buffer(_gated_bytes(B, H, L, code, None), workspace, "workspace", dev, stream)
     if kind != CKPT_NONE:
-        ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, (sp, kind), ckpt, "ckpt", dev, stream)
+        ckpt, _ = _buffer(_gated_bytes(B, H, L, code, kind), ckpt, "ckpt", dev, stream)
     _launch(lib().dssm_gated_forward, dev, stream, ctypes.byref(inp), sp, xp, xo, y.data_ptr(),
             kind, _ptr(ckpt), ws.data_ptr(), nbytes)
     return y, ckpt
@@ -833,8 +860,8 @@ def gated_backward(dy, ckpt, kind, log_re, u=None, r=None, i=None, dx=None, lens
     out["dlog_re"] = _empty((H,), torch.float32, dev, stream)
     out["dx0"] = _empty((B, H), torch.float32, dev, stream)
     sp = ctypes.byref(GatedShape(B, H, L, code))
-    ws, nbytes = _bytes(lib().dssm_gated_workspace_size, (sp,), workspace, "workspace", dev, stream)
-    ckpt, _ = _bytes(lib().dssm_gated_ckpt_size, (sp, kind), ckpt, "ckpt", dev, stream)
+    ws, nbytes = _buffer(_gated_bytes(B, H, L, code, None), workspace, "workspace", dev, stream)
+    ckpt, _ = _buffer(_gated_bytes(B, H, L, code, kind), ckpt, "ckpt", dev, stream)
     inp = GatedInputs(_ptr(u), _ptr(r), _ptr(i), sb, _vec(log_re, "log_re", H, dev),
                       _lens_ptr(lens, B, dev))
     g = GatedGrads(out["du"].data_ptr(), out["dr"].data_ptr(), out["di"].data_ptr(), gsb,
@@ -855,9 +882,7 @@ def _rows_of(shape):
 
 def ckpt8_size(shape):
     """Bytes of a tensor of this shape in 8 bits."""
-    out = ctypes.c_size_t(0)
-    check(lib().dssm_ckpt8_size(*_rows_of(tuple(shape)), ctypes.byref(out)))
-    return out.value
+    return _ckpt8_bytes(*_rows_of(tuple(shape)))
 
 
 def ckpt8_pack(x, blob=None, stream=None):
@@ -868,7 +893,7 @@ def ckpt8_pack(x, blob=None, stream=None):
         raise ValueError("x must be contiguous")
     rows, L = _rows_of(x.shape)
     dev = x.device
-    blob, _ = _bytes(lib().dssm_ckpt8_size, (rows, L), blob, "blob", dev, stream)
+    blob, _ = _buffer(_ckpt8_bytes(rows, L), blob, "blob", dev, stream)
     _launch(lib().dssm_ckpt8_pack, dev, stream, x.data_ptr(), rows, L, code, blob.data_ptr())
     return blob
 
@@ -881,7 +906,7 @@ def ckpt8_unpack(blob, shape, dtype, x=None, stream=None):
     shape = tuple(shape)
     rows, L = _rows_of(shape)
     dev = blob.device
-    _bytes(lib().dssm_ckpt8_size, (rows, L), blob, "blob", dev, stream)
+    _buffer(_ckpt8_bytes(rows, L), blob, "blob", dev, stream)
     if x is None:
         x = _empty(shape, dtype, dev, stream)
     code = _dtype_code(x, "x")
@@ -984,8 +1009,8 @@ def resnorm_backward(o, y, g, stats, w_post, scale, w_pre, do, dn, norm=NORM_RMS
     elif dg is not None:
         raise ValueError("dg needs g")
     sp = ctypes.byref(ResnormShape(B, H, L, code, int(norm), 0.0))
-    ws, nbytes = _bytes(lib().dssm_resnorm_workspace_size, (sp,), workspace, "workspace", dev,
-                        stream)
+    ws, nbytes = _buffer(_resnorm_bytes(B, H, L, code, int(norm)), workspace, "workspace", dev,
+                         stream)
     gr = ResnormGrads(_ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dg"]), sdg,
                       _ptr(out["dw_post"]), _ptr(out["dscale"]), _ptr(out["dw_pre"]))
     _launch(lib().dssm_resnorm_backward, dev, stream, o.data_ptr(), _ptr(y), _ptr(g), sg,

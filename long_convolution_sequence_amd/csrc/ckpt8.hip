@@ -12,16 +12,18 @@ namespace {
 // Lane slots of a row: 8 steps each, whole groups (8 slots).
 __host__ __device__ inline int row_slots(int L) { return ckpt8_groups(L) * 8; }
 
-template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, long n, int L,
+// I: the type slots are counted in, 32 bits where they fit (a division of 64
+// bits costs more than the rest of a slot's work).
+template <typename T, typename I>
+__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, I n, int L,
                                                    int8_t* __restrict__ q8,
                                                    uint8_t* __restrict__ e8) {
   const int slots = row_slots(L);
   const int pitch = ckpt8_row(L), groups = ckpt8_groups(L);
   // n is a multiple of 8: the lanes of a group take part together
-  for (long k = (long)blockIdx.x * 256 + threadIdx.x; k < n; k += (long)gridDim.x * 256) {
-    const long row = k / slots;
-    const int t = (int)(k - row * slots) * 8;
+  for (I k = (I)blockIdx.x * 256 + threadIdx.x; k < n; k += (I)gridDim.x * 256) {
+    const size_t row = k / (I)slots;
+    const int t = (int)(k - (I)row * (I)slots) * 8;
     const int ns = min(max(L - t, 0), 8);
     float v[8];
     load_n<T, 8>(x + row * L + t, ns, v);
@@ -34,15 +36,15 @@ __global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, long
   }
 }
 
-template <typename T>
+template <typename T, typename I>
 __global__ __launch_bounds__(256) void unpack_kernel(const int8_t* __restrict__ q8,
-                                                     const uint8_t* __restrict__ e8, long n, int L,
+                                                     const uint8_t* __restrict__ e8, I n, int L,
                                                      T* __restrict__ x) {
   const int slots = (L + 7) / 8;
   const int pitch = ckpt8_row(L), groups = ckpt8_groups(L);
-  for (long k = (long)blockIdx.x * 256 + threadIdx.x; k < n; k += (long)gridDim.x * 256) {
-    const long row = k / slots;
-    const int t = (int)(k - row * slots) * 8;
+  for (I k = (I)blockIdx.x * 256 + threadIdx.x; k < n; k += (I)gridDim.x * 256) {
+    const size_t row = k / (I)slots;
+    const int t = (int)(k - (I)row * (I)slots) * 8;
     float v[8];
     dequantise8(*reinterpret_cast<const uint2*>(q8 + row * pitch + t),
                 e8[row * groups + t / kGroup], v);
@@ -50,19 +52,26 @@ __global__ __launch_bounds__(256) void unpack_kernel(const int8_t* __restrict__ 
   }
 }
 
-template <typename T>
-hipError_t run(const void* x, long rows, int L, void* blob, void* out, hipStream_t st) {
+template <typename T, typename I>
+hipError_t start(const void* x, long rows, int L, long n, void* blob, void* out, hipStream_t st) {
   int8_t* q8 = static_cast<int8_t*>(blob);
   uint8_t* e8 = reinterpret_cast<uint8_t*>(blob) + ckpt8_exp_offset(rows, L);
-  const long n = rows * (out ? (L + 7) / 8 : row_slots(L));
-  const dim3 grid((unsigned)std::min<long>((n + 255) / 256, 8192));
+  const dim3 grid((unsigned)std::min<long>((n + 255) / 256, 16384));
   if (out)
-    hipLaunchKernelGGL((unpack_kernel<T>), grid, dim3(256), 0, st, q8, e8, n, L,
+    hipLaunchKernelGGL((unpack_kernel<T, I>), grid, dim3(256), 0, st, q8, e8, (I)n, L,
                        static_cast<T*>(out));
   else
-    hipLaunchKernelGGL((pack_kernel<T>), grid, dim3(256), 0, st, static_cast<const T*>(x), n, L,
-                       q8, e8);
+    hipLaunchKernelGGL((pack_kernel<T, I>), grid, dim3(256), 0, st, static_cast<const T*>(x), (I)n,
+                       L, q8, e8);
   return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const void* x, long rows, int L, void* blob, void* out, hipStream_t st) {
+  const long n = rows * (out ? (L + 7) / 8 : row_slots(L));
+  // the loop's counter runs up to a grid past n
+  return n < (1L << 31) ? start<T, uint32_t>(x, rows, L, n, blob, out, st)
+                        : start<T, uint64_t>(x, rows, L, n, blob, out, st);
 }
 
 }  // namespace

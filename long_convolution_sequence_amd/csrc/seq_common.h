@@ -203,16 +203,25 @@ __device__ __forceinline__ int quantise8(const float* x, int width, uint2* out) 
   for (int o = 1; o < width; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
   const int byte = group_byte(top);
   const float inv = byte == kExpNan ? 0.f : pow2f(127 - byte);
-  int q[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) q[k] = byte == kExpNan ? 0 : (int)__builtin_rintf(x[k] * inv);
+  // x inv is exact; added to 3 2^22 it is rounded to a whole number, to even, whose
+  // low byte is the float's
+  uint32_t q[8];
   if (byte == last_byte<T>()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = min(max(q[k], -63), 63);
-  }
-  uint32_t w[2] = {0, 0};
+    for (int k = 0; k < 8; ++k)
+      q[k] = __float_as_uint(fminf(fmaxf(x[k] * inv, -63.f), 63.f) + 12582912.f);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(q[k] & 255) << (8 * (k & 3));
+    for (int k = 0; k < 8; ++k) q[k] = __float_as_uint(fmaf(x[k], inv, 12582912.f));
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    // bytes 0 of two words side by side, then of two pairs
+    const uint32_t lo = __builtin_amdgcn_perm(q[4 * k + 1], q[4 * k], 0x0c0c0400);
+    const uint32_t hi = __builtin_amdgcn_perm(q[4 * k + 3], q[4 * k + 2], 0x0c0c0400);
+    w[k] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+  }
   *out = make_uint2(w[0], w[1]);
   return byte;
 }
