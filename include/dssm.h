@@ -446,7 +446,10 @@ int dssm_gated_workspace_size(const dssm_gated_shape* s, size_t* bytes);
 /* Bytes of a checkpoint of `kind` (0 for DSSM_CKPT_NONE).  Layout, every part
  * padded to 256 bytes: the states [B, H, ceil(L / 512)] float32 entering the
  * chunks, then for DSSM_CKPT_INT8 u, r and i, each as dssm_ckpt8_pack writes
- * B H rows of L. */
+ * B H rows of L, but the gates' logits r and i only up to +-31.75 (infinities
+ * and a mask's lowest value too: the sigmoid is 0 or 1 to 2^-45 there, and
+ * they would cost the rest of their group its scale).  Steps that are not live
+ * are 0. */
 int dssm_gated_ckpt_size(const dssm_gated_shape* s, int kind, size_t* bytes);
 
 /* The gated linear recurrence: for every (b, h) a real mode whose decay and
@@ -539,7 +542,7 @@ typedef struct {
  * 1 / sqrt of y, then of o) for DSSM_NORM_LAYER; rows of a norm that the call
  * does not form are not written.  Requires H <= 8192 (a workgroup holds the
  * channels of a few steps; larger H: DSSM_ERR_UNSUPPORTED), L <= 2^20
- * and B ceil(L / 4) <= 2^22.
+ * and B ceil(L / 8) <= 2^21.
  * A single token is L = 1. */
 int dssm_resnorm_forward(const void* x, const void* y, const void* g, long long stride_g,
                          const dssm_resnorm_params* p, const dssm_resnorm_shape* s,

@@ -14,7 +14,7 @@ namespace {
 constexpr int kMaxL = 1 << 24;
 constexpr int kMaxH = 65535;
 constexpr long kMaxRows = 1L << 24;   // workgroups of 256 lanes, four rows each at least
-constexpr long kMaxStrips = 1L << 22; // workgroups of up to 1024 lanes
+constexpr long kMaxStrips = 1L << 21; // workgroups of up to 1024 lanes
 
 bool dtype_ok(int d) { return d == DSSM_F32 || d == DSSM_BF16 || d == DSSM_F16; }
 size_t elem_size(int d) { return d == DSSM_F32 ? 4 : 2; }
@@ -317,10 +317,10 @@ static int check_resnorm(const dssm_resnorm_shape* s, bool* empty) {
     return fail(DSSM_ERR_UNSUPPORTED, "resnorm: H=%d exceeds %d", s->H, kResnormMaxH);
   if (s->L > kResnormMaxL)
     return fail(DSSM_ERR_UNSUPPORTED, "resnorm: L=%d exceeds %d", s->L, kResnormMaxL);
-  // strips of four steps at least
-  if ((long)s->B * ((s->L + 3) / 4) > kMaxStrips)
-    return fail(DSSM_ERR_UNSUPPORTED, "resnorm: B*ceil(L/4)=%ld exceeds 2^22",
-                (long)s->B * ((s->L + 3) / 4));
+  // strips of eight steps at least
+  if ((long)s->B * ((s->L + 7) / 8) > kMaxStrips)
+    return fail(DSSM_ERR_UNSUPPORTED, "resnorm: B*ceil(L/8)=%ld exceeds 2^21",
+                (long)s->B * ((s->L + 7) / 8));
   return DSSM_OK;
 }
 

@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ x, I n,
     float v[8];
     load_n<T, 8>(x + row * L + t, ns, v);
     uint2 q;
-    const int byte = quantise8<T>(v, 8, &q);
+    const int byte = quantise8<T, false>(v, 8, &q);
     if (ns > 0) {
       *reinterpret_cast<uint2*>(q8 + row * pitch + t) = q;
       if ((t & (kGroup - 1)) == 0) e8[row * groups + t / kGroup] = (uint8_t)byte;

@@ -146,18 +146,29 @@ __device__ __forceinline__ void tile_scan(float& S, float& V, int gl, int n, flo
 }
 
 // What enters segment `seg` of a split row: the pairs of the segments before
-// it (REV: after it) applied to `start`.  Every lane of the wave gets it.
+// it (REV: after it) applied to `start`, four neighbours to a lane and all of a
+// round asked for at once.  Every lane of the wave gets it.
+constexpr int kJoin = 256;  // segments of a round
 template <bool REV>
 __device__ float join_segments(const float2* agg, int nseg, int seg, float start) {
   const int lane = threadIdx.x & 63;
   const int count = REV ? nseg - 1 - seg : seg;
   float c = start;
-  for (int base = 0; base < count; base += 64) {
+  for (int base = 0; base < count; base += kJoin) {
     // lane order = order of application
-    const int j = base + lane;
-    float2 t = make_float2(0.f, 0.f);
-    if (j < count) t = agg[REV ? nseg - 1 - j : j];
-    float S = t.x, V = t.y;
+    float2 t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = base + 4 * lane + k;
+      t[k] = make_float2(0.f, 0.f);
+      if (j < count) t[k] = agg[REV ? nseg - 1 - j : j];
+    }
+    float S = 0.f, V = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      V = fmaf(exp2_fast(-t[k].x), V, t[k].y);
+      S += t[k].x;
+    }
     wave_scan<false>(S, V);
     c = fmaf(exp2_fast(-lane_of(S, 63)), c, lane_of(V, 63));
   }
@@ -398,10 +409,12 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
         for (int j = 0; j < 8; ++j) r[j] = j < nv ? r[j] : 0.f;
       }
       const float* x[3] = {u, r, i};
+      const int width = SHORT ? min(8, at.n) : 8;
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         uint2 q;
-        const int byte = quantise8<T>(x[m], SHORT ? min(8, at.n) : 8, &q);
+        const int byte = m == 0 ? quantise8<T, false>(x[m], width, &q)
+                                : quantise8<T, true>(x[m], width, &q);
         if (ns > 0) {
           *reinterpret_cast<uint2*>(p.q8[m] + (size_t)at.row * ckpt8_row(p.L) + t) = q;
           if ((t & (kGroup - 1)) == 0)
@@ -663,9 +676,22 @@ struct Plan {
   int wpr, lpr, nseg, seg_tiles;
 };
 
-Plan plan_of(long rows, int L) {
+// A row of up to 512 steps is one wave tile; shorter ones share a wave.
+//
+// Longer rows are walked by four waves, or by one each when there are enough
+// of them: the waves then meet no barrier and all rows are under way at once
+// (bf16, 2^26 elements, forward / backward: 8192 rows 109 / 190 us against 107 /
+// 215 with four waves; 2048 rows 111 / 192 against 112 / 195; 1024 rows 141 /
+// 244 against 113 / 200).
+//
+// Few rows leave compute units idle: they are cut into segments, about 2048
+// workgroups in all and no more to a row than one round joins, at the price of reading the inputs (backward: the
+// recurrence gate and dy) twice (bf16, 2^25 elements, forward / backward: 64
+// rows 90 / 109 us against 274 / 403 unsplit, with 1024 workgroups 92 / 114;
+// 256 rows 91 / 111 against 76 / 121; 512 rows 88 / 108 against 55 / 103).
+Plan plan_of(long rows, int L, bool backward) {
   Plan p{1, 64, 1, 1};
-  if (L <= kChunk) {  // one wave tile holds the row; short rows share a wave
+  if (L <= kChunk) {
     p.lpr = 1;
     while (p.lpr < 64 && p.lpr * 8 < L) p.lpr *= 2;
     return p;
@@ -676,8 +702,9 @@ Plan plan_of(long rows, int L) {
   }
   p.wpr = 4;
   const int ntile = (L + 4 * kChunk - 1) / (4 * kChunk);
-  // few rows: segments of whole tiles, about 1024 workgroups in all
-  const long nseg = rows >= 512 ? 1 : std::min<long>(ntile, (1024 + rows - 1) / rows);
+  const long nseg = rows >= (backward ? 512 : 256)
+                        ? 1
+                        : std::min<long>(std::min(ntile, kJoin), (2048 + rows - 1) / rows);
   p.seg_tiles = (int)((ntile + nseg - 1) / nseg);
   p.nseg = (ntile + p.seg_tiles - 1) / p.seg_tiles;
   return p;
@@ -763,7 +790,7 @@ hipError_t bwd_plan(const Args& a, const Plan& pl, hipStream_t st) {
 template <typename T>
 hipError_t gated_run(const GatedCall& c, bool backward, hipStream_t st) {
   const long rows = (long)c.B * c.H;
-  const Plan pl = plan_of(rows, c.L);
+  const Plan pl = plan_of(rows, c.L, backward);
   const Args a = make_args(c, pl);
   if (!backward) {
     if (pl.wpr > 1) return fwd_launch<T, 4, false>(a, pl, c.kind, st);
@@ -816,7 +843,8 @@ GatedCkpt gated_ckpt_layout(long rows, int L, int kind) {
 
 size_t gated_workspace(int B, int H, int L) {
   const long rows = (long)B * H;
-  const Plan pl = plan_of(rows, L);
+  // the backward pass is split at least as often as the forward pass
+  const Plan pl = plan_of(rows, L, true);
   return align_up((size_t)rows * pl.nseg * sizeof(float2), 256) +
          align_up((size_t)rows * pl.nseg * sizeof(double), 256);
 }

@@ -193,20 +193,31 @@ constexpr int last_byte() { return 128 - 6 + 127; }
 template <>
 constexpr int last_byte<_Float16>() { return 16 - 6 + 127; }
 
+// What a gate's logit may reach in 8 bits, 127 / 4: a sigmoid is 0 or 1 to
+// 2^-45 there, and a step that is masked by an infinite or the lowest logit
+// costs its neighbours no more of their scale.
+constexpr float kGateMax = 31.75f;
+
 // Eight steps of one lane, of type T, in 8 bits; the lanes of a group are
-// `width` (<= 8) neighbours.  Returns the group's byte.
-template <typename T>
+// `width` (<= 8) neighbours.  GATE: values past kGateMax (Inf too) count as it.
+// Returns the group's byte.
+template <typename T, bool GATE>
 __device__ __forceinline__ int quantise8(const float* x, int width, uint2* out) {
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) top = max(top, abs_bits(x[k]));
   for (int o = 1; o < width; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  if (GATE && top <= 0x7f800000u) top = min(top, __float_as_uint(kGateMax));
   const int byte = group_byte(top);
   const float inv = byte == kExpNan ? 0.f : pow2f(127 - byte);
   // x inv is exact; added to 3 2^22 it is rounded to a whole number, to even, whose
   // low byte is the float's
   uint32_t q[8];
-  if (byte == last_byte<T>()) {
+  if (GATE) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      q[k] = __float_as_uint(__builtin_amdgcn_fmed3f(x[k] * inv, -127.f, 127.f) + 12582912.f);
+  } else if (byte == last_byte<T>()) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       q[k] = __float_as_uint(fminf(fmaxf(x[k] * inv, -63.f), 63.f) + 12582912.f);

@@ -20,6 +20,8 @@ SHAPES = [
     (3, 3, 513, "f32", True), (4, 5, 2047, "f16", True), (2, 3, 2048, "bf16", False),
     (2, 3, 2049, "f32", False), (3, 2, 6145, "f32", True), (1, 1, 20000, "f32", False),
     (4, 131, 2100, "bf16", True), (4, 2049, 530, "f16", True), (8, 1024, 1030, "f32", False),
+    # many segments, and segments of several tiles
+    (1, 2, 150000, "f32", False), (3, 85, 30000, "bf16", True),
 ]
 IDS = ["B%dH%dL%d-%s%s" % (b, h, l, t, "-ragged" if r else "") for b, h, l, t, r in SHAPES]
 
@@ -32,6 +34,11 @@ def prepared(B, H, L, dtype, ragged, seed, joint=False):
         for k in ("u", "r", "i", "dy"):
             spoil_padding(s[k], s["lens"])
     return s
+
+
+def gate8(t):
+    """A gate's logit as an 8-bit checkpoint bounds it."""
+    return np.clip(t, -31.75, 31.75)
 
 
 def reference(s, **kw):
@@ -75,7 +82,7 @@ def test_backward(shape, kind):
     # the states a checkpoint begins with are the forward pass's own
     starts = np64(ckpt[:4 * B * H * nch].view(torch.float32).view(B, H, nch))
     if kind == "int8":
-        u, r, i = (oracle.ckpt8(t) for t in (u, r, i))
+        u, r, i = oracle.ckpt8(u), oracle.ckpt8(gate8(r)), oracle.ckpt8(gate8(i))
     args = (u, r, i, np64(s["log_re"]), dy, np64(s["dx"]), np64(s["x0"]), lens, starts)
     ref = oracle.gated_backward(*args)
     mag = oracle.gated_backward(*args, magnitude=True)
@@ -114,7 +121,46 @@ def test_eight_bits_hold_what_the_oracle_says():
         n = bd.ckpt8_size((3, 4, L))
         for k, name in enumerate(("u", "r", "i")):
             got = bd.ckpt8_unpack(ckpt[off + k * n:off + (k + 1) * n], (3, 4, L), torch.float32)
-            assert np.array_equal(np64(got), oracle.ckpt8(np.nan_to_num(np64(s[name])))), name
+            ref = np.nan_to_num(np64(s[name]))
+            assert np.array_equal(np64(got), oracle.ckpt8(ref if name == "u" else gate8(ref))), name
+
+
+@pytest.mark.parametrize("kind", ["state", "int8"])
+@pytest.mark.parametrize("mask", [float("-inf"), None, float("inf")])
+def test_masked_gates(mask, kind):
+    """Steps shut or opened by an infinite logit or the type's lowest value, whole
+    groups and rows of them: a shut step keeps the state and has no gradient of
+    its input; everything is finite and, from 8 bits too, the oracle's."""
+    torch = torch_()
+    B, H, L = 2, 3, 700
+    s = prepared(B, H, L, "bf16", False, seed=71)
+    value = torch.finfo(torch.bfloat16).min if mask is None else mask
+    shut = torch.rand(B, 1, L, device="cuda") < 0.2
+    shut[0, 0, 64:200] = True
+    shut[1] = True
+    for k in ("r", "i"):
+        s[k] = s[k].masked_fill(shut, value)
+    k = KINDS[kind]
+    y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], k, x=s["x0"],
+                                    x_out=torch.empty_like(s["x0"]))
+    big = lambda t: np.clip(np64(t), -1e30, 1e30)
+    a = [np64(s["u"]), big(s["r"]), big(s["i"]), np64(s["log_re"])]
+    ref, _ = oracle.gated_recurrence(*a, x0=np64(s["x0"]))
+    mag, _ = oracle.gated_recurrence(*a, x0=np64(s["x0"]), magnitude=True)
+    close(y, ref, mag, c_gated(L), "bf16", "y")
+    kept = dict(u=s["u"], r=s["r"], i=s["i"]) if kind == "state" else {}
+    got = bd.gated_backward(s["dy"], ckpt, k, s["log_re"], dx=s["dx"], **kept)
+    starts = np64(ckpt[:4 * B * H * 2].view(torch.float32).view(B, H, 2))
+    if kind == "int8":
+        a[:3] = oracle.ckpt8(a[0]), oracle.ckpt8(gate8(a[1])), oracle.ckpt8(gate8(a[2]))
+    elif value < 0:
+        assert not got["du"][shut.expand_as(y)].any()
+    args = a + [np64(s["dy"]), np64(s["dx"]), np64(s["x0"]), None, starts]
+    # a logit of 31.75 carries 31.75 log2(e) roundings of its exponent, twice
+    c = 2 * (c_gated(L) + 100)
+    for n, v, m in zip(("du", "dr", "di", "dlog_re", "dx0"), oracle.gated_backward(*args),
+                       oracle.gated_backward(*args, magnitude=True)):
+        close(got[n], v, m, c, "f32" if n in ("dlog_re", "dx0") else "bf16", n)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
