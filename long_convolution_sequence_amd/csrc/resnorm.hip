@@ -69,6 +69,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
   if (LT >= 4) v += row_move<0x4e>(v);    // pairs swapped
   if (LT >= 8) v += row_move<0x141>(v);   // mirrored in 8 lanes, whose fours agree by now
   if (LT >= 16) v += row_move<0x140>(v);  // mirrored in 16
+  if (LT >= 32) v = rows_sum(v);
+  if (LT >= 64) v = halves_sum(v);
   return v;
 }
 
@@ -79,7 +81,9 @@ __device__ __forceinline__ float column_sum(float v) {
   if (LT <= 2) v += row_move<0x4e>(v);   // the pairs' lanes keep their place
   if (LT <= 4) v += row_move<0x124>(v);  // rotated by 4: with the next, every fourth of 16
   if (LT <= 8) v += row_move<0x128>(v);  // rotated by 8
-  return halves_sum(rows_sum(v));
+  if (LT <= 16) v = rows_sum(v);
+  if (LT <= 32) v = halves_sum(v);
+  return v;
 }
 
 // N sets of VE values summed over the workgroup's lanes of the same strip
@@ -103,11 +107,12 @@ __device__ __forceinline__ void strip_sum(float (*v)[VE], float* buf) {
       for (int k = 0; k < VE; ++k) buf[wave * C + (m * LT + lt) * VE + k] = v[m][k];
   __syncthreads();
   if (W > 4) {
-    if (threadIdx.x < C) {
+    // each column is one thread's: no other reads or writes it before the barrier
+    for (int c = threadIdx.x; c < C; c += NT) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += buf[w * C + threadIdx.x];
-      buf[threadIdx.x] = s;  // its own column: no other thread reads it before the barrier
+      for (int w = 0; w < W; ++w) s += buf[w * C + c];
+      buf[c] = s;
     }
     __syncthreads();
   }
@@ -849,16 +854,18 @@ constexpr int kMaxGroups = 512;  // workgroups of the backward pass
 // reading inputs again from a cache.  Forward: held up to 512 channels (83 us
 // against 88 at 512; 87 against 81 at 1024).  Backward: held up to 1024 (200
 // against 209 there; 255 against 213 at 2048, 600 against 266 at 4096).
-// Looped strips are as wide as leaves one for every compute unit.  A single
-// step takes its channels side by side.
+// Up to 128 channels and where channels are looped over, strips are as wide as
+// the registers allow and as leaves one for every compute unit (32 channels,
+// forward / backward: 79 / 178 us with 256 and 512 bytes, 115 / 275 with 128
+// and 256).  A single step takes its channels side by side.
 struct Form {
   int nt, lt, ve, kh;  // kh 0: looped
 };
 
 int strips(const Form& f, int L) { return (L + f.lt * f.ve - 1) / (f.lt * f.ve); }
 
-Form widest(int B, int L, int ve, int least) {
-  Form f{1024, 16, ve, 0};
+// f, or narrower until there is a strip for every compute unit.
+Form spread(Form f, int B, int L, int least) {
   while (f.lt > least && (long)B * strips(f, L) < 256) f.lt /= 2;
   return f;
 }
@@ -866,14 +873,17 @@ Form widest(int B, int L, int ve, int least) {
 Form fwd_form(int B, int H, int L, int dtype) {
   if (L == 1) return H <= 1024 ? Form{256, 1, 1, 4} : Form{1024, 1, 1, 8};
   const int ve = dtype == 0 ? 4 : 8;
-  return H <= 512 ? Form{H <= 128 ? 256 : H <= 256 ? 512 : 1024, 8, ve, 4} : widest(B, L, ve, 2);
+  if (H > 512) return spread({1024, 16, ve, 0}, B, L, 2);
+  if (H > 128) return {H <= 256 ? 512 : 1024, 8, ve, 4};
+  return spread({256, H <= 16 ? 64 : H <= 32 ? 32 : H <= 64 ? 16 : 8, ve, 4}, B, L, 8);
 }
 
 Form bwd_form(int B, int H, int L, int dtype) {
   if (L == 1) return H <= 1024 ? Form{256, 1, 1, 4} : Form{1024, 1, 1, 8};
   const int ve = dtype == 0 ? 4 : 8;
-  return H <= 1024 ? Form{512, H <= 128 ? 16 : H <= 256 ? 8 : H <= 512 ? 4 : 2, ve, 4}
-                   : widest(B, L, 4, 4);
+  if (H > 1024) return spread({1024, 16, 4, 0}, B, L, 4);
+  if (H > 128) return {512, H <= 256 ? 8 : H <= 512 ? 4 : 2, ve, 4};
+  return spread({512, H <= 32 ? 64 : H <= 64 ? 32 : 16, ve, 4}, B, L, 16);
 }
 
 int groups_of(int B, int H, int L, int dtype) {
@@ -899,7 +909,10 @@ void fwd_run(const Args& a, const Form& f, hipStream_t st) {
   if (a.L == 1)
     f.nt == 256 ? fwd_held<T, LAYER, 256, 1, 1, 4>(a, st) : fwd_held<T, LAYER, 1024, 1, 1, 8>(a, st);
   else if (f.kh)
-    f.nt == 256   ? fwd_held<T, LAYER, 256, 8, VE, 4>(a, st)
+    f.lt == 64    ? fwd_held<T, LAYER, 256, 64, VE, 4>(a, st)
+    : f.lt == 32  ? fwd_held<T, LAYER, 256, 32, VE, 4>(a, st)
+    : f.lt == 16  ? fwd_held<T, LAYER, 256, 16, VE, 4>(a, st)
+    : f.nt == 256 ? fwd_held<T, LAYER, 256, 8, VE, 4>(a, st)
     : f.nt == 512 ? fwd_held<T, LAYER, 512, 8, VE, 4>(a, st)
                   : fwd_held<T, LAYER, 1024, 8, VE, 4>(a, st);
   else
@@ -928,7 +941,9 @@ void bwd_run(const Args& a, const Form& f, int groups, hipStream_t st) {
     f.nt == 256 ? bwd_held<T, LAYER, 256, 1, 1, 4>(a, groups, st)
                 : bwd_held<T, LAYER, 1024, 1, 1, 8>(a, groups, st);
   else if (f.kh)
-    f.lt == 16  ? bwd_held<T, LAYER, 512, 16, VE, 4>(a, groups, st)
+    f.lt == 64   ? bwd_held<T, LAYER, 512, 64, VE, 4>(a, groups, st)
+    : f.lt == 32 ? bwd_held<T, LAYER, 512, 32, VE, 4>(a, groups, st)
+    : f.lt == 16 ? bwd_held<T, LAYER, 512, 16, VE, 4>(a, groups, st)
     : f.lt == 8 ? bwd_held<T, LAYER, 512, 8, VE, 4>(a, groups, st)
     : f.lt == 4 ? bwd_held<T, LAYER, 512, 4, VE, 4>(a, groups, st)
                 : bwd_held<T, LAYER, 512, 2, VE, 4>(a, groups, st);

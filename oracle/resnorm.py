@@ -19,7 +19,13 @@ import numpy as np
 def _norm(a, layer, eps):
     m = a.mean(axis=1, keepdims=True) if layer else np.zeros_like(a[:, :1])
     f = 1.0 / np.sqrt(((a - m) ** 2).mean(axis=1, keepdims=True) + eps)
-    return a - m, f, m
+    return a - m, f
+
+
+def _wide(a, layer):
+    """|a| plus, where the mean is taken off, the mean of |a|: the terms of
+    a - mean(a) by their absolute values."""
+    return np.abs(a) + (np.abs(a).mean(axis=1, keepdims=True) if layer else 0.0)
 
 
 def _vec(w):
@@ -34,24 +40,24 @@ def _silu(g):
 def resnorm_stream(x, y, g, w_post, scale, layer, eps, magnitude=False):
     """o [B,H,L] (float64, not rounded)."""
     x, y = np.asarray(x, dtype=np.float64), np.asarray(y, dtype=np.float64)
-    c, f, m = _norm(y, layer, eps)
+    c, f = _norm(y, layer, eps)
     silu = np.ones_like(x) if g is None else _silu(np.asarray(g, dtype=np.float64))[0]
     if magnitude:
-        return np.abs(x) + np.abs(_vec(scale) * _vec(w_post) * silu) * (np.abs(y) + np.abs(m)) * f
+        return np.abs(x) + np.abs(_vec(scale) * _vec(w_post) * silu) * _wide(y, layer) * f
     return x + _vec(scale) * (c * f * _vec(w_post)) * silu
 
 
 def resnorm_out(stored, w_pre, layer, eps, magnitude=False):
     """n [B,H,L] from the stored stream."""
     o = np.asarray(stored, dtype=np.float64)
-    c, f, m = _norm(o, layer, eps)
+    c, f = _norm(o, layer, eps)
     if magnitude:
-        return (np.abs(o) + np.abs(m)) * f * np.abs(_vec(w_pre))
+        return _wide(o, layer) * f * np.abs(_vec(w_pre))
     return c * f * _vec(w_pre)
 
 
 def _through(grad, c, f, layer, magnitude, wide):
-    """The norm's transposed Jacobian times grad; wide: |a| + |mean| for magnitudes."""
+    """The norm's transposed Jacobian times grad; wide: _wide(a) for magnitudes."""
     if magnitude:
         grad = np.abs(grad)
         out = f * (grad + wide * f * (grad * wide * f).mean(axis=1, keepdims=True))
@@ -68,16 +74,16 @@ def resnorm_backward(stored, y, g, w_post, scale, w_pre, do, dn, layer, eps, mag
     t = np.zeros_like(o) if do is None else ab(np.asarray(do, dtype=np.float64))
     dw_pre = np.zeros(o.shape[1])
     if dn is not None:
-        c, f, m = _norm(o, layer, eps)
-        wide = np.abs(o) + np.abs(m)
+        c, f = _norm(o, layer, eps)
+        wide = _wide(o, layer)
         dn = np.asarray(dn, dtype=np.float64)
         t = t + _through(dn * _vec(w_pre), c, f, layer, magnitude, wide)
         dw_pre = (ab(dn) * (wide if magnitude else c) * f).sum(axis=(0, 2))
     if y is None:
         return t, None, None, None, None, dw_pre
     y = np.asarray(y, dtype=np.float64)
-    c, f, m = _norm(y, layer, eps)
-    wide = np.abs(y) + np.abs(m)
+    c, f = _norm(y, layer, eps)
+    wide = _wide(y, layer)
     yh = (wide if magnitude else c) * f
     if g is None:
         silu, dsilu = np.ones_like(o), np.zeros_like(o)

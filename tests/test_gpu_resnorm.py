@@ -23,6 +23,9 @@ SHAPES = [
     (1, 2050, 21, "f32", False, False), (1, 4096, 18, "bf16", False, False),
     (1, 4100, 9, "f16", True, False), (1, 8192, 11, "f32", False, False),
     (4, 24, 3000, "bf16", False, True),
+    # few channels: wide strips
+    (3, 9, 70000, "bf16", True, True), (4, 30, 33001, "f16", False, False),
+    (2, 61, 65600, "f32", True, False), (3, 33, 700, "f32", False, True),
     # strips as wide as they get where channels are looped over
     (5, 514, 6700, "f16", True, True), (4, 1030, 4100, "bf16", False, False),
 ]
