@@ -378,6 +378,24 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
   for (int k = t_lo; k < t_hi; ++k) {
     const int t = k * tile + at.t0;
     const int nv = clamp8(len - t);
+    if (!SHORT && k * tile >= len) {  // behind the row's end: the state stays, outputs are 0
+      if (AGG) break;
+      const int ns = clamp8(end - t);
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      store_n<T, 8>(static_cast<T*>(p.y) + (size_t)at.row * p.L + t, ns, zero);
+      if (CK >= 1 && at.gl == 0 && t < end)
+        p.bounds[(size_t)at.row * ((p.L + kChunk - 1) / kChunk) + t / kChunk] = carry;
+      if (CK == 2 && ns > 0) {
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+          *reinterpret_cast<uint2*>(p.q8[m] + (size_t)at.row * ckpt8_row(p.L) + t) =
+              make_uint2(0, 0);
+          if ((t & (kGroup - 1)) == 0)
+            p.e8[m][(size_t)at.row * ckpt8_groups(p.L) + t / kGroup] = (uint8_t)group_byte(0);
+        }
+      }
+      continue;
+    }
     const typename Source<T, false>::Tile now = next;
     if (k + 1 < t_hi) src.fetch(next, t + tile, clamp8(len - t - tile));
     float u[8], r[8], i[8], a[8], b[8];
@@ -460,6 +478,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_agg_kernel(Args p
   const T* dyp = static_cast<const T*>(p.dy) + (size_t)at.row * p.L;
   float carry = 0.f, Sseg = 0.f;
   for (int k = t_hi - 1; k >= t_lo; --k) {
+    if (k * tile >= len) continue;
     const int t = k * tile + at.t0;
     const int nv = clamp8(len - t);
     typename Source<T, Q8>::Tile now;
@@ -526,6 +545,14 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_kernel(Args p) {
     const Raw<T> g = next_g;
     const float bound = next_x;
     if (k > t_lo) fetch(k - 1);
+    if (!SHORT && k * tile >= len) {  // behind the row's end: nothing enters from there
+      const int ns = clamp8(end - t);
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      store_n<T, 8>(static_cast<T*>(p.du) + gbase + t, ns, zero);
+      store_n<T, 8>(static_cast<T*>(p.dr) + gbase + t, ns, zero);
+      store_n<T, 8>(static_cast<T*>(p.di) + gbase + t, ns, zero);
+      continue;
+    }
     float u[8], r[8], i[8], dy[8];
     now.u.get(u, nv, 0.f);
     now.r.get(r, nv, -__builtin_inff());
