@@ -645,18 +645,16 @@ def _opt_vec(t, name, numel, device):
 def _batch_stride(t, name):
     """Elements between the batch rows of t [B, H, L] (or [B, H]), whose H L
     elements are contiguous."""
-    inner = 1
-    for n in t.shape[1:]:
-        inner *= n
+    shape = t.shape
     if t.is_contiguous():
-        return inner
+        return shape[1] * shape[2] if len(shape) == 3 else shape[1]
     st = t.stride()
-    want = 1
-    for d in range(t.dim() - 1, 0, -1):
-        if t.shape[d] > 1 and st[d] != want:
+    inner = 1
+    for d in range(len(shape) - 1, 0, -1):
+        if st[d] != inner and shape[d] > 1:
             raise ValueError("%s must be contiguous within each batch row" % name)
-        want *= t.shape[d]
-    if t.shape[0] == 1:
+        inner *= shape[d]
+    if shape[0] == 1:
         return inner
     if st[0] < inner:
         raise ValueError("%s has overlapping batch rows" % name)
@@ -665,7 +663,9 @@ def _batch_stride(t, name):
 
 def _one_stride(a, b, c, names):
     s = _batch_stride(a, names[0])
-    if _batch_stride(b, names[1]) != s or _batch_stride(c, names[2]) != s:
+    st = a.stride()  # tensors of one shape and one set of strides are alike
+    if ((b.stride() != st and _batch_stride(b, names[1]) != s)
+            or (c.stride() != st and _batch_stride(c, names[2]) != s)):
         raise ValueError("%s, %s and %s must have the same batch stride" % names)
     return s
 
@@ -857,13 +857,14 @@ def gated_backward(dy, ckpt, kind, log_re, u=None, r=None, i=None, dx=None, lens
     for name, t in (("du", du), ("dr", dr), ("di", di)):
         out[name] = _new(dy, stream) if t is None else _like(t, name, dy, "dy")
     gsb = _one_stride(out["du"], out["dr"], out["di"], ("du", "dr", "di"))
-    out["dlog_re"] = _empty((H,), torch.float32, dev, stream)
+    lp = _vec(log_re, "log_re", H, dev)
+    out["dlog_re"] = (_new(log_re, stream) if log_re.dim() == 1
+                      else _empty((H,), torch.float32, dev, stream))
     out["dx0"] = _empty((B, H), torch.float32, dev, stream)
     sp = ctypes.byref(GatedShape(B, H, L, code))
     ws, nbytes = _buffer(_gated_bytes(B, H, L, code, None), workspace, "workspace", dev, stream)
     ckpt, _ = _buffer(_gated_bytes(B, H, L, code, kind), ckpt, "ckpt", dev, stream)
-    inp = GatedInputs(_ptr(u), _ptr(r), _ptr(i), sb, _vec(log_re, "log_re", H, dev),
-                      _lens_ptr(lens, B, dev))
+    inp = GatedInputs(_ptr(u), _ptr(r), _ptr(i), sb, lp, _lens_ptr(lens, B, dev))
     g = GatedGrads(out["du"].data_ptr(), out["dr"].data_ptr(), out["di"].data_ptr(), gsb,
                    out["dlog_re"].data_ptr(), out["dx0"].data_ptr())
     _launch(lib().dssm_gated_backward, dev, stream, ctypes.byref(inp), sp, kind, ckpt.data_ptr(),

@@ -333,6 +333,30 @@ def test_on_another_stream():
     assert torch.equal(y, ref)
 
 
+def test_two_streams_at_once():
+    """Calls under way on two streams, their workspaces the binding's own."""
+    torch = torch_()
+    sets = [prepared(2, 5, 9000, "f32", False, seed=52 + k) for k in range(2)]
+
+    def both(s, stream=None):
+        y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], bd.CKPT_INT8,
+                                        stream=stream)
+        g = bd.gated_backward(s["dy"], ckpt, bd.CKPT_INT8, s["log_re"], stream=stream)
+        return [y] + [g[k] for k in ("du", "dr", "di", "dlog_re", "dx0")]
+
+    ref = [both(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(8):
+        for k in range(2):
+            got[k].append(both(sets[k], streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for run in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(run, ref[k]))
+
+
 def test_binding_refuses():
     torch = torch_()
     s = prepared(2, 4, 64, "bf16", False, seed=61)
@@ -347,6 +371,13 @@ def test_binding_refuses():
                 torch.empty(2, 8, 64, dtype=r.dtype, device="cuda")[:, ::2]):
         with pytest.raises((ValueError, TypeError)):
             bd.gated_forward(u, bad, i, lr)
+    wide = torch.zeros(2, 12, 64, dtype=r.dtype, device="cuda")
+    with pytest.raises(ValueError):  # another batch stride than u's
+        bd.gated_forward(u, wide[:, :4], i, lr)
+    with pytest.raises(ValueError):
+        bd.gated_forward(wide[:, :4], wide[:, 4:8], i, lr)
+    with pytest.raises(ValueError):
+        bd.gated_forward(u.expand(2, 4, 64), r[:1].expand(2, 4, 64), i, lr)
     with pytest.raises(ValueError):
         bd.gated_forward(u, r, i, lr[:3].contiguous())
     with pytest.raises(TypeError):
@@ -369,3 +400,33 @@ def test_binding_refuses():
         bd.gated_backward(s["dy"], ckpt, bd.CKPT_INT8, lr, u=u, r=r, i=i)
     with pytest.raises(ValueError):
         bd.gated_step(u, r, i, lr, s["x0"])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last channels of a long bank against the same
+    channels alone (other segments: the same up to roundings), forward, 8 bits
+    and backward."""
+    torch = torch_()
+    H, L = 130, 1 << 24
+    say("case: B=1 H=%d L=%d bf16" % (H, L))
+    log_re = torch.full((H,), 0.2, device="cuda")
+    big = {k: torch.zeros(1, H, L, dtype=torch.bfloat16, device="cuda") for k in ("u", "r", "i", "dy")}
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for t in big.values():
+        t[0, -2:] = torch.randn(2, L, generator=gen, device="cuda").to(t.dtype)
+    small = {k: t[:, -2:].contiguous() for k, t in big.items()}
+    for kind in (bd.CKPT_STATE, bd.CKPT_INT8):
+        out = []
+        for s, lr in ((big, log_re), (small, log_re[-2:].contiguous())):
+            y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], lr, kind)
+            kept = dict(u=s["u"], r=s["r"], i=s["i"]) if kind == bd.CKPT_STATE else {}
+            g = bd.gated_backward(s["dy"], ckpt, kind, lr, **kept)
+            out.append([t[:, -2:].clone() for t in (y, g["du"], g["dr"], g["di"])])
+            del y, ckpt, g
+        for name, a, b in zip(("y", "du", "dr", "di"), *out):
+            # one rounding to bf16 may fall on either side: 2^-7 of the value, or of what
+            # float32 leaves of values of order 1
+            d = (a.float() - b.float()).abs()
+            worst = float((d / (2.0 ** -7 * b.float().abs() + 1e-5)).max())
+            say("  kind %d %-3s worst difference / bound %.3f" % (kind, name, worst))
+            assert worst <= 1.0, (kind, name, worst)

@@ -348,3 +348,36 @@ def test_block_trains_and_decodes():
         ot, nt = bd.resnorm_forward(xt, yt, gt, prm["w_post"], prm["scale"], prm["w_pre"])
         # float32 throughout, states over 90 steps: some 2^-14 of values of order 1
         assert (ot - o[..., t]).abs().max() < 2.0 ** -14 and (nt - n[..., t]).abs().max() < 2.0 ** -13
+
+
+def test_norm_offsets_past_32_bits():
+    """More than 2^31 elements: the last steps of a long call against the same
+    steps alone."""
+    torch = torch_()
+    H, L, n = 2100, 1 << 20, 96
+    say("case: B=1 H=%d L=%d bf16" % (H, L))
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    big = torch.zeros(1, H, L, dtype=torch.bfloat16, device="cuda")
+    big[..., -n:] = torch.randn(1, H, n, generator=gen, device="cuda").to(big.dtype)
+    w = torch.rand(H, generator=gen, device="cuda") + 0.5
+    small = big[..., -n:].contiguous()
+    end = lambda t: t[..., -n:].contiguous()
+    o, m, stats = bd.resnorm_forward_stats(big, big, None, w, w, w)
+    o2, _ = bd.resnorm_forward(small, small, None, w, w, w)
+    # the backward passes from the same values, so that only sums' orders differ
+    g = bd.resnorm_backward(o, big, None, stats, w, w, w, m, big)
+    g2 = bd.resnorm_backward(end(o), small, None, end(stats), w, w, w, end(m), small)
+    _, n1 = bd.resnorm_forward(big, None, None, None, None, w)
+    _, n2 = bd.resnorm_forward(small, None, None, None, None, w)
+    pairs = dict(o=(o, o2), n=(n1, n2), dx=(g["dx"], g2["dx"]), dy=(g["dy"], g2["dy"]))
+    for name, (a, b) in pairs.items():
+        d = (end(a).float() - b.float()).abs()
+        # one rounding to bf16 may fall on either side (2^-7 of the value), or of what float32
+        # leaves of terms of order 1 to 10
+        worst = float((d / (2.0 ** -7 * b.float().abs() + 1e-4)).max())
+        say("  %-3s worst difference / bound %.3f" % (name, worst))
+        assert worst <= 1.0, (name, worst)
+    x = big
+    y = bd.ckpt8_unpack(bd.ckpt8_pack(x), x.shape, x.dtype)
+    z = bd.ckpt8_unpack(bd.ckpt8_pack(x[0, -3:]), (3, L), x.dtype)
+    assert torch.equal(y[0, -3:], z)
