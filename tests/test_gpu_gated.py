@@ -20,6 +20,8 @@ SHAPES = [
     (3, 3, 513, "f32", True), (4, 5, 2047, "f16", True), (2, 3, 2048, "bf16", False),
     (2, 3, 2049, "f32", False), (3, 2, 6145, "f32", True), (1, 1, 20000, "f32", False),
     (4, 131, 2100, "bf16", True), (4, 2049, 530, "f16", True), (8, 1024, 1030, "f32", False),
+    # the most channels, many batch rows
+    (2, 65535, 3, "bf16", True), (40000, 3, 9, "f16", True),
     # many segments, and segments of several tiles
     (1, 2, 150000, "f32", False), (3, 85, 30000, "bf16", True),
 ]
@@ -184,7 +186,7 @@ def test_stream_in_parts_and_tokens(dtype):
 
 
 @pytest.mark.parametrize("B,H,dtype", [(1, 1, "f32"), (5, 63, "bf16"), (3, 1000, "f16"),
-                                       (64, 4096, "bf16"), (7, 2049, "f32")])
+                                       (64, 4096, "bf16"), (7, 2049, "f32"), (3, 65535, "f16")])
 def test_step(B, H, dtype):
     """One token: slices of a joint projection, idle streams, old states kept."""
     torch = torch_()

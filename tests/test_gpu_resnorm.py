@@ -23,6 +23,8 @@ SHAPES = [
     (1, 2050, 21, "f32", False, False), (1, 4096, 18, "bf16", False, False),
     (1, 4100, 9, "f16", True, False), (1, 8192, 11, "f32", False, False),
     (4, 24, 3000, "bf16", False, True),
+    # many batch rows of one and of few steps
+    (9000, 5, 1, "bf16", True, True), (5000, 40, 3, "f32", False, True),
     # few channels: wide strips
     (3, 9, 70000, "bf16", True, True), (4, 30, 33001, "f16", False, False),
     (2, 61, 65600, "f32", True, False), (3, 33, 700, "f32", False, True),
@@ -112,8 +114,13 @@ def test_one_token_is_a_sequence_of_one():
     s = prepared(6, 300, 1, "bf16", False, False, seed=2)
     args = (s["w_post"], s["scale"], s["w_pre"])
     o, n = bd.resnorm_forward(s["x"], s["y"], s["g"], *args)
-    o2, n2 = bd.resnorm_forward(s["x"][..., 0], s["y"][..., 0], s["g"][..., 0], *args)
+    flat = {k: s[k][..., 0] for k in ("x", "y", "g", "do", "dn")}
+    o2, n2, stats = bd.resnorm_forward_stats(flat["x"], flat["y"], flat["g"], *args)
     assert torch.equal(o[..., 0], o2) and torch.equal(n[..., 0], n2)
+    a = bd.resnorm_backward(o, s["y"], s["g"], stats, *args, s["do"], s["dn"])
+    b = bd.resnorm_backward(o2, flat["y"], flat["g"], stats, *args, flat["do"], flat["dn"])
+    for k in a:
+        assert torch.equal(a[k].reshape(b[k].shape), b[k]), k
 
 
 def test_bad_columns_stay_their_own():
