@@ -13,6 +13,8 @@
 //   dg  = t scale yh w_post silu'(g)
 //   dw_pre = sum dn oh,  dscale = sum t yh w_post silu(g),  dw_post = sum t scale silu(g) yh
 //   (the mean(P), mean(R) terms only for the layer norm; sums over b, t).
+// silu'(g) = s + silu(g) (1 - s), s = sigmoid(g), with 1 - s to full relative
+// precision: silu + s - silu s would lose the digits of 1 next to a large g.
 //
 // Layout: the normalised axis is the strided one.  A workgroup takes a strip
 // of LT VE steps (VE consecutive steps to a lane, LT lanes side by side) and
@@ -585,9 +587,10 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_kernel(Args p) {
         float silu = 1.f, dsilu = 0.f;
         if (p.g) {
           const float gk = gv[j][k];
-          const float sg = __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gk));
+          float rest;
+          const float sg = sigmoid_pair(gk, &rest);
           silu = gk * sg;
-          dsilu = fmaf(-silu, sg, silu + sg);  // sg (1 + g (1 - sg))
+          dsilu = fmaf(silu, rest, sg);
         }
         const float yh = LAYER ? fmaf(yv[j][k], ry[k], my[k]) : yv[j][k] * ry[k];
         const float ty = tv[k] * yh;
@@ -775,9 +778,10 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_wide_kernel(Args p) {
           float silu = 1.f, dsilu = 0.f;
           if (g) {
             const float gk = gv[u][k];
-            const float sg = __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gk));
+            float rest;
+            const float sg = sigmoid_pair(gk, &rest);
             silu = gk * sg;
-            dsilu = fmaf(-silu, sg, silu + sg);  // sg (1 + g (1 - sg))
+            dsilu = fmaf(silu, rest, sg);
           }
           const float yh = LAYER ? fmaf(yv[u][k], ry[k], my[k]) : yv[u][k] * ry[k];
           const float ty = tk * yh;

@@ -28,6 +28,8 @@ SHAPES = [
     # few channels: wide strips
     (3, 9, 70000, "bf16", True, True), (4, 30, 33001, "f16", False, False),
     (2, 61, 65600, "f32", True, False), (3, 33, 700, "f32", False, True),
+    # the most channels in strips as wide as they get, the most shared memory
+    (256, 8192, 2, "bf16", True, True),
     # strips as wide as they get where channels are looped over
     (5, 514, 6700, "f16", True, True), (4, 1030, 4100, "bf16", False, False),
 ]
@@ -169,6 +171,31 @@ def test_layer_norm_far_from_zero_and_with_outliers(H):
         a = [np64(o), np64(w[2]), True, EPS]
         close(n, oracle.resnorm_out(*a), oracle.resnorm_out(*a, magnitude=True), c_norm(H), "f32",
               "n")
+
+
+@pytest.mark.parametrize("H,L", [(40, 70), (1100, 30), (300, 1)])
+def test_large_gates(H, L):
+    """Gates open and shut far beyond exp's range: silu' is 1 and 0 there, not
+    what is left of the difference of two large numbers."""
+    torch = torch_()
+    s = prepared(2, H, L, "f32", False, False, seed=H)
+    sizes = torch.tensor([0.0, 17.3, -17.3, 60.1, -60.1, 1000.3, -1000.3, 3.0e6, 1e30, -1e30,
+                          torch.finfo(torch.float32).min], device="cuda")
+    s["g"].copy_(sizes[torch.randint(0, 11, s["g"].shape, device="cuda")])
+    s["do"] *= 2.0 ** -20  # times a gate of 1e30 it stays finite in float32
+    w = (s["w_post"], s["scale"] * 2.0 ** -20, s["w_pre"])
+    # a column's o is as large as its largest gate; of the gradients dg alone is looked at
+    o, _, stats = bd.resnorm_forward_stats(s["x"], s["y"], s["g"], w[0], w[1], None, eps=EPS)
+    got = bd.resnorm_backward(o, s["y"], s["g"], stats, w[0], w[1], None, s["do"], None)
+    a = [np64(t) for t in (s["x"], s["y"], s["g"]) + w[:2]] + [False, EPS]
+    # exp(-g) carries |g| log2(e) roundings of its exponent where it is not 0 or infinite
+    c = c_norm(H) + 100
+    with np.errstate(over="ignore"):
+        close(o, oracle.resnorm_stream(*a), oracle.resnorm_stream(*a, magnitude=True), c, "f32", "o")
+        a = [np64(t) for t in (o, s["y"], s["g"]) + w] + [np64(s["do"]), None, False, EPS]
+        ref, mag = (oracle.resnorm_backward(*a, magnitude=m) for m in (False, True))
+    assert torch.equal(got["dx"], s["do"])
+    close(got["dg"], ref[2], mag[2], 2 * c + 30, "f32", "dg")
 
 
 def test_no_steps():
