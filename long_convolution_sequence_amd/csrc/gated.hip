@@ -368,12 +368,23 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
   constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  if (AGG && at.seg == p.nseg - 1) {
+    // Nobody joins the last segment: its place keeps the state before the row,
+    // which every segment starts from and the last one may overwrite (xT = x0).
+    if (threadIdx.x == 0)
+      p.agg[at.row * p.nseg + at.seg] = make_float2(0.f, p.x0 ? p.x0[at.row] : 0.f);
+    return;
+  }
   const Source<T, false> src(p, at.row, at.b);
   typename Source<T, false>::Tile next;
   if (t_lo < t_hi) src.fetch(next, t_lo * tile + at.t0, clamp8(len - t_lo * tile - at.t0));
-  float carry = (p.x0 && !AGG) ? p.x0[at.row] : 0.f;
-  if (WPR > 1 && !AGG && p.nseg > 1)
-    carry = join_segments<false>(p.agg + at.row * p.nseg, p.nseg, at.seg, carry);
+  float carry = 0.f;
+  if (WPR > 1 && !AGG && p.nseg > 1) {
+    const float2* agg = p.agg + at.row * p.nseg;
+    carry = join_segments<false>(agg, p.nseg, at.seg, agg[p.nseg - 1].y);
+  } else if (!AGG && p.x0) {
+    carry = p.x0[at.row];
+  }
   float Sseg = 0.f;
   for (int k = t_lo; k < t_hi; ++k) {
     const int t = k * tile + at.t0;
@@ -474,6 +485,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_agg_kernel(Args p
   constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  if (at.seg == 0) return;  // nobody joins the first segment
   const Source<T, Q8> src(p, at.row, at.b);
   const T* dyp = static_cast<const T*>(p.dy) + (size_t)at.row * p.L;
   float carry = 0.f, Sseg = 0.f;

@@ -263,6 +263,20 @@ def test_extreme_gates_and_parameters():
             close(got[n], v, g + lost / (2 * c * STEP), 2 * c, "f32", n)
 
 
+@pytest.mark.parametrize("B,H,L", [(1, 2, 60000), (2, 100, 20000), (3, 5, 2100)])
+def test_streaming_in_place_over_split_rows(B, H, L):
+    """A state that is overwritten by the row's last segment is the one its
+    first segments started from."""
+    torch = torch_()
+    s = prepared(B, H, L, "bf16", False, seed=17)
+    s["log_re"].fill_(0.02)  # the state before the row is remembered to its end
+    xo = torch.empty_like(s["x0"])
+    y = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"], x=s["x0"], x_out=xo)
+    x = s["x0"].clone()
+    y2 = bd.gated_forward(s["u"], s["r"], s["i"], s["log_re"], x=x)
+    assert torch.equal(y, y2) and torch.equal(x, xo)
+
+
 def test_a_bad_row_stays_its_own():
     """NaN and Inf in one row's inputs leave every other row as it was."""
     torch = torch_()
