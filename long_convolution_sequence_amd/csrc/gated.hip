@@ -349,10 +349,11 @@ __device__ __forceinline__ float tile_carry(float2 (*tot)[WPR], int flip, int wa
   return in;
 }
 
-// log_re^2 log2(e), finite unless NaN: a shut gate times it has to be 0.
-__device__ __forceinline__ float kappa_of(float lr2) {
-  const float k = lr2 * kLog2e;
-  return k > 3.4e38f ? 3.4e38f : k;
+// log_re^2, finite with its product by log2(e) unless NaN: a shut gate's zero
+// times either has to be 0.
+__device__ __forceinline__ float square_of(float log_re) {
+  const float s = log_re * log_re;
+  return s > 0x1p126f ? 0x1p126f : s;
 }
 
 // Forward over a row (or one segment of it).  AGG: only the segment's pair.
@@ -364,7 +365,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
   const int len = at.live ? row_len(p, at.b) : 0;
   const int end = at.live ? p.L : 0;
   const float lr = p.log_re[at.row - at.b * p.H];
-  const float kappa = kappa_of(lr * lr);
+  const float kappa = square_of(lr) * kLog2e;
   constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_agg_kernel(Args p
   const Place<WPR, false> at(p);
   const int len = row_len(p, at.b);
   const float lr = p.log_re[at.row - at.b * p.H];
-  const float kappa = kappa_of(lr * lr);
+  const float kappa = square_of(lr) * kLog2e;
   constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
@@ -526,8 +527,8 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_kernel(Args p) {
   const int len = at.live ? row_len(p, at.b) : 0;
   const int end = at.live ? p.L : 0;
   const float lr = p.log_re[at.row - at.b * p.H];
-  const float lr2 = lr * lr;
-  const float kappa = kappa_of(lr2);
+  const float lr2 = square_of(lr);
+  const float kappa = lr2 * kLog2e;
   const size_t gbase = (size_t)(at.b * p.sdb + (at.row - at.b * p.H) * p.L);
   constexpr int tile = kChunk * WPR;
   const int ntile = (p.L + tile - 1) / tile;
@@ -698,7 +699,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const T* __restrict__ u
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     float rest;
-    const float e = kappa_of(lr[j] * lr[j]) * sigmoid_pair(rv[j], &rest);
+    const float e = square_of(lr[j]) * kLog2e * sigmoid_pair(rv[j], &rest);
     const float s = sigmoid_pair(iv[j], &rest);
     const float a = exp2_fast(-e);
     const float v =

@@ -263,6 +263,29 @@ def test_extreme_gates_and_parameters():
             close(got[n], v, g + lost / (2 * c * STEP), 2 * c, "f32", n)
 
 
+@pytest.mark.parametrize("L", [40, 700, 5000])
+def test_parameters_past_float32(L):
+    """log_re whose square float32 does not hold: no step remembers another, and
+    what is masked stays 0."""
+    torch = torch_()
+    B, H = 3, 3
+    s = prepared(B, H, L, "f32", True, seed=13)
+    s["log_re"][:] = torch.tensor([1e20, -3e38, float("inf")])
+    s["r"].clamp_(-5, 5)
+    y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], x=s["x0"],
+                                    x_out=torch.empty_like(s["x0"]), lens=s["lens"])
+    got = bd.gated_backward(s["dy"], ckpt, bd.CKPT_STATE, s["log_re"], u=s["u"], r=s["r"],
+                            i=s["i"], lens=s["lens"])
+    for b, n in enumerate(s["lens"].tolist()):
+        u, i, dy = (np64(s[k])[b, :, :n] for k in ("u", "i", "dy"))
+        sig = 1.0 / (1.0 + np.exp(-i))
+        close(y[b, :, :n], sig * u, np.abs(sig * u), c_gated(L), "f32", "y")
+        close(got["du"][b, :, :n], sig * dy, np.abs(sig * dy), 2 * c_gated(L), "f32", "du")
+        assert not got["dr"][b].any()
+        for t in (y, got["du"], got["di"]):
+            assert not t[b, :, n:].any()
+
+
 @pytest.mark.parametrize("B,H,L", [(1, 2, 60000), (2, 100, 20000), (3, 5, 2100)])
 def test_streaming_in_place_over_split_rows(B, H, L):
     """A state that is overwritten by the row's last segment is the one its
