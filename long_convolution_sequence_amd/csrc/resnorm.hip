@@ -291,6 +291,93 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
   }
 }
 
+// v summed over a row's NT threads, in the same order everywhere; buf: one
+// float per wave, of this sum alone (so one barrier does).
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
+  constexpr int W = NT / 64;
+  v = column_sum<1>(v);
+  if (W == 1) return v;
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return lanes_sum<W>(buf[threadIdx.x & (W - 1)]);
+}
+
+// Mean (layer norm) and factor of a row held 8 channels to a thread, m of them.
+template <bool LAYER, int NT>
+__device__ __forceinline__ void row_stats(const float* a, int m, float inv_h, float eps,
+                                          float (*buf)[NT / 64], float* mean, float* rstd) {
+  *mean = 0.f;
+  if (LAYER) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += a[k];  // 0 past the row's end
+    *mean = row_sum<NT>(s, buf[0]) * inv_h;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float d = k < m ? a[k] - *mean : 0.f;
+    s = fmaf(d, d, s);
+  }
+  *rstd = __builtin_amdgcn_rsqf(fmaf(row_sum<NT>(s, buf[1]), inv_h, eps));
+}
+
+// A single step: the channels are the contiguous axis, 8 of them to a thread.
+// A row to a workgroup of NT threads; rows of up to 512 channels to a wave each
+// (NT = 64), four to a workgroup.  What bounds it is latency: everything the
+// row needs, parameters too, is asked for before the first sum (a graph of 50
+// calls, bf16, us a call: 64 rows of 4096 channels 3.6, 1 row of 1024 2.8, with
+// the parameters asked for after the sums and channels side by side 6.8, 3.5).
+constexpr int token_rows(int NT) { return NT == 64 ? 4 : 1; }
+template <typename T, bool LAYER, int NT>
+__global__ __launch_bounds__(NT * token_rows(NT)) void resnorm_token_kernel(Args p) {
+  __shared__ float buf[4][NT / 64];
+  const int b = blockIdx.x * token_rows(NT) + threadIdx.y, h = threadIdx.x * 8;
+  if (b >= p.B) return;
+  const int m = min(max(p.H - h, 0), 8);
+  const bool live = !p.lens || p.lens[b] > 0;
+  const int nv = live ? m : 0;
+  const size_t at = (size_t)b * p.H + h;
+  const float inv_h = 1.f / (float)p.H;
+  float x[8], y[8], g[8], wp[8], sc[8], wn[8];
+  load_n<T, 8>(static_cast<const T*>(p.x) + at, nv, x);
+  if (p.y) {
+    load_n<T, 8>(static_cast<const T*>(p.y) + at, nv, y);
+    if (p.g) load_n<T, 8>(static_cast<const T*>(p.g) + ((size_t)(b * p.sg) + h), nv, g);
+    load_n<float, 8>(p.w_post + h, m, wp);
+    load_n<float, 8>(p.scale + h, m, sc);
+  }
+  if (p.n) load_n<float, 8>(p.w_pre + h, m, wn);
+  float mean, rstd;
+  if (p.y) {
+    row_stats<LAYER, NT>(y, m, inv_h, p.eps, buf, &mean, &rstd);
+    if (!live) rstd = 0.f;
+    if (p.stats && threadIdx.x == 0) {
+      if (LAYER) p.stats[b] = mean;
+      p.stats[(LAYER ? p.B : 0) + b] = rstd;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float silu = 1.f;
+      if (p.g) silu = g[k] * __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * g[k]));
+      x[k] = fmaf((y[k] - mean) * rstd * (wp[k] * sc[k]), silu, x[k]);
+      x[k] = k < m ? (float)(T)x[k] : 0.f;  // the second norm is of the stream as it is stored
+    }
+    store_n<T, 8>(static_cast<T*>(p.o) + at, m, x);
+  }
+  if (!p.n) return;
+  row_stats<LAYER, NT>(x, m, inv_h, p.eps, buf + 2, &mean, &rstd);
+  if (!live) rstd = 0.f;
+  if (p.stats && threadIdx.x == 0) {
+    if (LAYER) p.stats[2 * p.B + b] = mean;
+    p.stats[(LAYER ? 3 : 1) * p.B + b] = rstd;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = (x[k] - mean) * rstd * wn[k];
+  store_n<T, 8>(static_cast<T*>(p.n) + at, m, x);
+}
+
 // One strip of a workgroup that loops over its channels.
 template <typename T, int NT, int LT, int VE>
 struct WideStrip {
@@ -861,7 +948,8 @@ constexpr int kMaxGroups = 512;  // workgroups of the backward pass
 // Up to 128 channels and where channels are looped over, strips are as wide as
 // the registers allow and as leaves one for every compute unit (32 channels,
 // forward / backward: 79 / 178 us with 256 and 512 bytes, 115 / 275 with 128
-// and 256).  A single step takes its channels side by side.
+// and 256).  A single step has a kernel of its own forward; backward its
+// channels lie side by side.
 struct Form {
   int nt, lt, ve, kh;  // kh 0: looped
 };
@@ -875,7 +963,7 @@ Form spread(Form f, int B, int L, int least) {
 }
 
 Form fwd_form(int B, int H, int L, int dtype) {
-  if (L == 1) return H <= 1024 ? Form{256, 1, 1, 4} : Form{1024, 1, 1, 8};
+  if (L == 1) return {H <= 512 ? 64 : H <= 1024 ? 128 : H <= 4096 ? 512 : 1024, 1, 1, 8};
   const int ve = dtype == 0 ? 4 : 8;
   if (H > 512) return spread({1024, 16, ve, 0}, B, L, 2);
   if (H > 128) return {H <= 256 ? 512 : 1024, 8, ve, 4};
@@ -901,6 +989,13 @@ void fwd_held(const Args& a, hipStream_t st) {
                      st, a);
 }
 
+template <typename T, bool LAYER, int NT>
+void fwd_token(const Args& a, hipStream_t st) {
+  constexpr int R = token_rows(NT);
+  hipLaunchKernelGGL((resnorm_token_kernel<T, LAYER, NT>), dim3((unsigned)(a.B + R - 1) / R),
+                     dim3(NT, R), 0, st, a);
+}
+
 template <typename T, bool LAYER, int LT>
 void fwd_wide(const Args& a, hipStream_t st) {
   hipLaunchKernelGGL((resnorm_fwd_wide_kernel<T, LAYER, 1024, LT, 16 / (int)sizeof(T), 4>),
@@ -911,7 +1006,10 @@ template <typename T, bool LAYER>
 void fwd_run(const Args& a, const Form& f, hipStream_t st) {
   constexpr int VE = 16 / sizeof(T);
   if (a.L == 1)
-    f.nt == 256 ? fwd_held<T, LAYER, 256, 1, 1, 4>(a, st) : fwd_held<T, LAYER, 1024, 1, 1, 8>(a, st);
+    f.nt == 64    ? fwd_token<T, LAYER, 64>(a, st)
+    : f.nt == 128 ? fwd_token<T, LAYER, 128>(a, st)
+    : f.nt == 512 ? fwd_token<T, LAYER, 512>(a, st)
+                  : fwd_token<T, LAYER, 1024>(a, st);
   else if (f.kh)
     f.lt == 64    ? fwd_held<T, LAYER, 256, 64, VE, 4>(a, st)
     : f.lt == 32  ? fwd_held<T, LAYER, 256, 32, VE, 4>(a, st)

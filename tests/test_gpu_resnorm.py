@@ -23,6 +23,8 @@ SHAPES = [
     (1, 2050, 21, "f32", False, False), (1, 4096, 18, "bf16", False, False),
     (1, 4100, 9, "f16", True, False), (1, 8192, 11, "f32", False, False),
     (4, 24, 3000, "bf16", False, True),
+    # single steps: a wave's channels, and just past a wave's and a workgroup's
+    (5, 512, 1, "f32", True, True), (3, 700, 1, "f16", True, True), (2, 4097, 1, "bf16", True, False),
     # many batch rows of one and of few steps
     (9000, 5, 1, "bf16", True, True), (5000, 40, 3, "f32", False, True),
     # few channels: wide strips
