@@ -835,6 +835,9 @@ def gated_backward(dy, ckpt, kind, log_re, u=None, r=None, i=None, dx=None, lens
     Returns a dict du, dr, di [B,H,L], dlog_re [H] f32, dx0 [B,H] f32 (du, dr,
     di given: slices of one [B,3H,L] buffer are written as they are)."""
     torch = _torch()
+    # _buffer() below makes a buffer that is not given: this one is read
+    if not isinstance(ckpt, torch.Tensor):
+        raise TypeError("ckpt must be a torch tensor")
     code = _dtype_code(dy, "dy")
     if dy.dim() != 3:
         raise ValueError("dy must be [B, H, L]")

@@ -238,3 +238,16 @@ def test_resnorm_backward_refuses():
     assert size(L.dssm_resnorm_workspace_size, ctypes.byref(rshape(B=0))) == (0, 0)
     rc, n = size(L.dssm_resnorm_workspace_size, ctypes.byref(rshape()))
     assert rc == 0 and n >= 3 * 3 * 4 and n % 256 == 0
+
+
+def test_binding_needs_a_checkpoint():
+    """A backward pass reads what a forward pass kept: None is refused, and no
+    buffer made in its place (host side; nothing is launched)."""
+    import torch
+    dy = torch.zeros(1, 2, 3)
+    for kind in (bd.CKPT_STATE, bd.CKPT_INT8):
+        for ckpt in (None, 1 << 20):
+            with pytest.raises(TypeError, match="ckpt"):
+                bd.gated_backward(dy, ckpt, kind, torch.ones(2), u=dy, r=dy, i=dy)
+    with pytest.raises(ValueError, match="blob"):
+        bd.ckpt8_unpack(None, (2, 3), torch.float32)
