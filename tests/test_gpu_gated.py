@@ -469,3 +469,44 @@ def test_offsets_past_32_bits():
             worst = float((d / (2.0 ** -7 * b.float().abs() + 1e-5)).max())
             say("  kind %d %-3s worst difference / bound %.3f" % (kind, name, worst))
             assert worst <= 1.0, (kind, name, worst)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("B,H,L", [(1, 64, 1), (1, 64, 300), (1, 64, 600), (2, 200, 2100), (2, 4096, 600)])
+def test_drive_of_one_open_step(B, H, L, dtype):
+    """One open step among shut ones leaves sqrt(1 - a^2) sigmoid(i) u in the state
+    to float32's digits, whatever the activations' type.
+
+    In half steps h = 2^-24, x = 2 log_re^2 sigmoid(r): the exponent's two products
+    and its constant 3 h; the series of 1 - exp(-x) another 5 h (its first
+    coefficient, its last sum and product, h for the terms before, h for the one
+    left out); the root halves these 8 h and adds 2 h of its own; sigmoid(0) = 1/2,
+    u = 1 and the shut steps are exact.  6 h in all, and one for products of them."""
+    torch = torch_()
+    say("case: B=%d H=%d L=%d %s" % (B, H, L, dtype))
+    dt = dtype_of(dtype)
+    x = torch.linspace(0.02, 0.49, H, dtype=torch.float64)
+    log_re = x.sqrt().float()
+    ref = (0.5 * torch.sqrt(-torch.expm1(-log_re.double() ** 2))).expand(B, H).numpy()
+    u, i = torch.ones(B, H, L, device="cuda").to(dt), torch.zeros(B, H, L, device="cuda").to(dt)
+    r = torch.full((B, H, L), float("-inf"), device="cuda").to(dt)
+    r[..., L // 3] = 0.0
+
+    def near(got, what):
+        worst = float(np.max(np.abs(np64(got) - ref) / (7 * 2.0 ** -24 * ref)))
+        say("  %-6s worst error / tolerance %.3f" % (what, worst))
+        assert worst <= 1.0, (what, worst)
+
+    end = torch.empty(B, H, device="cuda")
+    lr = log_re.cuda()
+    y, ckpt = bd.gated_forward_ckpt(u, r, i, lr, x_out=end)
+    near(end, "state")
+    for c in range(1, -(-L // 512)):
+        if c * 512 > L // 3:
+            near(ckpt[:4 * B * H * -(-L // 512)].view(torch.float32).view(B, H, -1)[..., c], "kept")
+    if dtype == "f32":
+        near(y[..., -1], "y")
+    if L == 1:
+        state = torch.zeros(B, H, device="cuda")
+        bd.gated_step(u[..., 0], r[..., 0], i[..., 0], lr, state)
+        near(state, "token")
