@@ -447,9 +447,13 @@ int dssm_gated_workspace_size(const dssm_gated_shape* s, size_t* bytes);
  * padded to 256 bytes: the states [B, H, ceil(L / 512)] float32 entering the
  * chunks, then for DSSM_CKPT_INT8 u, r and i, each as dssm_ckpt8_pack writes
  * B H rows of L, but the gates' logits r and i only up to +-31.75 (infinities
- * and a mask's lowest value too: the sigmoid is 0 or 1 to 2^-45 there, and
- * they would cost the rest of their group its scale).  Steps that are not live
- * are 0. */
+ * and a mask's lowest value too: they would cost the rest of their group its
+ * scale).  The sigmoid is 0 or 1 to 2^-45 there, but a step's drive goes with
+ * sqrt(1 - a^2) ~ |log_re| sqrt(2 sigmoid(r)): from 8 bits a step that r alone
+ * shuts is driven by up to 2^-22 |log_re| sigmoid(i) u, and its u, r and i have
+ * the gradients of that, where the forward pass and DSSM_CKPT_STATE have 0
+ * (shut by i too, the drive is below 2^-67 |log_re u|).  Steps that are not
+ * live are 0. */
 int dssm_gated_ckpt_size(const dssm_gated_shape* s, int kind, size_t* bytes);
 
 /* The gated linear recurrence: for every (b, h) a real mode whose decay and

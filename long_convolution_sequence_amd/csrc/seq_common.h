@@ -195,7 +195,8 @@ constexpr int last_byte<_Float16>() { return 16 - 6 + 127; }
 
 // What a gate's logit may reach in 8 bits, 127 / 4: a sigmoid is 0 or 1 to
 // 2^-45 there, and a step that is masked by an infinite or the lowest logit
-// costs its neighbours no more of their scale.
+// costs its neighbours no more of their scale.  A step shut by r alone keeps
+// sqrt(2 sigmoid(-31.75)) < 2^-22 of its drive.
 constexpr float kGateMax = 31.75f;
 
 // Eight steps of one lane, of type T, in 8 bits; the lanes of a group are

@@ -510,3 +510,48 @@ def test_drive_of_one_open_step(B, H, L, dtype):
         state = torch.zeros(B, H, device="cuda")
         bd.gated_step(u[..., 0], r[..., 0], i[..., 0], lr, state)
         near(state, "token")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mask", [float("-inf"), None])
+def test_steps_shut_by_the_recurrence_gate_alone(mask, dtype):
+    """With i open and u large, a row shut by r keeps its state and, from kept
+    states, has no gradient but dx0; from 8 bits its drive is at most 2^-22
+    |log_re| sigmoid(i) u (r counts as -31.75, sqrt(2 sigmoid(-31.75)) = 2^-22.4:
+    the factor 2^0.4 holds all roundings, the type's among them), and so are the
+    gradients: with G = dx, du = G drive / u, di = G drive (1 - sigmoid(i)),
+    dr = G drive / 2, dlog_re = sum G drive / log_re."""
+    torch = torch_()
+    B, H, L = 2, 5, 700
+    s = prepared(B, H, L, dtype, False, seed=73)
+    s["dy"].zero_()
+    s["r"].fill_(torch.finfo(s["r"].dtype).min if mask is None else mask)
+    s["u"].mul_(1000.0)
+    G = np.abs(np64(s["dx"]))[..., None]
+    u, i, lr = np.abs(np64(s["u"])), np64(s["i"]), np.abs(np64(s["log_re"]))[None, :, None]
+    # u and i as 8 bits hold them: at most half a unit of their group's largest more
+    u = u + np.abs(u).max() / 127
+    sig = 1.0 / (1.0 + np.exp(-(i + np.abs(i).max() / 127)))
+    drive = 2.0 ** -22 * lr * sig * u
+    for kind in ("state", "int8"):
+        k = KINDS[kind]
+        y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], k, x=s["x0"],
+                                        x_out=torch.empty_like(s["x0"]))
+        assert torch.equal(y, s["x0"][..., None].to(y.dtype).expand(B, H, L))
+        kept = dict(u=s["u"], r=s["r"], i=s["i"]) if kind == "state" else {}
+        got = bd.gated_backward(s["dy"], ckpt, k, s["log_re"], dx=s["dx"], **kept)
+        if kind == "state":
+            assert torch.equal(got["dx0"], s["dx"])
+            assert not any(got[n].any() for n in ("du", "dr", "di", "dlog_re"))
+            continue
+        assert np.allclose(np64(got["dx0"]), np64(s["dx"]), rtol=2.0 ** -20, atol=0)
+        bounds = dict(du=G * drive / u, di=G * drive, dr=G * (drive / 2 + lr * lr * 2.0 ** -45 *
+                                                              np.abs(np64(y)).max()))
+        for n, b in bounds.items():
+            worst = float((np.abs(np64(got[n])) / b).max())
+            say("  %-7s largest / bound %.3f" % (n, worst))
+            assert worst <= 1.0, (n, worst)
+        b = (G * (drive / lr + 2 * lr * 2.0 ** -45 * np.abs(np64(y)).max())).sum(axis=(0, 2))
+        worst = float((np.abs(np64(got["dlog_re"])) / b).max())
+        say("  dlog_re largest / bound %.3f" % worst)
+        assert worst <= 1.0, worst
