@@ -555,3 +555,48 @@ def test_steps_shut_by_the_recurrence_gate_alone(mask, dtype):
         worst = float((np.abs(np64(got["dlog_re"])) / b).max())
         say("  dlog_re largest / bound %.3f" % worst)
         assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("kind,dtype", [("state", "f32"), ("int8", "bf16")])
+@pytest.mark.parametrize("tiles,rest", [(255, 77), (256, 5), (511, 900)])
+def test_many_segments_remember_each_other(tiles, rest, kind, dtype):
+    """A few rows of just over 255, 256 and 511 tiles of 2048 steps: 256 segments of
+    one tile, 129 and 256 of two.  Each channel is driven in one tile alone (the
+    last one by the state before the row) and read back in another, and forgets
+    nearly nothing in between, so what every segment passes on is seen by itself
+    at the far end, in either direction."""
+    torch = torch_()
+    B, H, L = 1, 8, tiles * 2048 + rest
+    s = prepared(B, H, L, dtype, False, seed=75)
+    first = [0, 1, 3, 75, 76, 128, 254, None]
+    far = [tiles, tiles, 200, 254, 0, 2, 1, tiles]
+    driven = torch.zeros(B, H, L, dtype=torch.bool, device="cuda")
+    asked = torch.zeros_like(driven)
+    for h in range(H):
+        if first[h] is not None:
+            driven[:, h, first[h] * 2048:(first[h] + 1) * 2048] = True
+        asked[:, h, far[h] * 2048:(far[h] + 1) * 2048] = True
+    # one sign each, so that a sum is as large as its terms
+    s["u"] = s["u"].abs() * driven
+    s["dy"] = s["dy"].abs() * asked
+    s["x0"] = s["x0"].abs() * torch.tensor([0.0] * 7 + [1.0], device="cuda")
+    s["dx"] = s["dx"].abs() * torch.tensor([1.0] + [0.0] * 7, device="cuda")
+    s["log_re"] = torch.full((H,), 1e-3, device="cuda") * torch.tensor([1.0, -1.0] * 4, device="cuda")
+    k = KINDS[kind]
+    end = torch.empty_like(s["x0"])
+    y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], k, x=s["x0"], x_out=end)
+    ref, last = reference(s)
+    mag, mlast = reference(s, magnitude=True)
+    close(y, ref, mag, c_gated(L), dtype, "y")
+    close(end, last, mlast, c_gated(L), "f32", "state")
+    kept = dict(u=s["u"], r=s["r"], i=s["i"]) if kind == "state" else {}
+    got = bd.gated_backward(s["dy"], ckpt, k, s["log_re"], dx=s["dx"], **kept)
+    u, r, i = (np64(s[n]) for n in ("u", "r", "i"))
+    if kind == "int8":
+        u, r, i = oracle.ckpt8(u), oracle.ckpt8(gate8(r)), oracle.ckpt8(gate8(i))
+    nch = -(-L // 512)
+    starts = np64(ckpt[:4 * B * H * nch].view(torch.float32).view(B, H, nch))
+    args = (u, r, i, np64(s["log_re"]), np64(s["dy"]), np64(s["dx"]), np64(s["x0"]), None, starts)
+    ref, mag = oracle.gated_backward(*args), oracle.gated_backward(*args, magnitude=True)
+    for n, v, m in zip(("du", "dr", "di", "dlog_re", "dx0"), ref, mag):
+        close(got[n], v, m, 2 * c_gated(L), "f32" if n in ("dlog_re", "dx0") else dtype, n)
