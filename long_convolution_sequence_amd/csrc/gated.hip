@@ -141,33 +141,29 @@ __device__ __forceinline__ void tile_scan(float& S, float& V, int gl, int n, flo
 }
 
 // What enters segment `seg` of a split row: the pairs of the segments before
-// it (REV: after it) applied to `start`, four neighbours to a lane and all of a
-// round asked for at once.  Every lane of the wave gets it.
-constexpr int kJoin = 256;  // segments of a round
+// it (REV: after it) applied to `start`, four neighbours to a lane and all
+// asked for at once.  Every lane of the wave gets it.
+constexpr int kJoin = 256;  // segments of a row at most (64 lanes, four each)
 template <bool REV>
 __device__ float join_segments(const float2* agg, int nseg, int seg, float start) {
   const int lane = threadIdx.x & 63;
   const int count = REV ? nseg - 1 - seg : seg;
-  float c = start;
-  for (int base = 0; base < count; base += kJoin) {
-    // lane order = order of application
-    float2 t[4];
+  // lane order = order of application
+  float2 t[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = base + 4 * lane + k;
-      t[k] = make_float2(0.f, 0.f);
-      if (j < count) t[k] = agg[REV ? nseg - 1 - j : j];
-    }
-    float S = 0.f, V = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      V = fmaf(exp2_fast(-t[k].x), V, t[k].y);
-      S += t[k].x;
-    }
-    wave_scan<false>(S, V);
-    c = fmaf(exp2_fast(-lane_of(S, 63)), c, lane_of(V, 63));
+  for (int k = 0; k < 4; ++k) {
+    const int j = 4 * lane + k;
+    t[k] = make_float2(0.f, 0.f);
+    if (j < count) t[k] = agg[REV ? nseg - 1 - j : j];
   }
-  return c;
+  float S = 0.f, V = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    V = fmaf(exp2_fast(-t[k].x), V, t[k].y);
+    S += t[k].x;
+  }
+  wave_scan<false>(S, V);
+  return fmaf(exp2_fast(-lane_of(S, 63)), start, lane_of(V, 63));
 }
 
 struct Args {
@@ -720,8 +716,8 @@ struct Plan {
 // 244 against 113 / 200).
 //
 // Few rows leave compute units idle: they are cut into segments, about 2048
-// workgroups in all and no more to a row than one round joins, at the price of reading the inputs (backward: the
-// recurrence gate and dy) twice (bf16, 2^25 elements, forward / backward: 64
+// workgroups in all and no more to a row than a wave joins at once, at the price
+// of reading the inputs (backward: the recurrence gate and dy) twice (bf16, 2^25 elements, forward / backward: 64
 // rows 90 / 109 us against 274 / 403 unsplit, with 1024 workgroups 92 / 114;
 // 256 rows 91 / 111 against 76 / 121; 512 rows 88 / 108 against 55 / 103).
 Plan plan_of(long rows, int L, bool backward) {

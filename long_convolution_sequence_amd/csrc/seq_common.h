@@ -91,9 +91,8 @@ struct Packed {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int k = 0; k < N; ++k) w[k] = __float_as_uint(x[k]);
-    } else if constexpr (N == 1) {
-      w[0] = bits((T)x[0]);
     } else {
+      static_assert(N % 2 == 0, "16-bit elements are rounded in pairs");
       typedef T two __attribute__((ext_vector_type(2)));
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) {
@@ -103,14 +102,11 @@ struct Packed {
     }
   }
   __device__ __forceinline__ void store(T* p, int n) const {
+    static_assert(N * sizeof(T) >= 4, "whole words");
     if (n >= N) {
       typename VecOf<T, N>::type v;
-      if constexpr (N * sizeof(T) >= 4) {
-        __builtin_memcpy(&v, w, sizeof(w));
-        *reinterpret_cast<typename VecOf<T, N>::type*>(p) = v;
-      } else {
-        p[0] = __builtin_bit_cast(T, (uint16_t)w[0]);
-      }
+      __builtin_memcpy(&v, w, sizeof(w));
+      *reinterpret_cast<typename VecOf<T, N>::type*>(p) = v;
     } else {
 #pragma unroll
       for (int k = 0; k < N; ++k)
