@@ -130,6 +130,15 @@ __device__ __forceinline__ void strip_sum(float (*v)[VE], float* buf) {
     }
 }
 
+// Steps at or past nv are 0, whatever the parameters: of an infinite one the
+// zeros read there would make NaN.  Whole strips (the workgroup's) skip it.
+template <int VE>
+__device__ __forceinline__ void live_only(float* v, int nv, bool whole) {
+  if (whole) return;
+#pragma unroll
+  for (int k = 0; k < VE; ++k) v[k] = k < nv ? v[k] : 0.f;
+}
+
 // Strips to workgroups: each of the 8 dies takes a run of neighbouring strips,
 // which share the ends of their 128-byte lines in its cache (workgroups go to
 // the dies in turn).  `per` strips to a die; the last dies' numbers run past n.
@@ -263,9 +272,9 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
         if (p.g)
           silu = gv[j][k] * __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * gv[j][k]));
         const float v = (a[j][k] - mean[0][k]) * rstd[0][k];
-        // behind a row's end everything read is 0, and so is the factor
         out[k] = fmaf(v * c, silu, xv[j][k]);
       }
+      live_only<VE>(out, nv, whole);
       a[j].set(out);
       if (in) a[j].store(rows.at(static_cast<T*>(p.o) + base, j), ns);
     }
@@ -287,6 +296,7 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_kernel(Args p) {
     float out[VE];
 #pragma unroll
     for (int k = 0; k < VE; ++k) out[k] = (a[j][k] - mean[0][k]) * rstd[0][k] * w;
+    live_only<VE>(out, nv, whole);
     store_n<T, VE>(rows.at(static_cast<T*>(p.n) + base, j), ns, out);
   }
 }
@@ -362,7 +372,7 @@ __global__ __launch_bounds__(NT * token_rows(NT)) void resnorm_token_kernel(Args
       float silu = 1.f;
       if (p.g) silu = g[k] * __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * g[k]));
       x[k] = fmaf((y[k] - mean) * rstd * (wp[k] * sc[k]), silu, x[k]);
-      x[k] = k < m ? (float)(T)x[k] : 0.f;  // the second norm is of the stream as it is stored
+      x[k] = k < nv ? (float)(T)x[k] : 0.f;  // the second norm is of the stream as it is stored
     }
     store_n<T, 8>(static_cast<T*>(p.o) + at, m, x);
   }
@@ -374,7 +384,7 @@ __global__ __launch_bounds__(NT * token_rows(NT)) void resnorm_token_kernel(Args
     p.stats[(LAYER ? 3 : 1) * p.B + b] = rstd;
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = (x[k] - mean) * rstd * wn[k];
+  for (int k = 0; k < 8; ++k) x[k] = live ? (x[k] - mean) * rstd * wn[k] : 0.f;
   store_n<T, 8>(static_cast<T*>(p.n) + at, m, x);
 }
 
@@ -533,6 +543,7 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_wide_kernel(Args p) {
           const float v = (yv[u][k] - mean[k]) * rstd[k];
           out[k] = fmaf(v * c, silu, xv[u][k]);
         }
+        live_only<VE>(out, nv, at.whole);
         Vec ov;
         ov.set(out);
         if (in) ov.store(at.spot(o, j0 + u), ns);
@@ -560,6 +571,7 @@ __global__ __launch_bounds__(NT) void resnorm_fwd_wide_kernel(Args p) {
       float out[VE];
 #pragma unroll
       for (int k = 0; k < VE; ++k) out[k] = (v[u][k] - mean[k]) * rstd[k] * c;
+      live_only<VE>(out, nv, at.whole);
       store_n<T, VE>(at.spot(n, j0 + u), ns, out);
     }
   }
@@ -665,6 +677,7 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_kernel(Args p) {
         tv[k] = fmaf(c1[k], oh, tv[k]);
         if (LAYER) tv[k] += c0[k];
       }
+      live_only<VE>(tv, nv, whole);
       if (in) store_n<T, VE>(rows.at(static_cast<T*>(p.dx) + base, j), ns, tv);
       if (!p.y) continue;
       const float c = in ? p.w_post[h] * p.scale[h] : 0.f;
@@ -688,6 +701,7 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_kernel(Args p) {
         if (LAYER) r[N - 1][k] += R[j][k];
         dgv[k] = ty * dsilu * c;
       }
+      live_only<VE>(dgv, nv, whole);
       if (in && p.dg)
         store_n<T, VE>(rows.at(static_cast<T*>(p.dg) + (size_t)(b * p.sdg) + t0, j), ns, dgv);
     }
@@ -711,6 +725,7 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_kernel(Args p) {
         out[k] = fmaf(c1[k], yh, R[j][k] * ry[k]);
         if (LAYER) out[k] += c0[k];
       }
+      live_only<VE>(out, nv, whole);
       store_n<T, VE>(rows.at(static_cast<T*>(p.dy) + base, j), ns, out);
     }
   }
@@ -862,6 +877,7 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_wide_kernel(Args p) {
           float tk = fmaf(nn[u][k], w * ro[k], dv[u][k]);
           tk = fmaf(c1[k], oh, tk);
           if (LAYER) tk += c0[k];
+          if (!at.whole) tk = k < at.nv ? tk : 0.f;  // the parameters' sums take it too
           float silu = 1.f, dsilu = 0.f;
           if (g) {
             const float gk = gv[u][k];
@@ -878,6 +894,8 @@ __global__ __launch_bounds__(NT) void resnorm_bwd_wide_kernel(Args p) {
           if (LAYER) dyv[k] += d0[k];
           tv[k] = tk;
         }
+        live_only<VE>(dyv, at.nv, at.whole);
+        live_only<VE>(dgv, at.nv, at.whole);
         if (in) {
           store_n<T, VE>(at.spot(dx, j0 + u), ns, tv);
           if (y) store_n<T, VE>(at.spot(dy, j0 + u), ns, dyv);
@@ -928,8 +946,9 @@ __global__ __launch_bounds__(1024) void resnorm_sum_kernel(const float* __restri
     if (k >= H) {
       if (dw_pre) dw_pre[k - H] = (float)v;
     } else {
-      if (dw_post) dw_post[k] = (float)(G ? v * (double)scale[k] : 0.0);
-      if (dscale) dscale[k] = (float)(G ? v * (double)w_post[k] : 0.0);
+      // nothing to add up is 0, whatever the parameter
+      if (dw_post) dw_post[k] = (float)(v != 0.0 ? v * (double)scale[k] : 0.0);
+      if (dscale) dscale[k] = (float)(v != 0.0 ? v * (double)w_post[k] : 0.0);
     }
   }
 }

@@ -417,3 +417,34 @@ def test_norm_offsets_past_32_bits():
     y = bd.ckpt8_unpack(bd.ckpt8_pack(x), x.shape, x.dtype)
     z = bd.ckpt8_unpack(bd.ckpt8_pack(x[0, -3:]), (3, L), x.dtype)
     assert torch.equal(y[0, -3:], z)
+
+
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("H,L", [(40, 70), (300, 70), (600, 70), (1100, 70), (40, 1), (300, 1),
+                                 (1100, 1), (5000, 1)])
+def test_steps_behind_a_row_stay_zero_with_any_parameters(H, L, layer):
+    """Infinite and NaN parameters, and finite ones whose product is past float32:
+    outputs and gradients behind the rows' ends are 0 all the same, and without a
+    live step the parameters' gradients too."""
+    torch = torch_()
+    s = prepared(3, H, L, "f32", layer, True, seed=H + L)
+    s["w_post"][1], s["scale"][1] = 1e30, 1e30
+    s["scale"][2], s["w_post"][3] = float("nan"), float("-inf")
+    s["w_pre"][4], s["w_pre"][-1] = float("inf"), float("nan")
+    w = (s["w_post"], s["scale"], s["w_pre"])
+    norm = norm_of(layer)
+    for lens in (s["lens"], torch.zeros_like(s["lens"])):
+        for gate in (s["g"], None):
+            o, n, stats = bd.resnorm_forward_stats(s["x"], s["y"], gate, *w, norm=norm, lens=lens)
+            got = bd.resnorm_backward(o, s["y"], gate, stats, *w, s["do"], s["dn"], norm=norm,
+                                      lens=lens)
+            got.update(o=o, n=n)
+            for k, t in got.items():
+                if t is None:
+                    continue
+                if t.dim() == 1:
+                    live = lens.max() > 0
+                    assert live or not t.any(), k
+                else:
+                    for b, m in enumerate(lens.tolist()):
+                        assert not t[b, :, m:].any(), (k, b, m)
