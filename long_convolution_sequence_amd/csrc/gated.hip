@@ -377,6 +377,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
   } else if (!AGG && p.x0) {
     carry = p.x0[at.row];
   }
+  const float start = carry;
   float Sseg = 0.f;
   for (int k = t_lo; k < t_hi; ++k) {
     const int t = k * tile + at.t0;
@@ -455,7 +456,10 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_fwd_kernel(Args p) {
       for (int j = 0; j < 8; ++j) y[j] = j < nv ? y[j] : 0.f;
     }
     store_n<T, 8>(static_cast<T*>(p.y) + (size_t)at.row * p.L + t, ns, y);
-    if (SHORT) carry = __shfl(h, at.lane | (at.n - 1));  // the last lane's state is the row's
+    if (SHORT) {  // the last lane's state is the row's; an empty row keeps its own
+      const float last = __shfl(h, at.lane | (at.n - 1));
+      carry = len > 0 ? last : start;
+    }
   }
   if (!at.live) return;
   if (AGG) {
@@ -541,6 +545,7 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_kernel(Args p) {
   float carry = p.dx ? p.dx[at.row] : 0.f;
   if (WPR > 1 && p.nseg > 1)
     carry = join_segments<true>(p.agg + at.row * p.nseg, p.nseg, at.seg, carry);
+  const float start = carry;
   double acc = 0.0;
   for (int k = t_hi - 1; k >= t_lo; --k) {
     const int t = k * tile + at.t0;
@@ -624,12 +629,19 @@ __global__ __launch_bounds__(threads_of<WPR>()) void gated_bwd_kernel(Args p) {
       sum += r[j];
       r[j] *= qn[j] * lr2;
     }
+    if (nv < 8) {  // with a parameter that is NaN too
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = j < nv ? r[j] : 0.f;
+    }
     acc += (double)sum;
     const int ns = clamp8(end - t);
     store_n<T, 8>(static_cast<T*>(p.du) + gbase + t, ns, u);
     store_n<T, 8>(static_cast<T*>(p.dr) + gbase + t, ns, r);
     store_n<T, 8>(static_cast<T*>(p.di) + gbase + t, ns, i);
-    if (SHORT) carry = __shfl(c, at.lane & ~(at.n - 1));
+    if (SHORT) {
+      const float first = __shfl(c, at.lane & ~(at.n - 1));
+      carry = len > 0 ? first : start;
+    }
   }
   if (p.dx0 && at.live && at.gl == 0 && (WPR == 1 || (threadIdx.x == 0 && at.seg == 0)))
     p.dx0[at.row] = carry;
@@ -661,7 +673,9 @@ __global__ __launch_bounds__(256) void gated_dlog_kernel(const double* __restric
     s += part[(b * H + h) * nseg + (j - b * nseg)];
   }
   for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-  if ((threadIdx.x & 63) == 0) dlog_re[h] = (float)(2.0 * (double)log_re[h] * s);
+  // nothing to add up is 0, whatever the parameter
+  if ((threadIdx.x & 63) == 0)
+    dlog_re[h] = (float)(s != 0.0 ? 2.0 * (double)log_re[h] * s : 0.0);
 }
 
 // One token for every (b, h); V neighbouring channels to a thread.

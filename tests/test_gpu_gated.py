@@ -600,3 +600,29 @@ def test_many_segments_remember_each_other(tiles, rest, kind, dtype):
     ref, mag = oracle.gated_backward(*args), oracle.gated_backward(*args, magnitude=True)
     for n, v, m in zip(("du", "dr", "di", "dlog_re", "dx0"), ref, mag):
         close(got[n], v, m, 2 * c_gated(L), "f32" if n in ("dlog_re", "dx0") else dtype, n)
+
+
+@pytest.mark.parametrize("L", [1, 5, 40, 300, 700, 2100, 9000])
+def test_empty_rows_with_any_parameters(L):
+    """An empty row passes its state and its state's gradient through and has no
+    other, whatever its channels' parameters; without a live step the parameters'
+    gradients are 0."""
+    torch = torch_()
+    B, H = 3, 3
+    s = prepared(B, H, L, "f32", False, seed=77)
+    s["log_re"][:] = torch.tensor([float("nan"), float("inf"), 0.3])
+    for lens in ([L, 0, 0], [0, 0, 0]):
+        lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        for kind, k in KINDS.items():
+            end = torch.empty_like(s["x0"])
+            y, ckpt = bd.gated_forward_ckpt(s["u"], s["r"], s["i"], s["log_re"], k, x=s["x0"],
+                                            x_out=end, lens=lens)
+            kept = dict(u=s["u"], r=s["r"], i=s["i"]) if kind == "state" else {}
+            got = bd.gated_backward(s["dy"], ckpt, k, s["log_re"], dx=s["dx"], lens=lens, **kept)
+            empty = lens == 0
+            assert torch.equal(end[empty], s["x0"][empty])
+            assert torch.equal(got["dx0"][empty], s["dx"][empty])
+            for t in (y, got["du"], got["dr"], got["di"]):
+                assert not t[empty].any()
+            if empty.all():
+                assert not got["dlog_re"].any()
