@@ -387,7 +387,8 @@ int dssm_s5_forward_timed(const float* u, const dssm_s5_params* p, const dssm_s5
  *   float32 (sums of gradients over batch and time in float64 at the end) and
  *   every output is rounded once, to nearest even.
  * - Pointers need the alignment of their element type (workspaces and
- *   checkpoints 256 bytes).
+ *   checkpoints 256 bytes).  No output, checkpoint or workspace may be another
+ *   buffer of its call, except where stated (DSSM_ERR_INVALID_ARG).
  * - stride_b / stride_g / ...: elements between two batch rows, at least H L;
  *   the H L elements of a row are contiguous.  A joint projection's output
  *   [B, 3 H, L] is passed as three slices with stride_b = 3 H L.

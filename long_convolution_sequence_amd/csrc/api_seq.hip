@@ -177,6 +177,13 @@ int dssm_gated_forward(const dssm_gated_inputs* in, const dssm_gated_shape* s, c
   if ((rc = check_forward(in, s, x0, x_end, y, !empty))) return rc;
   if (!empty && kind != DSSM_CKPT_NONE && (rc = check_buffer(ckpt, "ckpt"))) return rc;
   if ((rc = check_space(ws, ws_bytes, gated_workspace(s->B, s->H, s->L)))) return rc;
+  if (!empty) {
+    const void* kept = kind == DSSM_CKPT_NONE ? nullptr : ckpt;
+    const std::initializer_list<Named> rest = {
+        {in->u, "u"}, {in->r, "r"},       {in->i, "i"}, {in->log_re, "log_re"},
+        {x0, "x0"},   {x_end, "x_end"}, {y, "y"},     {in->lens, "lens"}};
+    if ((rc = check_alias({{kept, "ckpt"}, {ws, "workspace"}}, rest))) return rc;
+  }
   GatedCall c = gated_call(in, s);
   c.x0 = x0;
   c.xT = x_end;
@@ -244,6 +251,13 @@ int dssm_gated_backward(const dssm_gated_inputs* in, const dssm_gated_shape* s, 
       return rc;
   }
   if (s->B > 0 && (rc = check_space(ws, ws_bytes, gated_workspace(s->B, s->H, s->L)))) return rc;
+  if (!empty &&
+      (rc = check_alias({{ws, "workspace"}},
+                        {{ckpt, "ckpt"}, {dy, "dy"}, {g->du, "du"}, {g->dr, "dr"}, {g->di, "di"},
+                         {g->dlog_re, "dlog_re"}, {g->dx0, "dx0"}, {in->log_re, "log_re"},
+                         {dx_end, "dx_end"}, {in->lens, "lens"}, {reads ? in->u : dy, "u"},
+                         {reads ? in->r : dy, "r"}, {reads ? in->i : dy, "i"}})))
+    return rc;
   GatedCall c = gated_call(in, s);
   c.kind = kind;
   c.ckpt = empty ? nullptr : const_cast<void*>(ckpt);
@@ -442,6 +456,12 @@ int dssm_resnorm_backward(const void* o, const void* y, const void* g, long long
                          {stats, "stats"}})))
     return rc;
   if ((rc = check_space(ws, ws_bytes, resnorm_workspace(s->B, s->H, s->L, s->dtype)))) return rc;
+  if ((rc = check_alias({{ws, "workspace"}},
+                        {{o, "o"}, {y, "y"}, {g, "g"}, {d_o, "d_o"}, {d_n, "d_n"}, {stats, "stats"},
+                         {gr->dx, "dx"}, {y ? gr->dy : none, "dy"}, {g ? gr->dg : none, "dg"},
+                         {y ? gr->dw_post : none, "dw_post"}, {y ? gr->dscale : none, "dscale"},
+                         {gr->dw_pre, "dw_pre"}})))
+    return rc;
   ResnormCall c = resnorm_call(o, y, g, stride_g, p, s, lens);
   c.stats = const_cast<float*>(stats);
   c.d_o = d_o;

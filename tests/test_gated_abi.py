@@ -251,3 +251,34 @@ def test_binding_needs_a_checkpoint():
                 bd.gated_backward(dy, ckpt, kind, torch.ones(2), u=dy, r=dy, i=dy)
     with pytest.raises(ValueError, match="blob"):
         bd.ckpt8_unpack(None, (2, 3), torch.float32)
+
+
+def test_scratch_memory_is_its_own():
+    """A checkpoint or workspace that is another buffer of the call would be
+    written over while it is read: refused."""
+    L = bd.lib()
+    inp, s = inputs(lens=at(4)), gshape()
+
+    def forward(ckpt, ws, kind=bd.CKPT_INT8):
+        rc = L.dssm_gated_forward(ctypes.byref(inp), ctypes.byref(s), at(5), at(6), at(7), kind,
+                                  ckpt, ws, 1 << 30, None)
+        return rc, L.dssm_last_error()
+
+    for k in list(range(8)) + [9]:
+        rc, text = forward(at(k), at(9))
+        assert rc == INV and b"alias" in text, k
+    for k in range(9):
+        rc, text = forward(at(8), at(k))
+        assert rc == INV and b"alias" in text, k
+    g = bd.GatedGrads(at(10), at(11), at(12), 120, at(13), at(14))
+    for kind in (bd.CKPT_STATE, bd.CKPT_INT8):
+        for k in ([0, 1, 2] if kind == bd.CKPT_STATE else []) + [3, 4, 6, 7, 8, 10, 11, 12, 13, 14]:
+            assert L.dssm_gated_backward(ctypes.byref(inp), ctypes.byref(s), kind, at(8), at(7), at(6),
+                                         ctypes.byref(g), at(k), 1 << 30, None) == INV, (kind, k)
+            assert b"alias" in L.dssm_last_error()
+    gr = bd.ResnormGrads(at(10), at(11), at(12), 120, at(13), at(14), at(15))
+    for k in (0, 1, 2, 6, 7, 8, 10, 11, 12, 13, 14, 15):
+        assert L.dssm_resnorm_backward(at(0), at(1), at(2), 120, at(6), ctypes.byref(rparams()),
+                                       ctypes.byref(rshape()), None, at(7), at(8), ctypes.byref(gr),
+                                       at(k), 1 << 30, None) == INV, k
+        assert b"alias" in L.dssm_last_error()
