@@ -384,8 +384,9 @@ int dssm_s5_forward_timed(const float* u, const dssm_s5_params* p, const dssm_s5
  * fastest.  Conventions that differ from the calls above:
  * - `dtype` is the type of the activations (u, r, i, y, their gradients, ...);
  *   parameters, states and statistics are float32.  All arithmetic is in
- *   float32 (sums of gradients over batch and time in float64 at the end) and
- *   every output is rounded once, to nearest even.
+ *   float32 (parameters' gradients are added up over batch and time in float32
+ *   within a workgroup's share at most, in float64 from there) and every output
+ *   is rounded once, to nearest even.
  * - Pointers need the alignment of their element type (workspaces and
  *   checkpoints 256 bytes).  No output, checkpoint or workspace may be another
  *   buffer of its call, except where stated (DSSM_ERR_INVALID_ARG).
@@ -511,7 +512,9 @@ int dssm_ckpt8_unpack(const void* blob, long long rows, int L, int dtype, void* 
  *   DSSM_NORM_RMS),
  *   v = norm(y) w_post,  o = x + scale v silu(g),  n = norm(o) w_pre,
  * o the residual stream after the layer and n what the next layer reads (the
- * second norm is of the stream as it is stored, in `dtype`). */
+ * second norm is of the stream as it is stored, in `dtype`).  Both norms have a
+ * weight and no bias, the layer norm too.  silu(g) = g sigmoid(g): 0 at the
+ * type's lowest value, NaN at -infinity. */
 typedef enum { DSSM_NORM_RMS = 0, DSSM_NORM_LAYER = 1 } dssm_norm;
 
 typedef struct {

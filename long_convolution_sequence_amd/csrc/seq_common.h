@@ -146,6 +146,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 // 1 / (1 + exp(-x)) and, to full relative precision, 1 minus it.  Where exp(-x)
 // is too large for its reciprocal the first is 0 and the second 1; NaN passes.
+// The exponent is one rounded product, so both carry (1 + 1.25 |x|) 2^-24 or so
+// beside the hardware's 2^-23: 2e-6 of a value of 1e-13 at x = -30, and nothing
+// of a step's size (the rest of log2(e) x would cost three more vector
+// operations a gate, in kernels whose vector work takes as long as their memory).
 __device__ __forceinline__ float sigmoid_pair(float x, float* rest) {
   const float t = exp2_fast(-kLog2e * x);
   const float s = __builtin_amdgcn_rcpf(1.f + t);

@@ -12,7 +12,8 @@ from seq_cases import (c_norm, close, dtype_of, gated_inputs, lens_of, norm_inpu
 pytestmark = pytest.mark.gpu
 
 # (B, H, L, type, layer norm, ragged): single steps, rows shorter than a strip, odd rows,
-# every strip width (H up to 1024, 2048, 4096, 8192) and channels just past each
+# the forms' borders in channels (forward 16 to 128, 256, 512; backward 32 to 128, 256, 512, 1024)
+# and past them up to the most
 SHAPES = [
     (1, 1, 1, "f32", False, False), (3, 17, 1, "bf16", True, True), (5, 2048, 1, "f16", False, False),
     (2, 2049, 1, "bf16", False, False), (2, 8192, 1, "f32", True, False),
