@@ -571,6 +571,141 @@ int dssm_resnorm_backward(const void* o, const void* y, const void* g, long long
                           const void* d_n, const dssm_resnorm_grads* gr, void* ws,
                           size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A selective state space block: the short causal convolution, the scan whose
+ * step sizes, drive and read-out come with every step, and the norm that feeds
+ * the next product in 8 bits.  Conventions as for the gated recurrence (types,
+ * strides, lens, aliases, sums in a fixed order).
+ * ------------------------------------------------------------------------ */
+typedef enum { DSSM_ACT_NONE = 0, DSSM_ACT_SILU = 1 } dssm_act;
+
+typedef struct {
+  int B, H, L;
+  int K;     /* taps, 1 .. 8 */
+  int dtype; /* dssm_dtype */
+  int act;   /* dssm_act */
+} dssm_shortconv_shape;
+
+/* du [B, H, L] (stride_b between batch rows), dw [H, K], dbias [H], dx0
+ * [B, H, K - 1] float32 (the last two may be NULL). */
+typedef struct {
+  void* du;
+  long long stride_b;
+  float* dw;
+  float* dbias;
+  float* dx0;
+} dssm_shortconv_grads;
+
+/* The short causal convolution of every channel,
+ *   y_t = act(bias + sum_{k < K} w_k u_{t - (K - 1) + k}),
+ * the steps before the first one coming from the state.
+ *   u, y [B, H, L] (u: stride_b between batch rows);  w [H, K], bias [H] float32
+ *   (bias may be NULL: zero);
+ *   x0 [B, H, K - 1] float32 (may be NULL: zero): the K - 1 inputs before step
+ *   0, the oldest first;  x_end [B, H, K - 1] (may be NULL) receives the last
+ *   K - 1 up to the last live step (with fewer live steps, x0's last are kept
+ *   ahead of them); it may be x0.
+ * silu is 0 at the type's lowest value, NaN at -infinity.  Requires B H <= 2^24
+ * and the limits of the gated recurrence. */
+int dssm_shortconv_forward(const void* u, long long stride_b, const float* w, const float* bias,
+                           const dssm_shortconv_shape* s, const int* lens, const float* x0,
+                           float* x_end, void* y, void* stream);
+
+/* One token for every (b, h): u, y [B, H] (s->L must be 1; stride_b >= H).  A
+ * stream with lens[b] <= 0 is idle: its state is kept and its output is 0. */
+int dssm_shortconv_step(const void* u, long long stride_b, const float* w, const float* bias,
+                        const dssm_shortconv_shape* s, const int* lens, const float* x0,
+                        float* x_end, void* y, void* stream);
+
+/* Bytes of workspace of dssm_shortconv_backward (host only). */
+int dssm_shortconv_workspace_size(const dssm_shortconv_shape* s, size_t* bytes);
+
+/* Gradients of f = sum(dy y) + sum(dx_end x_end) for the forward call with the
+ * same u, w, bias, lens and x0.  dy [B, H, L]; dx_end [B, H, K - 1] float32
+ * (may be NULL: zero). */
+int dssm_shortconv_backward(const void* u, long long stride_b, const float* w, const float* bias,
+                            const dssm_shortconv_shape* s, const int* lens, const float* x0,
+                            const void* dy, const float* dx_end, const dssm_shortconv_grads* g,
+                            void* ws, size_t ws_bytes, void* stream);
+
+#define DSSM_SELECTIVE_CHUNK 256 /* steps between two kept states */
+
+typedef struct {
+  int B, H, L;
+  int N;     /* modes of a channel, 1 .. 128 */
+  int G;     /* groups: channel h reads B and C of group h / (H / G); H % G = 0 */
+  int dtype; /* dssm_dtype */
+} dssm_selective_shape;
+
+/* u, delta, z [B, H, L], Bm, Cm [B, G, N, L], each with its elements between two
+ * batch rows (at least H L, G N L);  log_re [H, N], D [H], dt_bias [H] float32.
+ * z, D and dt_bias may be NULL: no gate, no skip, no bias. */
+typedef struct {
+  const void* u;
+  const void* delta;
+  const void* z;
+  const void* Bm;
+  const void* Cm;
+  long long stride_u, stride_delta, stride_z, stride_B, stride_C;
+  const float* log_re;
+  const float* D;
+  const float* dt_bias;
+  const int* lens; /* [B] or NULL */
+} dssm_selective_inputs;
+
+/* Gradients of the inputs, shaped and strided like them; dlog_re [H, N], dD,
+ * ddt_bias [H], dx0 [B, H, N] float32.  dz goes with z, dD with D, ddt_bias with
+ * dt_bias (NULL without them); dx0 may be NULL. */
+typedef struct {
+  void* du;
+  void* ddelta;
+  void* dz;
+  void* dB;
+  void* dC;
+  long long stride_u, stride_delta, stride_z, stride_B, stride_C;
+  float* dlog_re;
+  float* dD;
+  float* ddt_bias;
+  float* dx0;
+} dssm_selective_grads;
+
+/* Bytes of workspace of dssm_selective_forward or (backward != 0)
+ * dssm_selective_backward (host only).  Requires H <= 65535, B H <= 2^24, L <=
+ * 2^24, B H L <= 2^40, B H N ceil(L / 256) <= 2^36. */
+int dssm_selective_workspace_size(const dssm_selective_shape* s, int backward, size_t* bytes);
+
+/* Bytes of a checkpoint: the states [B, H, ceil(L / 256), N] float32 entering
+ * the chunks (those of a row's dead chunks are not written), padded to 256. */
+int dssm_selective_ckpt_size(const dssm_selective_shape* s, size_t* bytes);
+
+/* The selective scan: for every (b, h) a bank of N real modes driven alike,
+ *   dt_t = softplus(delta_t + dt_bias[h]),
+ *   x_t = exp(-log_re[h]^2 dt_t) x_{t-1} + dt_t B_t u_t         (N values each),
+ *   y_t = (sum_n C_t x_t + D[h] u_t) silu(z_t)
+ * (a step of length 1 decays as the mode exp(-log_re^2) of the layer above;
+ * delta = -infinity is a step that changes nothing).
+ *   x0 [B, H, N] float32 (may be NULL: zero): the state before step 0;
+ *   x_end [B, H, N] float32 (may be NULL): receives the state after the last
+ *   live step; it may be x0.
+ * ckpt (may be NULL): dssm_selective_ckpt_size bytes, for a backward pass. */
+int dssm_selective_forward(const dssm_selective_inputs* in, const dssm_selective_shape* s,
+                           const float* x0, float* x_end, void* y, void* ckpt, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* One token for every (b, h): u, delta, z, y [B, H], Bm, Cm [B, G, N] (s->L must
+ * be 1; strides at least H, G N), states as above.  A stream with lens[b] <= 0
+ * is idle: its state is kept and its output is 0.  No workspace. */
+int dssm_selective_step(const dssm_selective_inputs* in, const dssm_selective_shape* s,
+                        const float* x0, float* x_end, void* y, void* stream);
+
+/* Gradients of f = sum(dy y) + sum(dx_end x_end) for the forward call of the
+ * same inputs that wrote ckpt.  dy [B, H, L]; dx_end [B, H, N] float32 (may be
+ * NULL: zero). */
+int dssm_selective_backward(const dssm_selective_inputs* in, const dssm_selective_shape* s,
+                            const void* ckpt, const void* dy, const float* dx_end,
+                            const dssm_selective_grads* g, void* ws, size_t ws_bytes,
+                            void* stream);
+
 /* Timing variants: identical results to dssm_forward_fft / dssm_forward_scan;
  * the kernels of stage k are launched with hipExtLaunchKernel so that the GPU
  * itself stamps events[2k] when the stage's first kernel starts and

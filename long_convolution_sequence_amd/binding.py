@@ -29,6 +29,8 @@ F32, BF16, F16 = 0, 1, 2  # activation types of the gated recurrence and the blo
 CKPT_NONE, CKPT_STATE, CKPT_INT8 = 0, 1, 2
 GATED_CHUNK, CKPT8_GROUP = 512, 64
 NORM_RMS, NORM_LAYER = 0, 1
+ACT_NONE, ACT_SILU = 0, 1  # after the short convolution
+SELECTIVE_CHUNK = 256  # steps between the states a selective scan keeps
 
 # Every function the header declares (checked by the ABI tests).
 EXPORTS = [
@@ -43,6 +45,10 @@ EXPORTS = [
     "dssm_gated_workspace_size", "dssm_gated_ckpt_size", "dssm_gated_forward", "dssm_gated_step",
     "dssm_gated_backward", "dssm_ckpt8_size", "dssm_ckpt8_pack", "dssm_ckpt8_unpack",
     "dssm_resnorm_forward", "dssm_resnorm_workspace_size", "dssm_resnorm_backward",
+    "dssm_shortconv_forward", "dssm_shortconv_step", "dssm_shortconv_workspace_size",
+    "dssm_shortconv_backward",
+    "dssm_selective_workspace_size", "dssm_selective_ckpt_size", "dssm_selective_forward",
+    "dssm_selective_step", "dssm_selective_backward",
 ]
 
 
@@ -107,6 +113,33 @@ class ResnormGrads(ctypes.Structure):
     _fields_ = [("dx", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dg", ctypes.c_void_p),
                 ("stride_dg", ctypes.c_longlong), ("dw_post", ctypes.c_void_p),
                 ("dscale", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p)]
+
+
+class ShortconvShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int), ("K", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+class ShortconvGrads(ctypes.Structure):
+    _fields_ = [("du", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("dw", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("dx0", ctypes.c_void_p)]
+
+
+class SelectiveShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int), ("N", ctypes.c_int),
+                ("G", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class SelectiveInputs(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("u", "delta", "z", "Bm", "Cm")]
+                + [("stride_" + k, ctypes.c_longlong) for k in ("u", "delta", "z", "B", "C")]
+                + [(k, ctypes.c_void_p) for k in ("log_re", "D", "dt_bias", "lens")])
+
+
+class SelectiveGrads(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("du", "ddelta", "dz", "dB", "dC")]
+                + [("stride_" + k, ctypes.c_longlong) for k in ("u", "delta", "z", "B", "C")]
+                + [(k, ctypes.c_void_p) for k in ("dlog_re", "dD", "ddt_bias", "dx0")])
 
 
 class DSSMError(RuntimeError):
@@ -182,6 +215,8 @@ def lib():
     P = ctypes.POINTER
     gi, gs, gg = P(GatedInputs), P(GatedShape), P(GatedGrads)
     rp, rs, rg = P(ResnormParams), P(ResnormShape), P(ResnormGrads)
+    cs, ci, si, ss = P(ShortconvShape), ctypes.c_int, P(SelectiveInputs), P(SelectiveShape)
+    conv = [vp, ctypes.c_longlong, vp, vp, cs, vp, vp]
     for name, args in (
             ("dssm_gated_workspace_size", [gs, P(sz)]),
             ("dssm_gated_ckpt_size", [gs, ctypes.c_int, P(sz)]),
@@ -194,7 +229,16 @@ def lib():
             ("dssm_resnorm_forward", [vp, vp, vp, ctypes.c_longlong, rp, rs, vp, vp, vp, vp, vp]),
             ("dssm_resnorm_workspace_size", [rs, P(sz)]),
             ("dssm_resnorm_backward", [vp, vp, vp, ctypes.c_longlong, vp, rp, rs, vp, vp, vp, rg,
-                                       vp, sz, vp])):
+                                       vp, sz, vp]),
+            ("dssm_shortconv_forward", conv + [vp, vp, vp]),
+            ("dssm_shortconv_step", conv + [vp, vp, vp]),
+            ("dssm_shortconv_workspace_size", [cs, P(sz)]),
+            ("dssm_shortconv_backward", conv + [vp, vp, P(ShortconvGrads), vp, sz, vp]),
+            ("dssm_selective_workspace_size", [ss, ci, P(sz)]),
+            ("dssm_selective_ckpt_size", [ss, P(sz)]),
+            ("dssm_selective_forward", [si, ss, vp, vp, vp, vp, vp, sz, vp]),
+            ("dssm_selective_step", [si, ss, vp, vp, vp, vp]),
+            ("dssm_selective_backward", [si, ss, vp, vp, vp, P(SelectiveGrads), vp, sz, vp])):
         f = getattr(L, name)
         f.restype = ctypes.c_int
         f.argtypes = args
@@ -643,10 +687,12 @@ def _opt_vec(t, name, numel, device):
 
 
 def _batch_stride(t, name):
-    """Elements between the batch rows of t [B, H, L] (or [B, H]), whose H L
-    elements are contiguous."""
+    """Elements between the batch rows of t [B, H, L], [B, H] or [B, G, N, L],
+    whose elements are contiguous."""
     shape = t.shape
     if t.is_contiguous():
+        if len(shape) == 4:
+            return shape[1] * shape[2] * shape[3]
         return shape[1] * shape[2] if len(shape) == 3 else shape[1]
     st = t.stride()
     inner = 1
@@ -1021,6 +1067,243 @@ def resnorm_backward(o, y, g, stats, w_post, scale, w_pre, do, dn, norm=NORM_RMS
             _vec(stats, "stats", (4 if norm == NORM_LAYER else 2) * B * L, dev),
             _resnorm_params(w_post, scale, w_pre, H, dev, y is not None, dn is not None), sp,
             _lens_ptr(lens, B, dev), _ptr(do), _ptr(dn), ctypes.byref(gr), ws.data_ptr(), nbytes)
+    return out
+
+
+# ----------------------------------------------------------------------------
+# the short convolution and the selective scan
+# ----------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _shortconv_bytes(B, H, L, K, code):
+    """Bytes of workspace of the short convolution's backward pass."""
+    need = ctypes.c_size_t(0)
+    shape = ShortconvShape(B, H, L, K, code, ACT_NONE)
+    check(lib().dssm_shortconv_workspace_size(ctypes.byref(shape), ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=256)
+def _selective_bytes(B, H, L, N, G, code, which):
+    """Bytes of workspace of the selective scan, forward (which 0) or backward
+    (1), or of its checkpoint (None)."""
+    need = ctypes.c_size_t(0)
+    shape = SelectiveShape(B, H, L, N, G, code)
+    if which is None:
+        check(lib().dssm_selective_ckpt_size(ctypes.byref(shape), ctypes.byref(need)))
+    else:
+        check(lib().dssm_selective_workspace_size(ctypes.byref(shape), which, ctypes.byref(need)))
+    return need.value
+
+
+def _taps(w, H):
+    torch = _torch()
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch tensor")
+    if w.dim() != 2 or w.shape[0] != H:
+        raise ValueError("w must be [%d, K], got %s" % (H, tuple(w.shape)))
+    return w.shape[1]
+
+
+def _shortconv(fn, u, w, bias, act, x, x_out, lens, y, stream, L):
+    code = _dtype_code(u, "u")
+    B, H = u.shape[:2]
+    dev = u.device
+    K = _taps(w, H)
+    nx = B * H * (K - 1)
+    xp = _opt_vec(x, "x", nx, dev)
+    xo = xp if x_out is None else _vec(x_out, "x_out", nx, dev)
+    sb = _batch_stride(u, "u")
+    y = _new(u, stream) if y is None else _plain(y, "y", u, "u")
+    _launch(fn, dev, stream, u.data_ptr(), sb, _vec(w, "w", H * K, dev),
+            _opt_vec(bias, "bias", H, dev), ctypes.byref(ShortconvShape(B, H, L, K, code, int(act))),
+            _lens_ptr(lens, B, dev), xp, xo, y.data_ptr())
+    return y
+
+
+def shortconv_forward(u, w, bias=None, act=ACT_SILU, x=None, x_out=None, lens=None, y=None,
+                      stream=None):
+    """The short causal convolution of every channel: y_t = act(bias + sum_k w_k
+    u_{t - (K - 1) + k}).  u [B,H,L] f32, bf16 or f16 (a slice of a joint
+    projection is taken as it is), w [H,K] f32, K <= 8, bias [H] f32 -> y
+    [B,H,L].  x [B,H,K-1] f32: the inputs before the first step, oldest first,
+    None for zero; the last K - 1 inputs go to x_out, or back to x.  lens [B]
+    int32: live steps per batch row (y is 0 behind them)."""
+    if u.dim() != 3:
+        raise ValueError("u must be [B, H, L]")
+    return _shortconv(lib().dssm_shortconv_forward, u, w, bias, act, x, x_out, lens, y, stream,
+                      u.shape[2])
+
+
+def shortconv_step(u_t, w, bias, x, act=ACT_SILU, x_out=None, lens=None, y=None, stream=None):
+    """One token of the short convolution: u_t [B,H] -> y_t [B,H]; the state x
+    [B,H,K-1] f32 is updated in place, or left and written to x_out.  lens [B]
+    int32: rows with 0 are idle (state kept, y 0)."""
+    if u_t.dim() != 2:
+        raise ValueError("u_t must be [B, H]")
+    if x is None:
+        raise TypeError("x must be a torch tensor")
+    return _shortconv(lib().dssm_shortconv_step, u_t, w, bias, act, x, x_out, lens, y, stream, 1)
+
+
+def shortconv_backward(dy, u, w, bias=None, act=ACT_SILU, x=None, dx=None, lens=None, du=None,
+                       workspace=None, stream=None):
+    """Gradients of f = sum(dy y) + sum(dx x_end) for shortconv_forward of the
+    same u, w, bias, x and lens.  dy [B,H,L]; dx [B,H,K-1] f32 or None.  Returns
+    a dict du [B,H,L] (du given: a slice of a joint gradient is written as it
+    is), dw [H,K], dbias [H] (None without bias), dx0 [B,H,K-1] f32."""
+    torch = _torch()
+    code = _dtype_code(dy, "dy")
+    if dy.dim() != 3:
+        raise ValueError("dy must be [B, H, L]")
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    _like(u, "u", dy, "dy")
+    B, H, L = dy.shape
+    dev = dy.device
+    K = _taps(w, H)
+    nx = B * H * (K - 1)
+    out = dict(du=_new(dy, stream) if du is None else _like(du, "du", dy, "dy"),
+               dw=_empty((H, K), torch.float32, dev, stream),
+               dbias=None if bias is None else _empty((H,), torch.float32, dev, stream),
+               dx0=_empty((B, H, K - 1), torch.float32, dev, stream))
+    ws, nbytes = _buffer(_shortconv_bytes(B, H, L, K, code), workspace, "workspace", dev, stream)
+    g = ShortconvGrads(out["du"].data_ptr(), _batch_stride(out["du"], "du"), out["dw"].data_ptr(),
+                       _ptr(out["dbias"]), _ptr(out["dx0"]))
+    _launch(lib().dssm_shortconv_backward, dev, stream, u.data_ptr(), _batch_stride(u, "u"),
+            _vec(w, "w", H * K, dev), _opt_vec(bias, "bias", H, dev),
+            ctypes.byref(ShortconvShape(B, H, L, K, code, int(act))), _lens_ptr(lens, B, dev),
+            _opt_vec(x, "x", nx, dev), dy.data_ptr(), _opt_vec(dx, "dx", nx, dev), ctypes.byref(g),
+            ws.data_ptr(), nbytes)
+    return out
+
+
+def _selective_inputs(u, delta, Bm, Cm, log_re, D, dt_bias, z, lens, token):
+    """Checked inputs: their structure, shape structure and device."""
+    torch = _torch()
+    code = _dtype_code(u, "u")
+    if u.dim() != (2 if token else 3):
+        raise ValueError("u must be %s" % ("[B, H]" if token else "[B, H, L]"))
+    _like(delta, "delta", u, "u")
+    if z is not None:
+        _like(z, "z", u, "u")
+    for t, name in ((Bm, "Bm"), (Cm, "Cm")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch tensor" % name)
+    B, H = u.shape[:2]
+    L = 1 if token else u.shape[2]
+    if Bm.dim() != u.dim() + 1 or Bm.shape[0] != B or (not token and Bm.shape[3] != L):
+        raise ValueError("Bm must be %s, got %s" % ("[B, G, N]" if token else "[B, G, N, L]",
+                                                    tuple(Bm.shape)))
+    if Bm.dtype is not u.dtype:
+        raise TypeError("Bm is %s, u is %s" % (Bm.dtype, u.dtype))
+    if Bm.device != u.device:
+        raise ValueError("Bm is on %s, expected %s" % (Bm.device, u.device))
+    _like(Cm, "Cm", Bm, "Bm")
+    G, N = Bm.shape[1:3]
+    if G < 1 or H % G:
+        raise ValueError("H = %d is not a multiple of Bm's %d groups" % (H, G))
+    dev = u.device
+    inp = SelectiveInputs(
+        u.data_ptr(), delta.data_ptr(), _ptr(z), Bm.data_ptr(), Cm.data_ptr(),
+        _batch_stride(u, "u"), _batch_stride(delta, "delta"),
+        0 if z is None else _batch_stride(z, "z"), _batch_stride(Bm, "Bm"), _batch_stride(Cm, "Cm"),
+        _vec(log_re, "log_re", H * N, dev), _opt_vec(D, "D", H, dev),
+        _opt_vec(dt_bias, "dt_bias", H, dev), _lens_ptr(lens, B, dev))
+    return inp, (B, H, L, N, G, code), dev
+
+
+def _selective_forward(u, delta, Bm, Cm, log_re, D, dt_bias, z, x, x_out, lens, y, keep, ckpt,
+                       workspace, stream):
+    inp, dims, dev = _selective_inputs(u, delta, Bm, Cm, log_re, D, dt_bias, z, lens, False)
+    nx = dims[0] * dims[1] * dims[3]
+    xp = _opt_vec(x, "x", nx, dev)
+    xo = xp if x_out is None else _vec(x_out, "x_out", nx, dev)
+    y = _new(u, stream) if y is None else _plain(y, "y", u, "u")
+    need = _selective_bytes(*dims, 0)
+    wp, nbytes = None, 0
+    if need or workspace is not None:
+        workspace, nbytes = _buffer(need, workspace, "workspace", dev, stream)
+        wp = workspace.data_ptr()
+    if keep:
+        ckpt, _ = _buffer(_selective_bytes(*dims, None), ckpt, "ckpt", dev, stream)
+    _launch(lib().dssm_selective_forward, dev, stream, ctypes.byref(inp),
+            ctypes.byref(SelectiveShape(*dims)), xp, xo, y.data_ptr(), _ptr(ckpt) if keep else None,
+            wp, nbytes)
+    return y, ckpt
+
+
+def selective_forward(u, delta, Bm, Cm, log_re, D=None, dt_bias=None, z=None, x=None, x_out=None,
+                      lens=None, y=None, workspace=None, stream=None):
+    """The selective scan: dt = softplus(delta + dt_bias), x_t = exp(-log_re^2 dt)
+    x_{t-1} + dt B_t u_t (N modes per channel), y_t = (sum_n C_t x_t + D u_t)
+    silu(z_t).  u, delta, z [B,H,L] and Bm, Cm [B,G,N,L] f32, bf16 or f16 (slices
+    of joint projections are taken as they are; channel h reads group h // (H //
+    G)), log_re [H,N], D, dt_bias [H] f32 -> y [B,H,L].  x [B,H,N] f32: the state
+    before the first step, None for zero; the state after the last goes to
+    x_out, or back to x.  lens [B] int32: live steps per batch row (y is 0
+    behind them)."""
+    return _selective_forward(u, delta, Bm, Cm, log_re, D, dt_bias, z, x, x_out, lens, y, False,
+                              None, workspace, stream)[0]
+
+
+def selective_forward_ckpt(u, delta, Bm, Cm, log_re, D=None, dt_bias=None, z=None, x=None,
+                           x_out=None, lens=None, y=None, ckpt=None, workspace=None, stream=None):
+    """selective_forward that keeps what selective_backward needs, the states
+    entering every 256 steps: returns (y, ckpt)."""
+    return _selective_forward(u, delta, Bm, Cm, log_re, D, dt_bias, z, x, x_out, lens, y, True,
+                              ckpt, workspace, stream)
+
+
+def selective_step(u_t, delta_t, B_t, C_t, log_re, x, D=None, dt_bias=None, z=None, x_out=None,
+                   lens=None, y=None, stream=None):
+    """One token of the selective scan: u_t, delta_t, z [B,H], B_t, C_t [B,G,N]
+    -> y_t [B,H]; the state x [B,H,N] f32 is updated in place, or left and
+    written to x_out.  lens [B] int32: rows with 0 are idle (state kept, y 0)."""
+    inp, dims, dev = _selective_inputs(u_t, delta_t, B_t, C_t, log_re, D, dt_bias, z, lens, True)
+    nx = dims[0] * dims[1] * dims[3]
+    xp = _vec(x, "x", nx, dev)
+    xo = xp if x_out is None else _vec(x_out, "x_out", nx, dev)
+    y = _new(u_t, stream) if y is None else _plain(y, "y", u_t, "u_t")
+    _launch(lib().dssm_selective_step, dev, stream, ctypes.byref(inp),
+            ctypes.byref(SelectiveShape(*dims)), xp, xo, y.data_ptr())
+    return y
+
+
+def selective_backward(dy, ckpt, u, delta, Bm, Cm, log_re, D=None, dt_bias=None, z=None, dx=None,
+                       lens=None, du=None, ddelta=None, dz=None, dB=None, dC=None, workspace=None,
+                       stream=None):
+    """Gradients of f = sum(dy y) + sum(dx x_end) for the selective_forward_ckpt
+    of the same inputs that returned `ckpt`.  dy [B,H,L]; dx [B,H,N] f32 or None.
+    Returns a dict du, ddelta, dz, dB, dC shaped like their inputs (given ones,
+    slices of joint gradients, are written as they are), dlog_re [H,N], dD,
+    ddt_bias [H], dx0 [B,H,N] f32; dz, dD and ddt_bias are None without z, D and
+    dt_bias."""
+    torch = _torch()
+    # _buffer() below makes a buffer that is not given: this one is read
+    if not isinstance(ckpt, torch.Tensor):
+        raise TypeError("ckpt must be a torch tensor")
+    inp, dims, dev = _selective_inputs(u, delta, Bm, Cm, log_re, D, dt_bias, z, lens, False)
+    B, H, L, N, G, code = dims
+    _plain(dy, "dy", u, "u")
+    if z is None and dz is not None:
+        raise ValueError("dz needs z")
+    new = lambda t, ref, name: (_empty(ref.shape, ref.dtype, dev, stream) if t is None
+                                else _like(t, name, ref, name[1:]))
+    vec = lambda *shape: _empty(shape, torch.float32, dev, stream)
+    out = dict(du=new(du, u, "du"), ddelta=new(ddelta, u, "ddelta"),
+               dz=None if z is None else new(dz, u, "dz"), dB=new(dB, Bm, "dB"),
+               dC=new(dC, Bm, "dC"), dlog_re=vec(H, N), dD=None if D is None else vec(H),
+               ddt_bias=None if dt_bias is None else vec(H), dx0=vec(B, H, N))
+    ws, nbytes = _buffer(_selective_bytes(*dims, 1), workspace, "workspace", dev, stream)
+    ckpt, _ = _buffer(_selective_bytes(*dims, None), ckpt, "ckpt", dev, stream)
+    names = ("du", "ddelta", "dz", "dB", "dC")
+    strides = [0 if out[k] is None else _batch_stride(out[k], k) for k in names]
+    g = SelectiveGrads(*[_ptr(out[k]) for k in names], *strides, out["dlog_re"].data_ptr(),
+                       _ptr(out["dD"]), _ptr(out["ddt_bias"]), out["dx0"].data_ptr())
+    _launch(lib().dssm_selective_backward, dev, stream, ctypes.byref(inp),
+            ctypes.byref(SelectiveShape(*dims)), ckpt.data_ptr(), dy.data_ptr(),
+            _opt_vec(dx, "dx", B * H * N, dev), ctypes.byref(g), ws.data_ptr(), nbytes)
     return out
 
 

@@ -330,4 +330,59 @@ size_t resnorm_workspace(int B, int H, int L, int dtype);
 hipError_t launch_resnorm_forward(const ResnormCall& c, int dtype, hipStream_t st);
 hipError_t launch_resnorm_backward(const ResnormCall& c, int dtype, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Short causal convolution (shortconv.hip)
+// ---------------------------------------------------------------------------
+constexpr int kShortconvTaps = 8;
+struct ShortconvCall {
+  const void* u;       // [B,H,L], elements between batch rows: stride_b
+  long long stride_b;
+  const float *w, *bias;  // [H,K]; [H] or null
+  const int* lens;     // [B] or null
+  int B, H, L, K, silu;
+  const float* x0;     // [B,H,K-1] or null: the inputs before step 0
+  float* xT;           // [B,H,K-1] or null: the last inputs (may be x0)
+  void* y;
+  // backward
+  const void* dy;
+  const float* dx;     // [B,H,K-1] or null
+  void* du;
+  long long grad_stride_b;
+  float *dw, *dbias, *dx0;  // dbias, dx0 may be null
+  void* ws;
+};
+size_t shortconv_workspace(int B, int H, int K, int L);
+hipError_t launch_shortconv_forward(const ShortconvCall& c, int dtype, hipStream_t st);
+hipError_t launch_shortconv_step(const ShortconvCall& c, int dtype, hipStream_t st);
+hipError_t launch_shortconv_backward(const ShortconvCall& c, int dtype, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Selective scan (selective.hip)
+// ---------------------------------------------------------------------------
+constexpr int kSelectiveModes = 128;  // what a workgroup's states take of its LDS
+struct SelectiveCall {
+  const void *u, *delta, *z;  // [B,H,L]; z may be null
+  const void *Bm, *Cm;        // [B,G,N,L]
+  long long stride_u, stride_delta, stride_z, stride_B, stride_C;  // between batch rows
+  const float *log_re, *D, *dt_bias;  // [H,N]; [H] or null
+  const int* lens;            // [B] or null
+  int B, H, G, N, L;
+  const float* x0;            // [B,H,N] or null
+  float* xT;                  // [B,H,N] or null (may be x0)
+  void* y;
+  void* ckpt;                 // forward: may be null
+  void* ws;
+  // backward
+  const void* dy;
+  const float* dx;            // [B,H,N] or null
+  void *du, *ddelta, *dz, *dB, *dC;
+  long long stride_du, stride_ddelta, stride_dz, stride_dB, stride_dC;
+  float *dlog_re, *dD, *ddt_bias, *dx0;  // the last three may be null
+};
+size_t selective_ckpt(int B, int H, int N, int L);
+size_t selective_workspace(int B, int H, int G, int N, int L, bool backward);
+hipError_t launch_selective_forward(const SelectiveCall& c, int dtype, hipStream_t st);
+hipError_t launch_selective_backward(const SelectiveCall& c, int dtype, hipStream_t st);
+hipError_t launch_selective_step(const SelectiveCall& c, int dtype, hipStream_t st);
+
 }  // namespace dssm

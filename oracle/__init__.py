@@ -27,11 +27,14 @@ pages define, in float64, from the float32 input values promoted exactly:
   gradients by the chain rule, and the values an 8-bit checkpoint stands for.
 * ``resnorm`` -- the norms around a layer with its gate and residual scale, and
   their gradients.
+* ``selective`` -- the selective scan and the short causal convolution stepped
+  one step after another, and their gradients by the chain rule.
 
 Parity status: every function is pinned by the ``-m "not gpu"`` tests in
 ``tests/test_oracle_pins.py`` (closed forms, a library DFT, brute-force
-Toeplitz/circulant matrices and invariants) and, for the last two,
-``tests/test_oracle_gated_pins.py`` (closed forms, differences).  No function is "parity unpinned".
+Toeplitz/circulant matrices and invariants) and, for the last three,
+``tests/test_oracle_gated_pins.py`` and ``tests/test_oracle_selective_pins.py``
+(closed forms, differences).  No function is "parity unpinned".
 """
 
 from .dlr import (  # noqa: F401
@@ -46,3 +49,9 @@ from .dlr_grad import dlr_backward  # noqa: F401
 from .s5 import s5_recurrence, s5_direct_prefix, s5_recurrence_tv  # noqa: F401
 from .gated import gated_recurrence, gated_backward, ckpt8  # noqa: F401
 from .resnorm import resnorm_stream, resnorm_out, resnorm_backward  # noqa: F401
+from .selective import (  # noqa: F401
+    selective_scan,
+    selective_backward,
+    short_conv,
+    short_conv_backward,
+)
