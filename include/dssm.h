@@ -706,6 +706,28 @@ int dssm_selective_backward(const dssm_selective_inputs* in, const dssm_selectiv
                             const dssm_selective_grads* g, void* ws, size_t ws_bytes,
                             void* stream);
 
+/* The residual sum and norm of dssm_resnorm_forward with n in 8 bits, for the
+ * product that reads it: per step a scale and whole numbers or e4m3 values,
+ *   n_t = norm(o_t) w_pre,  qs_t = max_h |n_t| / M,  q_t = n_t / qs_t to nearest even,
+ * M = 127 (DSSM_Q8_INT8) or 448 (DSSM_Q8_E4M3: 4 exponent bits, 3 of fraction, no
+ * infinities).  n is not rounded in between.  A step that holds Inf or NaN has
+ * qs NaN and q 0; one whose largest |(o - mean) w_pre| is below 2^-100, or that
+ * is not live, has qs 0 and q 0.
+ *   q [B, L, H], one byte each: channels fastest, unlike every other activation
+ *   here (the operand of an 8-bit product reads along the summed axis);
+ *   qs [B, L] float32;  the rest as dssm_resnorm_forward, and its limits.
+ * Three forms: with y and w_post as there;  y without w_post: o = x + y (no norm
+ * of y; scale and g must be NULL);  without y: n = norm(x) w_pre, o NULL.
+ * stats (may be NULL): as there, for dssm_resnorm_backward, which takes the
+ * rounding for the identity; for o = x + y call it without y: its dx is the
+ * gradient of x and of y. */
+typedef enum { DSSM_Q8_INT8 = 0, DSSM_Q8_E4M3 = 1 } dssm_q8_form;
+
+int dssm_resnorm8_forward(const void* x, const void* y, const void* g, long long stride_g,
+                          const dssm_resnorm_params* p, const dssm_resnorm_shape* s,
+                          const int* lens, int form, void* o, void* q, float* qs, float* stats,
+                          void* stream);
+
 /* Timing variants: identical results to dssm_forward_fft / dssm_forward_scan;
  * the kernels of stage k are launched with hipExtLaunchKernel so that the GPU
  * itself stamps events[2k] when the stage's first kernel starts and

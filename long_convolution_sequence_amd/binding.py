@@ -29,6 +29,7 @@ F32, BF16, F16 = 0, 1, 2  # activation types of the gated recurrence and the blo
 CKPT_NONE, CKPT_STATE, CKPT_INT8 = 0, 1, 2
 GATED_CHUNK, CKPT8_GROUP = 512, 64
 NORM_RMS, NORM_LAYER = 0, 1
+Q8_INT8, Q8_E4M3 = 0, 1  # the norm's output in 8 bits
 ACT_NONE, ACT_SILU = 0, 1  # after the short convolution
 SELECTIVE_CHUNK = 256  # steps between the states a selective scan keeps
 
@@ -44,7 +45,8 @@ EXPORTS = [
     "dssm_s5_forward_timed", "dssm_s5_forward_tv",
     "dssm_gated_workspace_size", "dssm_gated_ckpt_size", "dssm_gated_forward", "dssm_gated_step",
     "dssm_gated_backward", "dssm_ckpt8_size", "dssm_ckpt8_pack", "dssm_ckpt8_unpack",
-    "dssm_resnorm_forward", "dssm_resnorm_workspace_size", "dssm_resnorm_backward",
+    "dssm_resnorm_forward", "dssm_resnorm8_forward", "dssm_resnorm_workspace_size",
+    "dssm_resnorm_backward",
     "dssm_shortconv_forward", "dssm_shortconv_step", "dssm_shortconv_workspace_size",
     "dssm_shortconv_backward",
     "dssm_selective_workspace_size", "dssm_selective_ckpt_size", "dssm_selective_forward",
@@ -227,6 +229,8 @@ def lib():
             ("dssm_ckpt8_pack", [vp, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, vp, vp]),
             ("dssm_ckpt8_unpack", [vp, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, vp, vp]),
             ("dssm_resnorm_forward", [vp, vp, vp, ctypes.c_longlong, rp, rs, vp, vp, vp, vp, vp]),
+            ("dssm_resnorm8_forward", [vp, vp, vp, ctypes.c_longlong, rp, rs, vp, ctypes.c_int, vp,
+                                       vp, vp, vp, vp]),
             ("dssm_resnorm_workspace_size", [rs, P(sz)]),
             ("dssm_resnorm_backward", [vp, vp, vp, ctypes.c_longlong, vp, rp, rs, vp, vp, vp, rg,
                                        vp, sz, vp]),
@@ -1025,6 +1029,68 @@ def resnorm_forward_stats(x, y, g, w_post, scale, w_pre, norm=NORM_RMS, eps=1e-6
                           o=None, n=None, stream=None):
     """resnorm_forward that also returns what resnorm_backward needs: (o, n, stats)."""
     return _resnorm_forward(x, y, g, w_post, scale, w_pre, norm, eps, lens, o, n, True, stream)
+
+
+def _resnorm8_forward(x, y, g, w_post, scale, w_pre, norm, eps, form, lens, o, q, qs, stats,
+                      stream):
+    torch = _torch()
+    code = _dtype_code(x, "x")
+    B, H, L = _resnorm_dims(x, "x")
+    dev = x.device
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if y is None and (g is not None or o is not None):
+        raise ValueError("a gate or a stream output needs y")
+    if w_pre is None:
+        raise ValueError("w_pre is needed")
+    if y is not None and w_post is None and (g is not None or scale is not None):
+        raise ValueError("a gate or a scale needs w_post")
+    if form not in (Q8_INT8, Q8_E4M3):
+        raise ValueError("form must be Q8_INT8 or Q8_E4M3")
+    sg = 0
+    if y is not None:
+        _plain(y, "y", x, "x")
+        o = _new(x, stream) if o is None else _plain(o, "o", x, "x")
+        if g is not None:
+            sg = _batch_stride(_like(g, "g", x, "x"), "g")
+    rows = (B, L) if x.dim() == 3 else (B,)
+    kind = torch.int8 if form == Q8_INT8 else torch.float8_e4m3fn
+    if q is None:
+        q = _empty(rows + (H,), kind, dev, stream)
+    elif (not isinstance(q, torch.Tensor) or q.dtype is not kind or tuple(q.shape) != rows + (H,)
+          or q.device != dev or not q.is_contiguous()):
+        raise ValueError("q must be a contiguous %s tensor of %s on %s" % (kind, rows + (H,), dev))
+    if qs is None:
+        qs = _empty(rows, torch.float32, dev, stream)
+    if stats is True:
+        stats = _empty((4 if norm == NORM_LAYER else 2, B, L), torch.float32, dev, stream)
+    _launch(lib().dssm_resnorm8_forward, dev, stream, x.data_ptr(), _ptr(y), _ptr(g), sg,
+            _resnorm_params(w_post, scale, w_pre, H, dev, y is not None and w_post is not None,
+                            True),
+            ctypes.byref(ResnormShape(B, H, L, code, int(norm), float(eps))),
+            _lens_ptr(lens, B, dev), int(form), _ptr(o), q.data_ptr(), _vec(qs, "qs", B * L, dev),
+            _ptr(stats))
+    return o, q, qs, stats
+
+
+def resnorm8_forward(x, y, g, w_post, scale, w_pre, norm=NORM_RMS, eps=1e-6, form=Q8_INT8,
+                     lens=None, o=None, q=None, qs=None, stream=None):
+    """resnorm_forward with n in 8 bits, for the product that reads it: returns
+    (o, q, qs), n ~ q qs[..., None].  q [B,L,H] (or [B,H]), channels fastest, int8
+    (Q8_INT8) or float8_e4m3fn (Q8_E4M3); qs [B,L] (or [B]) f32, max |n| over 127
+    or 448.  w_post (and scale, g) None: o = x + y; y None: n = norm(x) w_pre and
+    o is None."""
+    return _resnorm8_forward(x, y, g, w_post, scale, w_pre, norm, eps, form, lens, o, q, qs, None,
+                             stream)[:3]
+
+
+def resnorm8_forward_stats(x, y, g, w_post, scale, w_pre, norm=NORM_RMS, eps=1e-6, form=Q8_INT8,
+                           lens=None, o=None, q=None, qs=None, stream=None):
+    """resnorm8_forward that also returns what resnorm_backward needs, which
+    takes the rounding for the identity: (o, q, qs, stats).  For o = x + y call
+    that without y: its dx is the gradient of x and of y."""
+    return _resnorm8_forward(x, y, g, w_post, scale, w_pre, norm, eps, form, lens, o, q, qs, True,
+                             stream)
 
 
 def resnorm_backward(o, y, g, stats, w_post, scale, w_pre, do, dn, norm=NORM_RMS, lens=None,

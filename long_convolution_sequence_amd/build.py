@@ -22,8 +22,8 @@ LIB = os.path.join(HERE, "libdssm.so")
 BUILD_STAMPS = os.path.join(HERE, "_build_stamps")
 LIB_STAMPS = os.path.join(HERE, "libdssm_stamps.so")
 SOURCES = ["api.hip", "api_selective.hip", "api_seq.hip", "chunk.hip", "ckpt8.hip", "eig_gen.hip",
-           "fft.hip", "gated.hip", "grad.hip", "resnorm.hip", "scan.hip", "s5.hip",
-           "selective.hip", "shortconv.hip"]
+           "fft.hip", "gated.hip", "grad.hip", "resnorm.hip", "resnorm8.hip", "scan.hip",
+           "s5.hip", "selective.hip", "shortconv.hip"]
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 FLAGS = [

@@ -320,6 +320,43 @@ int dssm_resnorm_forward(const void* x, const void* y, const void* g, long long 
   return ok();
 }
 
+int dssm_resnorm8_forward(const void* x, const void* y, const void* g, long long stride_g,
+                          const dssm_resnorm_params* p, const dssm_resnorm_shape* s,
+                          const int* lens, int form, void* o, void* q, float* qs, float* stats,
+                          void* stream) {
+  bool empty = false;
+  int rc = check_resnorm(s, &empty);
+  if (rc) return rc;
+  if (form != DSSM_Q8_INT8 && form != DSSM_Q8_E4M3)
+    return fail(DSSM_ERR_INVALID_ARG, "form must be DSSM_Q8_INT8 or DSSM_Q8_E4M3, got %d", form);
+  if (empty) return ok();
+  const size_t e = elem_size(s->dtype);
+  if (!p) return fail(DSSM_ERR_INVALID_ARG, "params is NULL");
+  if (y && !p->w_post && (g || p->scale))
+    return fail(DSSM_ERR_INVALID_ARG, "a gate or a scale needs w_post");
+  // without w_post y is only added: as a call without y, but for o
+  const bool plain = y && !p->w_post;
+  if ((rc = check_resnorm_in(x, "x", plain ? nullptr : y, g, stride_g, p, s, lens, true)) ||
+      (rc = check_opt(y, "y", e)) || (y && (rc = check_ptrs({{o, "o"}}, e))))
+    return rc;
+  if (!y && o) return fail(DSSM_ERR_INVALID_ARG, "o needs y (without y the stream is x)");
+  if ((rc = check_ptrs({{q, "q"}}, 1)) || (rc = check_ptrs({{qs, "qs"}}, 4)) ||
+      (rc = check_opt(stats, "stats", 4)))
+    return rc;
+  if ((rc = check_alias({{o, "o"}, {q, "q"}, {qs, "qs"}, {stats, "stats"}},
+                        {{x, "x"}, {y, "y"}, {g, "g"}, {p->w_post, "w_post"},
+                         {p->scale, "scale"}, {p->w_pre, "w_pre"}, {lens, "lens"}})))
+    return rc;
+  ResnormCall c = resnorm_call(x, y, g, stride_g, p, s, lens);
+  c.o = o;
+  c.stats = stats;
+  const Resnorm8Out out{form == DSSM_Q8_E4M3, q, qs};
+  if ((rc = hip_check(launch_resnorm8(c, s->dtype, out, static_cast<hipStream_t>(stream)),
+                      "resnorm8 forward launch")))
+    return rc;
+  return ok();
+}
+
 int dssm_resnorm_workspace_size(const dssm_resnorm_shape* s, size_t* bytes) {
   if (!bytes) return fail(DSSM_ERR_INVALID_ARG, "bytes is NULL");
   bool empty = false;

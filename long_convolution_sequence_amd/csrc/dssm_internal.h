@@ -330,6 +330,16 @@ size_t resnorm_workspace(int B, int H, int L, int dtype);
 hipError_t launch_resnorm_forward(const ResnormCall& c, int dtype, hipStream_t st);
 hipError_t launch_resnorm_backward(const ResnormCall& c, int dtype, hipStream_t st);
 
+// With the second norm's output in 8 bits (resnorm8.hip); c.n is not used, and
+// without c.w_post o = x + y.
+struct Resnorm8Out {
+  int e4m3;
+  void* q;    // [B,L,H] bytes
+  float* qs;  // [B,L]
+};
+hipError_t launch_resnorm8(const ResnormCall& c, int dtype, const Resnorm8Out& out,
+                           hipStream_t st);
+
 // ---------------------------------------------------------------------------
 // Short causal convolution (shortconv.hip)
 // ---------------------------------------------------------------------------

@@ -27,6 +27,7 @@
 
 #include "dssm_internal.h"
 #include "seq_common.h"
+#include "strip.h"
 
 namespace dssm {
 namespace {
@@ -61,16 +62,9 @@ struct Args {
   float* part_h;          // [rows][nseg][2]
 };
 
-// A value from another lane of its row of 16; lanes the pattern does not reach get 0.
-template <int CTRL>
-__device__ __forceinline__ float row_move(float x) {
-  return __uint_as_float(
-      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
-}
-
 // Inclusive scan over a row's 16 lanes, in time order or (REV) against it, of
-// x -> P x + V.  P is only right where it is still used: a lane without a
-// neighbour joins 0, and its P, 0 from there on, meets no further neighbour.
+// x -> P x + V.  A lane without a neighbour joins 0 (what row_move gives there);
+// its P, 0 from there on, meets no further neighbour.
 template <bool REV>
 __device__ __forceinline__ void row_scan(float P, float& V) {
   constexpr int S = REV ? kRowShl : kRowShr;
