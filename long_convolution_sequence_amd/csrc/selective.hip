@@ -24,6 +24,7 @@
 // recurrence (one to join the lanes, one from the joined state) and the
 // read-out, about 6 operations and an exponential per mode and step.
 #include <algorithm>
+#include <type_traits>
 
 #include "dssm_internal.h"
 #include "seq_common.h"
@@ -65,16 +66,23 @@ struct Args {
 // Inclusive scan over a row's 16 lanes, in time order or (REV) against it, of
 // x -> P x + V.  A lane without a neighbour joins 0 (what row_move gives there);
 // its P, 0 from there on, meets no further neighbour.
-template <bool REV>
-__device__ __forceinline__ void row_scan(float P, float& V) {
+template <bool REV, int M>
+__device__ __forceinline__ void row_scan(float* P, float* V) {
   constexpr int S = REV ? kRowShl : kRowShr;
-  V = fmaf(P, row_move<S + 1>(V), V);
-  P *= row_move<S + 1>(P);
-  V = fmaf(P, row_move<S + 2>(V), V);
-  P *= row_move<S + 2>(P);
-  V = fmaf(P, row_move<S + 4>(V), V);
-  P *= row_move<S + 4>(P);
-  V = fmaf(P, row_move<S + 8>(V), V);
+#pragma unroll
+  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 1>(V[i]), V[i]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) P[i] *= row_move<S + 1>(P[i]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 2>(V[i]), V[i]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) P[i] *= row_move<S + 2>(P[i]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 4>(V[i]), V[i]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) P[i] *= row_move<S + 4>(P[i]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 8>(V[i]), V[i]);
 }
 
 // x summed over a row's 16 lanes; all of them get the sum.
@@ -86,28 +94,23 @@ __device__ __forceinline__ float row_total(float x) {
   return x;
 }
 
-// log(1 + exp(v)) to a few roundings, NaN passing: max(v, 0) + log1p(t),
-// t = exp(-|v|) with the rest of the product by log2(e), log1p as the odd
-// series of s = t / (2 + t) <= 1/3 (the ninth power's successor is 2^-26 of the
-// first).  Steps of 1e-3 and less are what the map is used with: 1 + t would
-// keep ten bits of them.
+// log(1 + exp(v)), NaN passing: max(v, 0) + log1p(t), t = exp(-|v|), log1p(t) / t
+// on [0, 1] the polynomial of least relative error (3e-8; 2e-7 with its
+// roundings).  Steps of 1e-3 and less are what the map is used with: log2(1 + t)
+// would keep ten bits of them, and this takes half the operations of the series
+// of t / (2 + t).
 __device__ __forceinline__ float softplus(float v) {
-  const float m = fminf(fabsf(v), 128.f);
-  const float hi = m * kLog2e;
-  const float lo = fmaf(m, kLog2e, -hi) + m * 1.92596299e-8f;
-  float t = exp2_fast(-hi);
-  t = fmaf(t, -0.69314718f * lo, t);
-  const float s = t * __builtin_amdgcn_rcpf(2.f + t);
-  const float q = s * s;
-  float r = 2.f / 15.f;
-  r = fmaf(r, q, 2.f / 13.f);
-  r = fmaf(r, q, 2.f / 11.f);
-  r = fmaf(r, q, 2.f / 9.f);
-  r = fmaf(r, q, 2.f / 7.f);
-  r = fmaf(r, q, 2.f / 5.f);
-  r = fmaf(r, q, 2.f / 3.f);
-  r = fmaf(r * q, s, 2.f * s);
-  return (v < 0.f ? 0.f : v) + r;
+  const float t = exp2_fast(-kLog2e * fabsf(v));
+  float r = 0.005232690833508968f;
+  r = fmaf(r, t, -0.029505228623747826f);
+  r = fmaf(r, t, 0.07822594791650772f);
+  r = fmaf(r, t, -0.13663245737552643f);
+  r = fmaf(r, t, 0.19106008112430573f);
+  r = fmaf(r, t, -0.2484298199415207f);
+  r = fmaf(r, t, 0.3331909775733948f);
+  r = fmaf(r, t, -0.4999949336051941f);
+  r = fmaf(r, t, 0.9999999403953552f);
+  return fmaf(r, t, fmaxf(v, 0.f));
 }
 
 // log_re^2, finite with its product by log2(e) unless NaN: a step of length
@@ -167,6 +170,14 @@ struct Place {
   }
 };
 
+// An address the workgroup shares (in scalar registers) plus a lane's own 32 bits
+// of bytes: 32 rows of 2^24 steps of 4 bytes.
+template <typename T>
+__device__ __forceinline__ T* spot(T* shared, uint32_t bytes) {
+  return reinterpret_cast<T*>(
+      reinterpret_cast<char*>(const_cast<typename std::remove_const<T>::type*>(shared)) + bytes);
+}
+
 // The group's B and C over one tile and kModes modes, on their way to LDS.
 template <typename T, int NT, int TILE, bool BOTH>
 struct Stage {
@@ -176,13 +187,14 @@ struct Stage {
   // modes n0 .. of the tile from t0; steps at or past len are 0
   __device__ __forceinline__ void fetch(const T* Bm, const T* Cm, int N, int L, int n0, int t0,
                                         int len) {
+    const size_t first = (size_t)n0 * L + t0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       const int k = (int)threadIdx.x + i * NT;
-      const int t = t0 + (k % (TILE / 8)) * 8, n = n0 + k / (TILE / 8) % kModes;
+      const int t = (k % (TILE / 8)) * 8, n = k / (TILE / 8) % kModes;
       const bool second = BOTH && k >= kChunks / 2;
-      const int nv = (IT * NT == kChunks || k < kChunks) && n < N ? len - t : 0;
-      const T* from = (second ? Cm : Bm) + (size_t)min(n, N - 1) * L + t;
+      const int nv = (IT * NT == kChunks || k < kChunks) && n0 + n < N ? len - t0 - t : 0;
+      const T* from = spot((second ? Cm : Bm) + first, (uint32_t)(n * L + t) * sizeof(T));
       if (nv >= 8)
         v[i].load(from);
       else
@@ -203,32 +215,41 @@ struct Stage {
   }
 };
 
-// A lane's steps of one row as they lie in memory.
+// A lane's steps of one row as they lie in memory; row0: the workgroup's first
+// row at the tile's first step.
 template <typename T, int SP>
 struct Lane {
   Packed<T, SP> v;
-  __device__ __forceinline__ void fetch(const T* p, int nv) {
+  __device__ __forceinline__ void fetch(const T* row0, uint32_t own, int nv) {
     if (nv >= SP)
-      v.load(p);
+      v.load(spot(row0, own));
     else
-      v.load(p, max(nv, 0), (T)0.f);
+      v.load(spot(row0, own), max(nv, 0), (T)0.f);
   }
 };
 
-// What a lane does with one mode over its steps, given the state entering its
-// row's tile in the row's first lane: leaves the state entering its own first
-// step.  a: decays, b: drives.  next: (first lane) the state after the tile.
-template <int ST>
-__device__ __forceinline__ float enter_forward(const float* a, const float* b, float P,
-                                               float carry, bool first, float* next) {
-  float V = b[0];
+// The states entering a lane's first step, of M modes side by side, given those
+// entering the row's tile in its first lane.  a: decays, b: drives, P: decay over
+// the lane's steps.  next: (first lane) the states after the tile.
+template <int ST, int M>
+__device__ __forceinline__ void enter_forward(const float (*a)[ST], const float (*b)[ST], float* P,
+                                              const float* carry, bool first, float* x,
+                                              float* next) {
+  float V[M];
 #pragma unroll
-  for (int j = 1; j < ST; ++j) V = fmaf(a[j], V, b[j]);
-  V = fmaf(P, first ? carry : 0.f, V);
-  row_scan<false>(P, V);
-  const float r = row_move<kRowRor + 1>(V);
-  *next = r;
-  return first ? carry : r;
+  for (int i = 0; i < M; ++i) V[i] = b[i][0];
+#pragma unroll
+  for (int j = 1; j < ST; ++j)
+#pragma unroll
+    for (int i = 0; i < M; ++i) V[i] = fmaf(a[i][j], V[i], b[i][j]);
+#pragma unroll
+  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], first ? carry[i] : 0.f, V[i]);
+  row_scan<false, M>(P, V);
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    next[i] = row_move<kRowRor + 1>(V[i]);
+    x[i] = first ? carry[i] : next[i];
+  }
 }
 
 // Forward over a row or a segment of it.  RW groups of four rows, the modes of
@@ -244,7 +265,7 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
   __shared__ float4 yred[kJoinY ? RW * NW : 1][kJoinY ? NW : 1][kJoinY ? 64 : 1];
   extern __shared__ float dyn[];
   float* kap = dyn;               // [N][RP]
-  float* car = dyn + p.N * RP;    // [N][RP] state entering the tile
+  float* car = dyn + p.N * RP;    // [N][RP] state entering the tile, and a spare word
   const Place at(p);
   if (AGG && at.seg == p.nseg - 1) return;  // nobody joins the last segment
   const int lane = threadIdx.x & 63, seg = lane & (kSeg - 1);
@@ -276,23 +297,27 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
       car[n * RP + q] = c;
     }
   }
-  const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + (size_t)h * p.L;
-  const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + (size_t)h * p.L;
-  const T* z = static_cast<const T*>(p.z) + (p.z ? (size_t)(at.b * p.sz) + (size_t)h * p.L : 0);
+  const size_t first_row = (size_t)(at.g * p.HG + at.rb * R) * p.L;
+  const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + first_row;
+  const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + first_row;
+  const T* z = static_cast<const T*>(p.z) + (p.z ? (size_t)(at.b * p.sz) + first_row : 0);
   const T* Bm = static_cast<const T*>(p.Bm) + (size_t)(at.b * p.sB) + (size_t)at.g * p.N * p.L;
   const T* Cm = static_cast<const T*>(p.Cm) + (size_t)(at.b * p.sC) + (size_t)at.g * p.N * p.L;
+  T* out = static_cast<T*>(p.y) + row0 * p.L;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
   const float D = !AGG && p.D ? p.D[h] : 0.f;
   const int nblk = (p.N + kModes - 1) / kModes;
   const int off = seg * ST + nw * SP;  // the lane's own part of a tile
+  const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
+  // a row's first lane puts its states, the others the spare word: no branch
+  const int put = first ? p.N * RP + r : 2 * p.N * RP, pitch = first ? RP : 0;
   Stage<T, NT, TILE, !AGG> stage;
-  Lane<T, SP> un, dn, zn;
+  Lane<T, SP> un, dn;
   if (t_lo < t_live) {
     const int t = t_lo * TILE;
     stage.fetch(Bm, Cm, p.N, p.L, 0, t, len);
-    dn.fetch(delta + t + off, len - t - off);
-    un.fetch(u + t + off, len - t - off);
-    if (!AGG && p.z) zn.fetch(z + t + off, len - t - off);
+    dn.fetch(delta + t, mine, len - t - off);
+    un.fetch(u + t, mine, len - t - off);
   }
   float Sseg = 0.f;
   int buf = 0;
@@ -308,36 +333,45 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
             p.bounds[((row0 + q) * p.nchunk + (t0 >> 8)) * p.N + n] = car[n * RP + q];
       }
     }
-    const Lane<T, SP> uc = un, zc = zn;
-    float dt[ST], du[ST], y[ST];
+    Lane<T, SP> zc;
+    float dt[ST], du[ST], y[ST], skip[SP];
     {
       float own[2][SP];
 #pragma unroll
       for (int j = 0; j < SP; ++j) {
-        const float d = softplus(dn.v[j] + bias);
-        own[0][j] = j < nv ? d : 0.f;
-        own[1][j] = j < nv ? d * uc.v[j] : 0.f;
+        own[0][j] = softplus(dn.v[j] + bias);
+        own[1][j] = own[0][j] * un.v[j];
+        skip[j] = D * un.v[j];
+      }
+      if (t0 + TILE > len) {
+#pragma unroll
+        for (int j = 0; j < SP; ++j) {
+          own[0][j] = j < nv ? own[0][j] : 0.f;
+          own[1][j] = j < nv ? own[1][j] : 0.f;
+        }
       }
       if constexpr (NW == 1) {
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
           dt[j] = own[0][j];
           du[j] = own[1][j];
+          y[j] = skip[j];
         }
       } else {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
           xch[rg][m * NW + nw][lane] = make_float4(own[m][0], own[m][1], own[m][2], own[m][3]);
+#pragma unroll
+        for (int j = 0; j < ST; ++j) y[j] = 0.f;
       }
     }
+    // the gate is read for this tile's end, the rest for the next tile
+    if (!AGG && p.z) zc.fetch(z + t0, mine, nv);
     if (tile + 1 < t_live) {
-      const int t = t0 + TILE + off;
-      dn.fetch(delta + t, len - t);
-      un.fetch(u + t, len - t);
-      if (!AGG && p.z) zn.fetch(z + t, len - t);
+      const int t = t0 + TILE;
+      dn.fetch(delta + t, mine, len - t - off);
+      un.fetch(u + t, mine, len - t - off);
     }
-#pragma unroll
-    for (int j = 0; j < ST; ++j) y[j] = 0.f;
     float S = 0.f;
     for (int blk = 0; blk < nblk; ++blk) {
       stage.put(bc[buf]);
@@ -366,27 +400,43 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
         if (AGG) Sseg += S;
       }
       const int n0 = blk * kModes, nm = min(kModes, p.N - n0);
-      for (int m = nw; m < nm; m += NW) {
-        float* cell = car + (n0 + m) * RP + r;
-        const float k = kap[(n0 + m) * RP + r], carry = *cell;
-        float v[ST], a[ST], b[ST];
-        read_steps<ST>(bc[buf][0][m], seg, v);
+      // two modes at a time: the passes are chains, and two fill each other's waits
+      const auto walk = [&](auto count, int m) {
+        constexpr int M = decltype(count)::value;
+        float k[M], P[M], carry[M], x[M], next[M], v[M][ST], a[M][ST], b[M][ST];
 #pragma unroll
-        for (int j = 0; j < ST; ++j) {
-          a[j] = exp2_fast(-k * dt[j]);
-          b[j] = du[j] * v[j];
+        for (int i = 0; i < M; ++i) {
+          k[i] = kap[(n0 + m + i * NW) * RP + r];
+          carry[i] = car[(n0 + m + i * NW) * RP + r];
+          read_steps<ST>(bc[buf][0][m + i * NW], seg, b[i]);
         }
-        float next;
-        float x = enter_forward<ST>(a, b, exp2_fast(-k * S), carry, first, &next);
-        if (first) *cell = next;
-        if (AGG) continue;
-        read_steps<ST>(bc[buf][AGG ? 0 : 1][m], seg, v);
+        if (!AGG)
 #pragma unroll
-        for (int j = 0; j < ST; ++j) {
-          x = fmaf(a[j], x, b[j]);
-          y[j] = fmaf(v[j], x, y[j]);
+          for (int i = 0; i < M; ++i) read_steps<ST>(bc[buf][AGG ? 0 : 1][m + i * NW], seg, v[i]);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+#pragma unroll
+          for (int j = 0; j < ST; ++j) {
+            a[i][j] = exp2_fast(-k[i] * dt[j]);
+            b[i][j] *= du[j];
+          }
+          P[i] = exp2_fast(-k[i] * S);
         }
-      }
+        enter_forward<ST, M>(a, b, P, carry, first, x, next);
+#pragma unroll
+        for (int i = 0; i < M; ++i) dyn[put + (n0 + m + i * NW) * pitch] = next[i];
+        if (AGG) return;
+#pragma unroll
+        for (int j = 0; j < ST; ++j)
+#pragma unroll
+          for (int i = 0; i < M; ++i) {
+            x[i] = fmaf(a[i][j], x[i], b[i][j]);
+            y[j] = fmaf(v[i][j], x[i], y[j]);
+          }
+      };
+      int m = nw;
+      for (; m + NW < nm; m += 2 * NW) walk(std::integral_constant<int, 2>(), m);
+      if (m < nm) walk(std::integral_constant<int, 1>(), m);
       buf ^= 1;
     }
     if constexpr (AGG) {
@@ -400,7 +450,7 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
           yred[wave][k][lane] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < SP; ++j) own[j] = 0.f;
+        for (int j = 0; j < SP; ++j) own[j] = skip[j];
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
           const float4 a = yred[rg * NW + k][nw][lane];
@@ -415,13 +465,14 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
       }
 #pragma unroll
       for (int j = 0; j < SP; ++j) {
-        float v = fmaf(D, uc.v[j], own[j]), rest;
-        if (p.z) v *= zc.v[j] * sigmoid_pair(zc.v[j], &rest);
-        own[j] = j < nv ? v : 0.f;
+        float rest;
+        if (p.z) own[j] *= zc.v[j] * sigmoid_pair(zc.v[j], &rest);
       }
-      if (live)
-        store_n<T, SP>(static_cast<T*>(p.y) + ((size_t)at.b * p.H + h) * p.L + t0 + off,
-                       p.L - t0 - off, own);
+      if (t0 + TILE > len) {
+#pragma unroll
+        for (int j = 0; j < SP; ++j) own[j] = j < nv ? own[j] : 0.f;
+      }
+      if (live) store_n<T, SP>(spot(out + t0, mine), p.L - t0 - off, own);
     }
   }
   if (AGG) {
@@ -434,9 +485,7 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
       float zero[SP];
 #pragma unroll
       for (int j = 0; j < SP; ++j) zero[j] = 0.f;
-      if (live)
-        store_n<T, SP>(static_cast<T*>(p.y) + ((size_t)at.b * p.H + h) * p.L + t0 + off,
-                       p.L - t0 - off, zero);
+      if (live) store_n<T, SP>(spot(out + t0, mine), p.L - t0 - off, zero);
     }
   }
   // what leaves: the state after the row, or the segment's own part of it
@@ -532,23 +581,25 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
       car[n * RP + q] = 0.f;
     }
   }
-  const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + (size_t)h * p.L;
-  const T* z = static_cast<const T*>(p.z) + (p.z ? (size_t)(at.b * p.sz) + (size_t)h * p.L : 0);
-  const T* dy = static_cast<const T*>(p.dy) + ((size_t)at.b * p.H + h) * p.L;
+  const size_t first_row = (size_t)(at.g * p.HG + at.rb * R) * p.L;
+  const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + first_row;
+  const T* z = static_cast<const T*>(p.z) + (p.z ? (size_t)(at.b * p.sz) + first_row : 0);
+  const T* dy = static_cast<const T*>(p.dy) + row0 * p.L;
   const T* Cm = static_cast<const T*>(p.Cm) + (size_t)(at.b * p.sC) + (size_t)at.g * p.N * p.L;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
   const int nblk = (p.N + kModes - 1) / kModes;
   const int off = seg * ST;
+  const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
   Stage<T, NT, TILE, false> stage;
   if (t_lo < t_live) stage.fetch(Cm, Cm, p.N, p.L, 0, (t_live - 1) * TILE, len);
   float Sseg = 0.f;
   int buf = 0;
   for (int tile = t_live - 1; tile >= t_lo; --tile) {
-    const int t0 = tile * TILE, t = t0 + off, nv = len - t;
+    const int t0 = tile * TILE, nv = len - t0 - off;
     Lane<T, ST> dv, zv, gv;
-    dv.fetch(delta + t, nv);
-    gv.fetch(dy + t, nv);
-    if (p.z) zv.fetch(z + t, nv);
+    dv.fetch(delta + t0, mine, nv);
+    gv.fetch(dy + t0, mine, nv);
+    if (p.z) zv.fetch(z + t0, mine, nv);
     float dt[ST], gy[ST], S = 0.f;
 #pragma unroll
     for (int j = 0; j < ST; ++j) {
@@ -577,9 +628,9 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
 #pragma unroll
         for (int j = ST - 1; j >= 0; --j)
           F = exp2_fast(-k * dt[j]) * fmaf(v[j], gy[j], F);
-        const float P = exp2_fast(-k * S);
+        float P = exp2_fast(-k * S);
         F = fmaf(P, last ? carry : 0.f, F);
-        row_scan<true>(P, F);
+        row_scan<true, 1>(&P, &F);
         const float next = row_move<kRowRor + 15>(F);
         if (last) *cell = next;
       }
@@ -604,12 +655,14 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
 template <typename T, int ST, int RW, bool Z>
 __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
   constexpr int NT = 64 * RW, R = 4 * RW, RP = R + 1, TILE = kSeg * ST, Q = ST / 4;
+  typedef float Quad __attribute__((ext_vector_type(4)));
+  typedef typename std::conditional<Q == 4, Quad, float>::type Part;  // Q steps
   __shared__ float bc[2][2][kModes][TILE];
-  __shared__ float slab[2][RW][2][2][64 * Q];
+  __shared__ Part slab[2][RW][2][2][64];
   extern __shared__ float dyn[];
   float* kap = dyn;                  // [N][RP]
   float* car = dyn + p.N * RP;       // [N][RP] state gradient entering the tile
-  float* dre = dyn + 2 * p.N * RP;   // [N][RP] sum of w dt
+  float* dre = dyn + 2 * p.N * RP;   // [N][RP] sum of w dt, and a spare word
   const Place at(p);
   const int lane = threadIdx.x & 63, seg = lane & (kSeg - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -639,149 +692,179 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
       dre[n * RP + q] = 0.f;
     }
   }
-  const size_t rl = (size_t)h * p.L;
-  const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + rl;
-  const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + rl;
-  const T* z = static_cast<const T*>(p.z) + (Z ? (size_t)(at.b * p.sz) + rl : 0);
-  const T* dy = static_cast<const T*>(p.dy) + (size_t)at.b * p.H * p.L + rl;
-  T* du = static_cast<T*>(p.du) + (size_t)(at.b * p.sdu) + rl;
-  T* ddelta = static_cast<T*>(p.ddelta) + (size_t)(at.b * p.sdd) + rl;
-  T* dz = static_cast<T*>(p.dz) + (Z ? (size_t)(at.b * p.sdz) + rl : 0);
+  const size_t first_row = (size_t)(at.g * p.HG + at.rb * R) * p.L;
+  const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + first_row;
+  const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + first_row;
+  const T* z = static_cast<const T*>(p.z) + (Z ? (size_t)(at.b * p.sz) + first_row : 0);
+  const T* dy = static_cast<const T*>(p.dy) + row0 * p.L;
+  T* du = static_cast<T*>(p.du) + (size_t)(at.b * p.sdu) + first_row;
+  T* ddelta = static_cast<T*>(p.ddelta) + (size_t)(at.b * p.sdd) + first_row;
+  T* dz = static_cast<T*>(p.dz) + (Z ? (size_t)(at.b * p.sdz) + first_row : 0);
   const T* Bm = static_cast<const T*>(p.Bm) + (size_t)(at.b * p.sB) + (size_t)at.g * p.N * p.L;
   const T* Cm = static_cast<const T*>(p.Cm) + (size_t)(at.b * p.sC) + (size_t)at.g * p.N * p.L;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f, D = p.D ? p.D[h] : 0.f;
   const int nblk = (p.N + kModes - 1) / kModes;
   const int off = seg * ST;
+  const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
   const int Lp = p.nchunk * 256;
   float* part = p.part_bc +
                 (((size_t)at.rb * p.B + at.b) * p.G + at.g) * 2 * p.N * (size_t)Lp;
+  // the lanes that put a row's values; the others take the spare word: no branch
+  const int put_c = last ? p.N * RP + r : 3 * p.N * RP, pitch_c = last ? RP : 0;
+  const int put_d = first ? 2 * p.N * RP + r : 3 * p.N * RP, pitch_d = first ? RP : 0;
   // behind the rows' end: no gradients
   for (int tile = t_hi - 1; tile >= max(t_lo, t_live); --tile) {
-    const int t = tile * TILE + off;
+    const int t0 = tile * TILE, ns = p.L - t0 - off;
     float zero[ST];
 #pragma unroll
     for (int j = 0; j < ST; ++j) zero[j] = 0.f;
     if (live) {
-      store_n<T, ST>(du + t, p.L - t, zero);
-      store_n<T, ST>(ddelta + t, p.L - t, zero);
-      if (Z) store_n<T, ST>(dz + t, p.L - t, zero);
+      store_n<T, ST>(spot(du + t0, mine), ns, zero);
+      store_n<T, ST>(spot(ddelta + t0, mine), ns, zero);
+      if (Z) store_n<T, ST>(spot(dz + t0, mine), ns, zero);
     }
   }
   Stage<T, NT, TILE, true> stage;
-  if (t_lo < t_live) stage.fetch(Bm, Cm, p.N, p.L, 0, (t_live - 1) * TILE, len);
+  // the kept states of a stage's modes, one to each of a row's first lanes
+  float starts = 0.f;
+  const auto fetch_starts = [&](int n0, int t0) {
+    starts = 0.f;
+    if (live && seg < kModes && n0 + seg < p.N)
+      starts = p.bounds[((row0 + r) * p.nchunk + (t0 >> 8)) * p.N + n0 + seg];
+  };
+  if (t_lo < t_live) {
+    stage.fetch(Bm, Cm, p.N, p.L, 0, (t_live - 1) * TILE, len);
+    fetch_starts(0, (t_live - 1) * TILE);
+  }
   float sumD = 0.f, sumb = 0.f;
   int buf = 0, sb = 0;
   for (int tile = t_live - 1; tile >= t_lo; --tile) {
-    const int t0 = tile * TILE, t = t0 + off, nv = len - t;
+    const int t0 = tile * TILE, nv = len - t0 - off;
     float dt[ST], dtu[ST], gy[ST], y[ST], q[ST], w[ST], S = 0.f;
     {
       Lane<T, ST> uv, dv, zv, gv;
-      uv.fetch(u + t, nv);
-      dv.fetch(delta + t, nv);
-      gv.fetch(dy + t, nv);
-      if (Z) zv.fetch(z + t, nv);
+      uv.fetch(u + t0, mine, nv);
+      dv.fetch(delta + t0, mine, nv);
+      gv.fetch(dy + t0, mine, nv);
+      if (Z) zv.fetch(z + t0, mine, nv);
 #pragma unroll
       for (int j = 0; j < ST; ++j) {
         const float d = softplus(dv.v[j] + bias);
         float g = gv.v[j], rest;
         if (Z) g *= zv.v[j] * sigmoid_pair(zv.v[j], &rest);
-        dt[j] = j < nv ? d : 0.f;
-        dtu[j] = j < nv && live ? d * uv.v[j] : 0.f;
-        gy[j] = j < nv && live ? g : 0.f;
-        S += dt[j];
-        y[j] = q[j] = w[j] = 0.f;
+        dt[j] = d;
+        dtu[j] = d * uv.v[j];
+        gy[j] = g;
+        y[j] = D * uv.v[j];
+        q[j] = w[j] = 0.f;
       }
+      if (t0 + TILE > len || !live) {
+#pragma unroll
+        for (int j = 0; j < ST; ++j) {
+          dt[j] = j < nv ? dt[j] : 0.f;
+          dtu[j] = j < nv && live ? dtu[j] : 0.f;
+          gy[j] = j < nv && live ? gy[j] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < ST; ++j) S += dt[j];
     }
     for (int blk = 0; blk < nblk; ++blk) {
       stage.put(bc[buf]);
+      float start = starts;
       __syncthreads();
-      if (blk + 1 < nblk)
+      if (blk + 1 < nblk) {
         stage.fetch(Bm, Cm, p.N, p.L, (blk + 1) * kModes, t0, len);
-      else if (tile > t_lo)
+        fetch_starts((blk + 1) * kModes, t0);
+      } else if (tile > t_lo) {
         stage.fetch(Bm, Cm, p.N, p.L, 0, t0 - TILE, len);
+        fetch_starts(0, t0 - TILE);
+      }
       const int n0 = blk * kModes, nm = min(kModes, p.N - n0);
       for (int m = 0; m < nm; ++m) {
         const int n = n0 + m;
-        const float k = kap[n * RP + r];
-        const float start =
-            live ? p.bounds[((row0 + r) * p.nchunk + (t0 >> 8)) * p.N + n] : 0.f;
-        float v[ST], a[ST], ax[ST], c[ST];
-        float dC[ST];
+        const float k = kap[n * RP + r], carry = car[n * RP + r], was = dre[n * RP + r];
+        float v[ST], a[1][ST], ax[ST], c[1][ST], g[ST];
         read_steps<ST>(bc[buf][0][m], seg, v);
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
-          a[j] = exp2_fast(-k * dt[j]);
-          c[j] = dtu[j] * v[j];
+          a[0][j] = exp2_fast(-k * dt[j]);
+          c[0][j] = dtu[j] * v[j];
         }
-        const float P = exp2_fast(-k * S);
-        float next;
-        float x = enter_forward<ST>(a, c, P, start, first, &next);
+        const float decay = exp2_fast(-k * S);
+        float P = decay, next, x;
+        enter_forward<ST, 1>(a, c, &P, &start, first, &x, &next);
+        start = row_move<kRowShl + 1>(start);  // the next mode's to the first lane
         float cv[ST];
         read_steps<ST>(bc[buf][1][m], seg, cv);
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
-          ax[j] = a[j] * x;
-          x = ax[j] + c[j];
+          ax[j] = a[0][j] * x;
+          x = ax[j] + c[0][j];
           if (Z) y[j] = fmaf(cv[j], x, y[j]);
-          dC[j] = gy[j] * x;
-          c[j] = cv[j] * gy[j];
+          g[j] = gy[j] * x;
+          c[0][j] = cv[j] * gy[j];
         }
-        float* mine = &slab[sb][wave][m & 1][1][lane * Q];
+        const auto leave = [&](int which) {
+          float o[Q];
 #pragma unroll
-        for (int i = 0; i < Q; ++i)
-          mine[i] = rows_quad(dC[i], dC[Q + i], dC[2 * Q + i], dC[3 * Q + i]);
+          for (int i = 0; i < Q; ++i) o[i] = rows_quad(g[i], g[Q + i], g[2 * Q + i], g[3 * Q + i]);
+          Part to;
+          if constexpr (Q == 4)
+            to = Part{o[0], o[1], o[2], o[3]};
+          else
+            to = o[0];
+          slab[sb][wave][m & 1][which][lane] = to;
+        };
+        leave(1);
         // against time
-        float F = c[ST - 1];
+        float F = c[0][ST - 1];
 #pragma unroll
-        for (int j = ST - 2; j >= 0; --j) F = fmaf(a[j + 1], F, c[j]);
-        F *= a[0];
-        float* cell = car + n * RP + r;
-        const float carry = *cell;
+        for (int j = ST - 2; j >= 0; --j) F = fmaf(a[0][j + 1], F, c[0][j]);
+        F *= a[0][0];
+        P = decay;
         F = fmaf(P, last ? carry : 0.f, F);
-        row_scan<true>(P, F);
+        row_scan<true, 1>(&P, &F);
         const float out = row_move<kRowRor + 15>(F);
-        if (last) *cell = out;
+        dyn[put_c + n * pitch_c] = out;
         float G = last ? carry : out;
-        float acc = 0.f, dB[ST];
-        // G here: a_{j+1} G_{j+1}, then G_j
+        float acc = 0.f;
 #pragma unroll
         for (int j = ST - 1; j >= 0; --j) {
-          G = j == ST - 1 ? G + c[j] : fmaf(a[(j + 1) % ST], G, c[j]);
+          G = j == ST - 1 ? G + c[0][j] : fmaf(a[0][(j + 1) % ST], G, c[0][j]);
           const float wx = G * ax[j];
-          dB[j] = G * dtu[j];
+          g[j] = G * dtu[j];
           q[j] = fmaf(G, v[j], q[j]);
           w[j] = fmaf(k, wx, w[j]);
           acc = fmaf(wx, dt[j], acc);
         }
-        mine = &slab[sb][wave][m & 1][0][lane * Q];
-#pragma unroll
-        for (int i = 0; i < Q; ++i)
-          mine[i] = rows_quad(dB[i], dB[Q + i], dB[2 * Q + i], dB[3 * Q + i]);
-        acc = row_total(acc);
-        if (first) dre[n * RP + r] += acc;
+        leave(0);
+        dyn[put_d + n * pitch_d] = was + row_total(acc);
         if ((m & 1) || m + 1 == nm) {
           // one barrier for two modes: the slabs alternate
           __syncthreads();
-          const int count = 64 * Q * 2 * ((m & 1) + 1);
+          const int count = 128 * ((m & 1) + 1);
           for (int i = threadIdx.x; i < count; i += NT) {
-            const int e = i % (64 * Q), which = i / (64 * Q) & 1, mm = i / (128 * Q);
-            float s = 0.f;
+            const int e = i & 63, which = i / 64 & 1, mm = i / 128;
+            Part sum = slab[sb][0][mm][which][e];
 #pragma unroll
-            for (int k2 = 0; k2 < RW; ++k2) s += slab[sb][k2][mm][which][e];
-            const int ln = e / Q, st = (ln & 15) * ST + (ln >> 4) * Q + e % Q;
-            part[(size_t)(which * p.N + (m & ~1) + n0 + mm) * Lp + t0 + st] = s;
+            for (int o = 1; o < RW; ++o) sum += slab[sb][o][mm][which][e];
+            const int st = (e & 15) * ST + (e >> 4) * Q;
+            *reinterpret_cast<Part*>(part + (size_t)(which * p.N + n0 + (m & ~1) + mm) * Lp + t0 +
+                                     st) = sum;
           }
           sb ^= 1;
         }
       }
       buf ^= 1;
     }
+    // the inputs again, from a cache: held through the modes they would not fit the registers
     Lane<T, ST> uv, dv, zv, gv;
-    uv.fetch(u + t, nv);
-    dv.fetch(delta + t, nv);
+    uv.fetch(u + t0, mine, nv);
+    dv.fetch(delta + t0, mine, nv);
     if (Z) {
-      gv.fetch(dy + t, nv);
-      zv.fetch(z + t, nv);
+      gv.fetch(dy + t0, mine, nv);
+      zv.fetch(z + t0, mine, nv);
     }
     float o[3][ST];
 #pragma unroll
@@ -797,14 +880,15 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
       }
       if (Z) {
         const float s = sigmoid_pair(zv.v[j], &rest);
-        const float e = gv.v[j] * fmaf(D, uj, y[j]) * fmaf(zv.v[j] * s, rest, s);
+        const float e = gv.v[j] * y[j] * fmaf(zv.v[j] * s, rest, s);
         o[2][j] = j < nv ? e : 0.f;
       }
     }
     if (live) {
-      store_n<T, ST>(du + t, p.L - t, o[0]);
-      store_n<T, ST>(ddelta + t, p.L - t, o[1]);
-      if (Z) store_n<T, ST>(dz + t, p.L - t, o[2]);
+      const int ns = p.L - t0 - off;
+      store_n<T, ST>(spot(du + t0, mine), ns, o[0]);
+      store_n<T, ST>(spot(ddelta + t0, mine), ns, o[1]);
+      if (Z) store_n<T, ST>(spot(dz + t0, mine), ns, o[2]);
     }
   }
   sumD = row_total(sumD);
@@ -1034,7 +1118,7 @@ unsigned blocks_of(long n) { return (unsigned)((n + 255) / 256); }
 template <typename T, int ST, int RW, int NW>
 hipError_t forward(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)a.B * a.G * a.nrb * a.nseg), block(64 * RW * NW);
-  const size_t lds = 2 * (size_t)a.N * (4 * RW + 1) * sizeof(float);
+  const size_t lds = (2 * (size_t)a.N * (4 * RW + 1) + 1) * sizeof(float);
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
     hipLaunchKernelGGL((selective_join_kernel<false>), dim3(blocks_of((long)a.B * a.H * a.N)),
@@ -1065,9 +1149,9 @@ hipError_t backward(const Args& a, hipStream_t st) {
                        a.nseg);
   }
   if (a.z)
-    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, true>), grid, block, 3 * lds, st, a);
+    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, true>), grid, block, 3 * lds + 4, st, a);
   else
-    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, false>), grid, block, 3 * lds, st, a);
+    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, false>), grid, block, 3 * lds + 4, st, a);
   if (a.L > 0)
     hipLaunchKernelGGL((selective_dbc_kernel<T>),
                        dim3((unsigned)a.B * a.G * 2 * a.N * (unsigned)((a.L + 1023) / 1024)),
