@@ -628,7 +628,7 @@ int dssm_shortconv_backward(const void* u, long long stride_b, const float* w, c
                             const void* dy, const float* dx_end, const dssm_shortconv_grads* g,
                             void* ws, size_t ws_bytes, void* stream);
 
-#define DSSM_SELECTIVE_CHUNK 256 /* steps between two kept states */
+#define DSSM_SELECTIVE_CHUNK 128 /* steps between two kept states */
 
 typedef struct {
   int B, H, L;
@@ -671,10 +671,10 @@ typedef struct {
 
 /* Bytes of workspace of dssm_selective_forward or (backward != 0)
  * dssm_selective_backward (host only).  Requires H <= 65535, B H <= 2^24, L <=
- * 2^24, B H L <= 2^40, B H N ceil(L / 256) <= 2^36. */
+ * 2^24, B H L <= 2^40, B H N ceil(L / 128) <= 2^36. */
 int dssm_selective_workspace_size(const dssm_selective_shape* s, int backward, size_t* bytes);
 
-/* Bytes of a checkpoint: the states [B, H, ceil(L / 256), N] float32 entering
+/* Bytes of a checkpoint: the states [B, H, ceil(L / 128), N] float32 entering
  * the chunks (those of a row's dead chunks are not written), padded to 256. */
 int dssm_selective_ckpt_size(const dssm_selective_shape* s, size_t* bytes);
 

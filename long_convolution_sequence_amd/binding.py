@@ -31,7 +31,7 @@ GATED_CHUNK, CKPT8_GROUP = 512, 64
 NORM_RMS, NORM_LAYER = 0, 1
 Q8_INT8, Q8_E4M3 = 0, 1  # the norm's output in 8 bits
 ACT_NONE, ACT_SILU = 0, 1  # after the short convolution
-SELECTIVE_CHUNK = 256  # steps between the states a selective scan keeps
+SELECTIVE_CHUNK = 128  # steps between the states a selective scan keeps
 
 # Every function the header declares (checked by the ABI tests).
 EXPORTS = [
@@ -1316,7 +1316,7 @@ def selective_forward(u, delta, Bm, Cm, log_re, D=None, dt_bias=None, z=None, x=
 def selective_forward_ckpt(u, delta, Bm, Cm, log_re, D=None, dt_bias=None, z=None, x=None,
                            x_out=None, lens=None, y=None, ckpt=None, workspace=None, stream=None):
     """selective_forward that keeps what selective_backward needs, the states
-    entering every 256 steps: returns (y, ckpt)."""
+    entering every 128 steps: returns (y, ckpt)."""
     return _selective_forward(u, delta, Bm, Cm, log_re, D, dt_bias, z, x, x_out, lens, y, True,
                               ckpt, workspace, stream)
 

@@ -93,8 +93,8 @@ int check_selective(const dssm_selective_shape* s, bool* empty) {
     return fail(DSSM_ERR_INVALID_ARG, "selective: H=%d is not a multiple of G=%d", s->H, s->G);
   if ((long)s->B * s->H > kMaxRows)
     return fail(DSSM_ERR_UNSUPPORTED, "selective: B*H=%ld exceeds 2^24", (long)s->B * s->H);
-  if ((__int128)s->B * s->H * s->N * ((s->L + 255) / 256) > ((__int128)1 << 36))
-    return fail(DSSM_ERR_UNSUPPORTED, "selective: B*H*N*ceil(L/256) exceeds 2^36");
+  if ((__int128)s->B * s->H * s->N * ((s->L + 127) / 128) > ((__int128)1 << 36))
+    return fail(DSSM_ERR_UNSUPPORTED, "selective: B*H*N*ceil(L/128) exceeds 2^36");
   return DSSM_OK;
 }
 

@@ -34,8 +34,10 @@ namespace dssm {
 namespace {
 
 constexpr int kSeg = 16;  // lanes of a row
+constexpr int kKeep = 128; // steps between two kept states
 constexpr int kModes = 8; // modes whose B and C are in LDS at once
-constexpr int kRowShl = 0x100, kRowShr = 0x110, kRowRor = 0x120;
+constexpr int kPair = 2;  // modes a wave walks side by side
+constexpr int kRowShl = 0x100, kRowRor = 0x120;
 
 struct Args {
   const void *u, *delta, *z, *Bm, *Cm;
@@ -58,31 +60,62 @@ struct Args {
   void *du, *ddelta, *dz, *dB, *dC;
   long long sdu, sdd, sdz, sdB, sdC;
   float *dlog_re, *dD, *ddt_bias, *dx0;
-  float* part_bc;         // [nrb][B][G][2][N][nchunk * 256]
+  float* part_bc;         // [nrb][B][G][2][N][nchunk kKeep]
   float* part_n;          // [rows][nseg][N]
   float* part_h;          // [rows][nseg][2]
 };
 
 // Inclusive scan over a row's 16 lanes, in time order or (REV) against it, of
-// x -> P x + V.  A lane without a neighbour joins 0 (what row_move gives there);
-// its P, 0 from there on, meets no further neighbour.
-template <bool REV, int M>
-__device__ __forceinline__ void row_scan(float* P, float* V) {
-  constexpr int S = REV ? kRowShl : kRowShr;
-#pragma unroll
-  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 1>(V[i]), V[i]);
-#pragma unroll
-  for (int i = 0; i < M; ++i) P[i] *= row_move<S + 1>(P[i]);
-#pragma unroll
-  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 2>(V[i]), V[i]);
-#pragma unroll
-  for (int i = 0; i < M; ++i) P[i] *= row_move<S + 2>(P[i]);
-#pragma unroll
-  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 4>(V[i]), V[i]);
-#pragma unroll
-  for (int i = 0; i < M; ++i) P[i] *= row_move<S + 4>(P[i]);
-#pragma unroll
-  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], row_move<S + 8>(V[i]), V[i]);
+// x -> P x + V, and what each lane's neighbour leaves (0 at the first lane).  A
+// lane without a neighbour joins 0; its P, 0 from there on, meets no further
+// neighbour.  In assembly, as the compiler moves a lane's value first and adds
+// it in an instruction of its own.  A lane's value is read two wait states after
+// it is written at the earliest.
+#define DSSM_ROW(dir, n) "row_sh" dir ":" n " row_mask:0xf bank_mask:0xf bound_ctrl:1\n\t"
+#define DSSM_SCAN1(dir)                                                   \
+  "s_nop 1\n\t"                                                          \
+  "v_fmac_f32_dpp %0, %0, %1 " DSSM_ROW(dir, "1")                         \
+  "v_mul_f32_dpp %1, %1, %1 " DSSM_ROW(dir, "1") "s_nop 0\n\t"           \
+  "v_fmac_f32_dpp %0, %0, %1 " DSSM_ROW(dir, "2")                         \
+  "v_mul_f32_dpp %1, %1, %1 " DSSM_ROW(dir, "2") "s_nop 0\n\t"           \
+  "v_fmac_f32_dpp %0, %0, %1 " DSSM_ROW(dir, "4")                         \
+  "v_mul_f32_dpp %1, %1, %1 " DSSM_ROW(dir, "4") "s_nop 0\n\t"           \
+  "v_fmac_f32_dpp %0, %0, %1 " DSSM_ROW(dir, "8") "s_nop 1\n\t"          \
+  "v_mov_b32_dpp %2, %0 " DSSM_ROW(dir, "1")
+#define DSSM_SCAN2(dir)                                                   \
+  "s_nop 1\n\t"                                                          \
+  "v_fmac_f32_dpp %0, %0, %2 " DSSM_ROW(dir, "1")                         \
+  "v_fmac_f32_dpp %1, %1, %3 " DSSM_ROW(dir, "1")                         \
+  "v_mul_f32_dpp %2, %2, %2 " DSSM_ROW(dir, "1")                          \
+  "v_mul_f32_dpp %3, %3, %3 " DSSM_ROW(dir, "1")                          \
+  "v_fmac_f32_dpp %0, %0, %2 " DSSM_ROW(dir, "2")                         \
+  "v_fmac_f32_dpp %1, %1, %3 " DSSM_ROW(dir, "2")                         \
+  "v_mul_f32_dpp %2, %2, %2 " DSSM_ROW(dir, "2")                          \
+  "v_mul_f32_dpp %3, %3, %3 " DSSM_ROW(dir, "2")                          \
+  "v_fmac_f32_dpp %0, %0, %2 " DSSM_ROW(dir, "4")                         \
+  "v_fmac_f32_dpp %1, %1, %3 " DSSM_ROW(dir, "4")                         \
+  "v_mul_f32_dpp %2, %2, %2 " DSSM_ROW(dir, "4")                          \
+  "v_mul_f32_dpp %3, %3, %3 " DSSM_ROW(dir, "4")                          \
+  "v_fmac_f32_dpp %0, %0, %2 " DSSM_ROW(dir, "8")                         \
+  "v_fmac_f32_dpp %1, %1, %3 " DSSM_ROW(dir, "8") "s_nop 0\n\t"          \
+  "v_mov_b32_dpp %4, %0 " DSSM_ROW(dir, "1")                              \
+  "v_mov_b32_dpp %5, %1 " DSSM_ROW(dir, "1")
+
+template <bool REV>
+__device__ __forceinline__ void row_scan(float (&P)[1], float (&V)[1], float (&in)[1]) {
+  if (REV)
+    asm(DSSM_SCAN1("l") : "+v"(V[0]), "+v"(P[0]), "=&v"(in[0]));
+  else
+    asm(DSSM_SCAN1("r") : "+v"(V[0]), "+v"(P[0]), "=&v"(in[0]));
+}
+template <bool REV>
+__device__ __forceinline__ void row_scan(float (&P)[2], float (&V)[2], float (&in)[2]) {
+  if (REV)
+    asm(DSSM_SCAN2("l")
+        : "+v"(V[0]), "+v"(V[1]), "+v"(P[0]), "+v"(P[1]), "=&v"(in[0]), "=&v"(in[1]));
+  else
+    asm(DSSM_SCAN2("r")
+        : "+v"(V[0]), "+v"(V[1]), "+v"(P[0]), "+v"(P[1]), "=&v"(in[0]), "=&v"(in[1]));
 }
 
 // x summed over a row's 16 lanes; all of them get the sum.
@@ -129,7 +162,7 @@ __device__ __forceinline__ int row_len(const Args& p, int b) {
 // 16 lanes read 16 bytes each from all banks.
 template <int ST>
 __device__ __forceinline__ int slot(int seg, int j) {
-  if (ST == 16) return seg * 16 + 4 * (j ^ (seg >> 2));
+  if (ST == 8) return seg * 8 + 4 * (j ^ (seg >> 3));
   return seg * 4;
 }
 
@@ -151,7 +184,7 @@ __device__ __forceinline__ void write_steps(float* tile, int t, const float* v) 
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int q = t / 4 + k;
-    float* to = tile + (ST == 16 ? slot<ST>(q / 4, q % 4) : slot<ST>(q, 0));
+    float* to = tile + slot<ST>(q / (ST / 4), q % (ST / 4));
     *reinterpret_cast<float4*>(to) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
   }
 }
@@ -170,12 +203,22 @@ struct Place {
   }
 };
 
+// A lane number the compiler knows nothing of: addresses derived from it are
+// formed where they are used instead of being kept in registers through a loop.
+__device__ __forceinline__ int opaque(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // An address the workgroup shares (in scalar registers) plus a lane's own 32 bits
 // of bytes: 32 rows of 2^24 steps of 4 bytes.
+// The lane's part is made opaque: as loop-invariant sums the compiler would keep
+// every tensor's whole address in vector registers.
 template <typename T>
 __device__ __forceinline__ T* spot(T* shared, uint32_t bytes) {
   return reinterpret_cast<T*>(
-      reinterpret_cast<char*>(const_cast<typename std::remove_const<T>::type*>(shared)) + bytes);
+      reinterpret_cast<char*>(const_cast<typename std::remove_const<T>::type*>(shared)) +
+      (uint32_t)opaque((int)bytes));
 }
 
 // The group's B and C over one tile and kModes modes, on their way to LDS.
@@ -190,7 +233,7 @@ struct Stage {
     const size_t first = (size_t)n0 * L + t0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int k = (int)threadIdx.x + i * NT;
+      const int k = opaque((int)threadIdx.x) + i * NT;
       const int t = (k % (TILE / 8)) * 8, n = k / (TILE / 8) % kModes;
       const bool second = BOTH && k >= kChunks / 2;
       const int nv = (IT * NT == kChunks || k < kChunks) && n0 + n < N ? len - t0 - t : 0;
@@ -204,7 +247,7 @@ struct Stage {
   __device__ __forceinline__ void put(float (*to)[kModes][TILE]) const {
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int k = (int)threadIdx.x + i * NT;
+      const int k = opaque((int)threadIdx.x) + i * NT;
       if (IT * NT != kChunks && k >= kChunks) break;
       float f[8];
 #pragma unroll
@@ -228,44 +271,57 @@ struct Lane {
   }
 };
 
-// The states entering a lane's first step, of M modes side by side, given those
-// entering the row's tile in its first lane.  a: decays, b: drives, P: decay over
-// the lane's steps.  next: (first lane) the states after the tile.
+__host__ __device__ inline int padded(int N) { return (N + kModes - 1) / kModes * kModes; }
+
+// The states entering a lane's first step, of M modes side by side.  a: decays,
+// b: drives, P: decay over the lane's steps; carry: in a row's first lane the
+// state entering the tile, in the others 0.  end: in its last lane the state
+// after the tile.
 template <int ST, int M>
-__device__ __forceinline__ void enter_forward(const float (*a)[ST], const float (*b)[ST], float* P,
-                                              const float* carry, bool first, float* x,
-                                              float* next) {
-  float V[M];
+__device__ __forceinline__ void enter_forward(const float (&a)[M][ST], const float (&b)[M][ST],
+                                              float (&P)[M], const float (&carry)[M],
+                                              float (&x)[M], float (&end)[M]) {
 #pragma unroll
-  for (int i = 0; i < M; ++i) V[i] = b[i][0];
+  for (int i = 0; i < M; ++i) end[i] = b[i][0];
 #pragma unroll
   for (int j = 1; j < ST; ++j)
 #pragma unroll
-    for (int i = 0; i < M; ++i) V[i] = fmaf(a[i][j], V[i], b[i][j]);
+    for (int i = 0; i < M; ++i) end[i] = fmaf(a[i][j], end[i], b[i][j]);
 #pragma unroll
-  for (int i = 0; i < M; ++i) V[i] = fmaf(P[i], first ? carry[i] : 0.f, V[i]);
-  row_scan<false, M>(P, V);
+  for (int i = 0; i < M; ++i) end[i] = fmaf(P[i], carry[i], end[i]);
+  row_scan<false>(P, end, x);
 #pragma unroll
-  for (int i = 0; i < M; ++i) {
-    next[i] = row_move<kRowRor + 1>(V[i]);
-    x[i] = first ? carry[i] : next[i];
-  }
+  for (int i = 0; i < M; ++i) x[i] += carry[i];
 }
+
+// A workgroup's values of every row and mode, in LDS: a row's first (or last)
+// lane has the value, the others find zeros to read and a place to write that
+// nobody reads, at the same distances: no branch and no address per mode.
+// pitch: modes, rounded up to what the waves take at once.
+struct Cells {
+  float* at;  // [R][pitch], then pitch zeros, then pitch spare
+  int R, pitch;
+  __device__ __forceinline__ float* row(int r) const { return at + r * pitch; }
+  __device__ __forceinline__ float* from(int r, bool mine) const { return row(mine ? r : R); }
+  __device__ __forceinline__ float* to(int r, bool mine) const { return row(mine ? r : R + 1); }
+};
 
 // Forward over a row or a segment of it.  RW groups of four rows, the modes of
 // each shared out among NW waves: with NW > 1 every wave forms a part of the
 // lanes' step sizes, and of their outputs.  AGG: only the segment's ends.
 template <typename T, int ST, int RW, int NW, bool AGG>
-__global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
-  constexpr int NT = 64 * RW * NW, R = 4 * RW, RP = R + 1, TILE = kSeg * ST, SP = ST / NW;
-  static_assert(NW == 1 || SP == 4, "the waves of a row exchange 16 bytes a lane");
+__global__ __launch_bounds__(64 * RW * NW) __attribute__((amdgpu_waves_per_eu(4)))
+void selective_fwd_kernel(Args p) {
+  constexpr int NT = 64 * RW * NW, R = 4 * RW, TILE = kSeg * ST, SP = ST / NW;
+  constexpr int QS = ST / 4, QP = SP / 4;  // a lane's, and its own part's, groups of four steps
+  static_assert(SP % 4 == 0, "the waves of a row exchange 16 bytes a lane");
   __shared__ float bc[2][AGG ? 1 : 2][kModes][TILE];
-  __shared__ float4 xch[NW > 1 ? RW : 1][NW > 1 ? 2 * NW : 1][NW > 1 ? 64 : 1];
+  __shared__ float4 xch[NW > 1 ? RW : 1][2][NW > 1 ? QS : 1][NW > 1 ? 64 : 1];
   constexpr bool kJoinY = NW > 1 && !AGG;
-  __shared__ float4 yred[kJoinY ? RW * NW : 1][kJoinY ? NW : 1][kJoinY ? 64 : 1];
+  __shared__ float4 yred[kJoinY ? RW * NW : 1][kJoinY ? QS : 1][kJoinY ? 64 : 1];
   extern __shared__ float dyn[];
-  float* kap = dyn;               // [N][RP]
-  float* car = dyn + p.N * RP;    // [N][RP] state entering the tile, and a spare word
+  const int NP = padded(p.N);
+  const Cells kap{dyn, R, NP}, car{dyn + R * NP, R, NP};  // log_re^2; the state entering the tile
   const Place at(p);
   if (AGG && at.seg == p.nseg - 1) return;  // nobody joins the last segment
   const int lane = threadIdx.x & 63, seg = lane & (kSeg - 1);
@@ -284,19 +340,23 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int q = rg * 4 + k;
-    for (int n = lane * NW + nw; n < p.N; n += 64 * NW) {
+    for (int n = lane * NW + nw; n < NP; n += 64 * NW) {
       float c = 0.f, s = 0.f;
-      if (q < nrow) {
+      if (q < nrow && n < p.N) {
         s = square_of(p.log_re[(size_t)(row0 - (size_t)at.b * p.H + q) * p.N + n]) * kLog2e;
         if (!AGG && p.nseg > 1)
           c = p.agg[((row0 + q) * p.nseg + at.seg) * p.N + n];
         else if (!AGG && p.x0)
           c = p.x0[(row0 + q) * p.N + n];
       }
-      kap[n * RP + q] = s;
-      car[n * RP + q] = c;
+      kap.row(q)[n] = s;
+      car.row(q)[n] = c;
     }
   }
+  for (int n = threadIdx.x; n < NP; n += NT) car.row(R)[n] = 0.f;  // before the first barrier
+  const float* krow = kap.row(r) + nw;
+  const float* from = car.from(r, first) + nw;
+  float* to = car.to(r, seg == kSeg - 1) + nw;
   const size_t first_row = (size_t)(at.g * p.HG + at.rb * R) * p.L;
   const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + first_row;
   const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + first_row;
@@ -309,8 +369,6 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
   const int nblk = (p.N + kModes - 1) / kModes;
   const int off = seg * ST + nw * SP;  // the lane's own part of a tile
   const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
-  // a row's first lane puts its states, the others the spare word: no branch
-  const int put = first ? p.N * RP + r : 2 * p.N * RP, pitch = first ? RP : 0;
   Stage<T, NT, TILE, !AGG> stage;
   Lane<T, SP> un, dn;
   if (t_lo < t_live) {
@@ -322,15 +380,15 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
   float Sseg = 0.f;
   int buf = 0;
   for (int tile = t_lo; tile < t_live; ++tile) {
-    const int t0 = tile * TILE, nv = len - t0 - off;
-    // the states entering a chunk of 256 steps, for the backward pass
-    if (!AGG && p.bounds && (t0 & 255) == 0) {
+    const int t0 = tile * TILE, nv = len - t0 - off, ln = opaque(lane);
+    // the states entering a chunk, for the backward pass
+    if (!AGG && p.bounds && (t0 & (kKeep - 1)) == 0) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int q = rg * 4 + k;
         if (q < nrow)
-          for (int n = lane * NW + nw; n < p.N; n += 64 * NW)
-            p.bounds[((row0 + q) * p.nchunk + (t0 >> 8)) * p.N + n] = car[n * RP + q];
+          for (int n = ln * NW + nw; n < p.N; n += 64 * NW)
+            p.bounds[((row0 + q) * p.nchunk + t0 / kKeep) * p.N + n] = car.row(q)[n];
       }
     }
     Lane<T, SP> zc;
@@ -360,7 +418,10 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
       } else {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          xch[rg][m * NW + nw][lane] = make_float4(own[m][0], own[m][1], own[m][2], own[m][3]);
+#pragma unroll
+          for (int i = 0; i < QP; ++i)
+            xch[rg][m][nw * QP + i][ln] = make_float4(own[m][4 * i], own[m][4 * i + 1],
+                                                        own[m][4 * i + 2], own[m][4 * i + 3]);
 #pragma unroll
         for (int j = 0; j < ST; ++j) y[j] = 0.f;
       }
@@ -385,8 +446,8 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
       if (blk == 0) {
         if constexpr (NW > 1) {
 #pragma unroll
-          for (int k = 0; k < NW; ++k) {
-            const float4 a = xch[rg][k][lane], b = xch[rg][NW + k][lane];
+          for (int k = 0; k < QS; ++k) {
+            const float4 a = xch[rg][0][k][ln], b = xch[rg][1][k][ln];
             const float va[4] = {a.x, a.y, a.z, a.w}, vb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -399,33 +460,31 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
         for (int j = 0; j < ST; ++j) S += dt[j];
         if (AGG) Sseg += S;
       }
-      const int n0 = blk * kModes, nm = min(kModes, p.N - n0);
-      // two modes at a time: the passes are chains, and two fill each other's waits
-      const auto walk = [&](auto count, int m) {
-        constexpr int M = decltype(count)::value;
-        float k[M], P[M], carry[M], x[M], next[M], v[M][ST], a[M][ST], b[M][ST];
+      const int n0 = blk * kModes, nm = p.N - n0;
+      // two modes at a time: the passes are chains, and two fill each other's
+      // waits.  Modes past the last one are zeros.
+      const auto walk = [&](auto step) {
+        constexpr int M = kPair, m0 = decltype(step)::value * M * NW;
+        __builtin_amdgcn_sched_barrier(0);  // steps mixed together would not fit the registers
+        float P[M], carry[M], x[M], end[M], v[M][ST], a[M][ST], b[M][ST];
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-          k[i] = kap[(n0 + m + i * NW) * RP + r];
-          carry[i] = car[(n0 + m + i * NW) * RP + r];
-          read_steps<ST>(bc[buf][0][m + i * NW], seg, b[i]);
-        }
-        if (!AGG)
-#pragma unroll
-          for (int i = 0; i < M; ++i) read_steps<ST>(bc[buf][AGG ? 0 : 1][m + i * NW], seg, v[i]);
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
+          const float k = krow[n0 + m0 + i * NW];
+          carry[i] = from[n0 + m0 + i * NW];
+          read_steps<ST>(bc[buf][0][m0 + i * NW + nw], seg, b[i]);
 #pragma unroll
           for (int j = 0; j < ST; ++j) {
-            a[i][j] = exp2_fast(-k[i] * dt[j]);
+            a[i][j] = exp2_fast(-k * dt[j]);
             b[i][j] *= du[j];
           }
-          P[i] = exp2_fast(-k[i] * S);
+          P[i] = exp2_fast(-k * S);
         }
-        enter_forward<ST, M>(a, b, P, carry, first, x, next);
+        enter_forward<ST, M>(a, b, P, carry, x, end);
 #pragma unroll
-        for (int i = 0; i < M; ++i) dyn[put + (n0 + m + i * NW) * pitch] = next[i];
+        for (int i = 0; i < M; ++i) to[n0 + m0 + i * NW] = end[i];
         if (AGG) return;
+#pragma unroll
+        for (int i = 0; i < M; ++i) read_steps<ST>(bc[buf][AGG ? 0 : 1][m0 + i * NW + nw], seg, v[i]);
 #pragma unroll
         for (int j = 0; j < ST; ++j)
 #pragma unroll
@@ -434,9 +493,12 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
             y[j] = fmaf(v[i][j], x[i], y[j]);
           }
       };
-      int m = nw;
-      for (; m + NW < nm; m += 2 * NW) walk(std::integral_constant<int, 2>(), m);
-      if (m < nm) walk(std::integral_constant<int, 1>(), m);
+      walk(std::integral_constant<int, 0>());
+      if (nm > kPair * NW) walk(std::integral_constant<int, 1>());
+      if constexpr (kModes > 2 * kPair * NW) {
+        if (nm > 2 * kPair * NW) walk(std::integral_constant<int, 2>());
+        if (nm > 3 * kPair * NW) walk(std::integral_constant<int, 3>());
+      }
       buf ^= 1;
     }
     if constexpr (AGG) {
@@ -446,19 +508,21 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
       if constexpr (kJoinY) {
         // the next tile's first barrier keeps these from being overwritten too early
 #pragma unroll
-        for (int k = 0; k < NW; ++k)
-          yred[wave][k][lane] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        for (int k = 0; k < QS; ++k)
+          yred[wave][k][ln] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < SP; ++j) own[j] = skip[j];
 #pragma unroll
-        for (int k = 0; k < NW; ++k) {
-          const float4 a = yred[rg * NW + k][nw][lane];
-          own[0] += a.x;
-          own[1] += a.y;
-          own[2] += a.z;
-          own[3] += a.w;
-        }
+        for (int k = 0; k < NW; ++k)
+#pragma unroll
+          for (int i = 0; i < QP; ++i) {
+            const float4 a = yred[rg * NW + k][nw * QP + i][ln];
+            own[4 * i] += a.x;
+            own[4 * i + 1] += a.y;
+            own[4 * i + 2] += a.z;
+            own[4 * i + 3] += a.w;
+          }
       } else {
 #pragma unroll
         for (int j = 0; j < SP; ++j) own[j] = y[j];
@@ -489,14 +553,15 @@ __global__ __launch_bounds__(64 * RW * NW) void selective_fwd_kernel(Args p) {
     }
   }
   // what leaves: the state after the row, or the segment's own part of it
-  float* to = AGG ? p.agg + (size_t)at.seg * p.N : at.seg == p.nseg - 1 ? p.xT : nullptr;
-  if (to) {
+  float* out_x = AGG ? p.agg + (size_t)at.seg * p.N : at.seg == p.nseg - 1 ? p.xT : nullptr;
+  if (out_x) {
     const size_t pitch = (size_t)(AGG ? p.nseg : 1) * p.N;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int q = rg * 4 + k;
       if (q < nrow)
-        for (int n = lane * NW + nw; n < p.N; n += 64 * NW) to[(row0 + q) * pitch + n] = car[n * RP + q];
+        for (int n = lane * NW + nw; n < p.N; n += 64 * NW)
+          out_x[(row0 + q) * pitch + n] = car.row(q)[n];
     }
   }
 }
@@ -628,11 +693,9 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
 #pragma unroll
         for (int j = ST - 1; j >= 0; --j)
           F = exp2_fast(-k * dt[j]) * fmaf(v[j], gy[j], F);
-        float P = exp2_fast(-k * S);
-        F = fmaf(P, last ? carry : 0.f, F);
-        row_scan<true, 1>(&P, &F);
-        const float next = row_move<kRowRor + 15>(F);
-        if (last) *cell = next;
+        float P[1] = {exp2_fast(-k * S)}, V[1] = {fmaf(P[0], last ? carry : 0.f, F)}, in[1];
+        row_scan<true>(P, V, in);
+        if (seg == 0) *cell = V[0];
       }
       buf ^= 1;
     }
@@ -655,8 +718,8 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
 template <typename T, int ST, int RW, bool Z>
 __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
   constexpr int NT = 64 * RW, R = 4 * RW, RP = R + 1, TILE = kSeg * ST, Q = ST / 4;
-  typedef float Quad __attribute__((ext_vector_type(4)));
-  typedef typename std::conditional<Q == 4, Quad, float>::type Part;  // Q steps
+  typedef float Pair __attribute__((ext_vector_type(2)));
+  typedef typename std::conditional<Q == 2, Pair, float>::type Part;  // Q steps
   __shared__ float bc[2][2][kModes][TILE];
   __shared__ Part slab[2][RW][2][2][64];
   extern __shared__ float dyn[];
@@ -706,11 +769,11 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
   const int nblk = (p.N + kModes - 1) / kModes;
   const int off = seg * ST;
   const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
-  const int Lp = p.nchunk * 256;
+  const int Lp = p.nchunk * kKeep;
   float* part = p.part_bc +
                 (((size_t)at.rb * p.B + at.b) * p.G + at.g) * 2 * p.N * (size_t)Lp;
   // the lanes that put a row's values; the others take the spare word: no branch
-  const int put_c = last ? p.N * RP + r : 3 * p.N * RP, pitch_c = last ? RP : 0;
+  const int put_c = first ? p.N * RP + r : 3 * p.N * RP, pitch_c = first ? RP : 0;
   const int put_d = first ? 2 * p.N * RP + r : 3 * p.N * RP, pitch_d = first ? RP : 0;
   // behind the rows' end: no gradients
   for (int tile = t_hi - 1; tile >= max(t_lo, t_live); --tile) {
@@ -730,7 +793,7 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
   const auto fetch_starts = [&](int n0, int t0) {
     starts = 0.f;
     if (live && seg < kModes && n0 + seg < p.N)
-      starts = p.bounds[((row0 + r) * p.nchunk + (t0 >> 8)) * p.N + n0 + seg];
+      starts = p.bounds[((row0 + r) * p.nchunk + t0 / kKeep) * p.N + n0 + seg];
   };
   if (t_lo < t_live) {
     stage.fetch(Bm, Cm, p.N, p.L, 0, (t_live - 1) * TILE, len);
@@ -792,8 +855,10 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
           c[0][j] = dtu[j] * v[j];
         }
         const float decay = exp2_fast(-k * S);
-        float P = decay, next, x;
-        enter_forward<ST, 1>(a, c, &P, &start, first, &x, &next);
+        float P[1] = {decay}, V[1], xs[1];
+        const float enter[1] = {first ? start : 0.f};
+        enter_forward<ST, 1>(a, c, P, enter, xs, V);
+        float x = xs[0];
         start = row_move<kRowShl + 1>(start);  // the next mode's to the first lane
         float cv[ST];
         read_steps<ST>(bc[buf][1][m], seg, cv);
@@ -810,8 +875,8 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
 #pragma unroll
           for (int i = 0; i < Q; ++i) o[i] = rows_quad(g[i], g[Q + i], g[2 * Q + i], g[3 * Q + i]);
           Part to;
-          if constexpr (Q == 4)
-            to = Part{o[0], o[1], o[2], o[3]};
+          if constexpr (Q == 2)
+            to = Part{o[0], o[1]};
           else
             to = o[0];
           slab[sb][wave][m & 1][which][lane] = to;
@@ -822,12 +887,12 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
 #pragma unroll
         for (int j = ST - 2; j >= 0; --j) F = fmaf(a[0][j + 1], F, c[0][j]);
         F *= a[0][0];
-        P = decay;
-        F = fmaf(P, last ? carry : 0.f, F);
-        row_scan<true, 1>(&P, &F);
-        const float out = row_move<kRowRor + 15>(F);
-        dyn[put_c + n * pitch_c] = out;
-        float G = last ? carry : out;
+        const float right = last ? carry : 0.f;
+        P[0] = decay;
+        V[0] = fmaf(decay, right, F);
+        row_scan<true>(P, V, xs);
+        dyn[put_c + n * pitch_c] = V[0];
+        float G = xs[0] + right;
         float acc = 0.f;
 #pragma unroll
         for (int j = ST - 1; j >= 0; --j) {
@@ -920,7 +985,7 @@ __global__ __launch_bounds__(256) void selective_dbc_kernel(Args p) {
   const int which = bg2 & 1;
   const unsigned bg = bg2 >> 1;
   const int b = bg / (unsigned)p.G, g = bg - b * p.G;
-  const int Lp = p.nchunk * 256, len = row_len(p, b);
+  const int Lp = p.nchunk * kKeep, len = row_len(p, b);
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (t < len) {
     const size_t step = (size_t)p.B * p.G * 2 * p.N * Lp;
@@ -1007,24 +1072,20 @@ __global__ __launch_bounds__(256) void selective_step_kernel(Args p, int lpr) {
 
 // How rows go to workgroups.
 struct Plan {
-  int st;         // steps of a lane: 16, or 4 where rows have at most 64 steps
-  int rw, nw;     // groups of four rows, waves of each
+  int st;         // steps of a lane: 8, or 4 where rows have at most 64 steps
+  int rw;         // groups of four rows
   int nrb;        // row blocks of a group of channels
   int nseg, seg_tiles;
 };
 
 Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
-  Plan p{16, 8, 1, 1, 1, 1};
+  Plan p{8, 8, 1, 1, 1};
   if (L <= 64) p.st = 4;
   const int tile = kSeg * p.st, ntile = std::max(1, (L + tile - 1) / tile), hg = H / G;
-  const long waves = (long)B * G * ((hg + 3) / 4);
-  if (!backward && p.st == 16 && waves < 1024 && N >= 4) {
-    p.nw = 4;
-    p.rw = 2;
-  }
+  if (!backward && p.st == 8) p.rw = 4;
   p.nrb = (hg + 4 * p.rw - 1) / (4 * p.rw);
   const long have = std::max(1L, (long)B * G * p.nrb);
-  const long want = have >= 128 ? 1 : std::min<long>(ntile, 256 / have);
+  const long want = have >= 256 ? 1 : std::min<long>(ntile, 512 / have);
   p.seg_tiles = (int)((ntile + want - 1) / want);
   p.nseg = (ntile + p.seg_tiles - 1) / p.seg_tiles;
   return p;
@@ -1056,7 +1117,7 @@ Args make_args(const SelectiveCall& c, const Plan& pl) {
   a.xT = c.xT;
   a.y = c.y;
   a.bounds = static_cast<float*>(c.ckpt);
-  a.nchunk = (c.L + 255) / 256;
+  a.nchunk = (c.L + kKeep - 1) / kKeep;
   a.nrb = pl.nrb;
   a.nseg = pl.nseg;
   a.seg_tiles = pl.seg_tiles;
@@ -1096,7 +1157,7 @@ Layout layout_of(const Plan& pl, int B, int H, int G, int N, int L, bool backwar
   o.agg = take(pl.nseg > 1 ? rows * pl.nseg * N : 0);
   o.aggS = take(pl.nseg > 1 ? rows * pl.nseg : 0);
   if (backward) {
-    o.bc = take((size_t)pl.nrb * B * G * 2 * N * ((size_t)(L + 255) / 256 * 256));
+    o.bc = take((size_t)pl.nrb * B * G * 2 * N * ((size_t)(L + kKeep - 1) / kKeep * kKeep));
     o.n = take(rows * pl.nseg * N);
     o.h = take(rows * pl.nseg * 2);
   }
@@ -1118,7 +1179,7 @@ unsigned blocks_of(long n) { return (unsigned)((n + 255) / 256); }
 template <typename T, int ST, int RW, int NW>
 hipError_t forward(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)a.B * a.G * a.nrb * a.nseg), block(64 * RW * NW);
-  const size_t lds = (2 * (size_t)a.N * (4 * RW + 1) + 1) * sizeof(float);
+  const size_t lds = (size_t)padded(a.N) * (2 * 4 * RW + 2) * sizeof(float);
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
     hipLaunchKernelGGL((selective_join_kernel<false>), dim3(blocks_of((long)a.B * a.H * a.N)),
@@ -1134,8 +1195,7 @@ hipError_t run_forward(const SelectiveCall& c, hipStream_t st) {
   const Plan pl = plan_of(c.B, c.H, c.G, c.N, c.L, false);
   Args a = make_args(c, pl);
   place(a, c, layout_of(pl, c.B, c.H, c.G, c.N, c.L, false));
-  if (pl.nw > 1) return forward<T, 16, 2, 4>(a, st);
-  return pl.st == 4 ? forward<T, 4, 8, 1>(a, st) : forward<T, 16, 8, 1>(a, st);
+  return pl.st == 4 ? forward<T, 4, 8, 1>(a, st) : forward<T, 8, 4, 2>(a, st);
 }
 
 template <typename T, int ST, int RW>
@@ -1165,7 +1225,7 @@ hipError_t run_backward(const SelectiveCall& c, hipStream_t st) {
   Args a = make_args(c, pl);
   place(a, c, layout_of(pl, c.B, c.H, c.G, c.N, c.L, true));
   if (c.B > 0) {
-    const hipError_t e = pl.st == 4 ? backward<T, 4, 8>(a, st) : backward<T, 16, 8>(a, st);
+    const hipError_t e = pl.st == 4 ? backward<T, 4, 8>(a, st) : backward<T, 8, 8>(a, st);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(selective_param_kernel, dim3(blocks_of((long)c.H * (c.N + 2) * 16)), dim3(256),
@@ -1175,7 +1235,7 @@ hipError_t run_backward(const SelectiveCall& c, hipStream_t st) {
 
 template <typename T>
 hipError_t run_step(const SelectiveCall& c, hipStream_t st) {
-  const Args a = make_args(c, Plan{16, 8, 1, 1, 1, 1});
+  const Args a = make_args(c, Plan{8, 8, 1, 1, 1});
   int lpr = 1;
   while (lpr * 4 < c.N) lpr *= 2;
   const long rows = (long)c.B * c.H, per = 256 / lpr;
@@ -1191,7 +1251,7 @@ size_t selective_workspace(int B, int H, int G, int N, int L, bool backward) {
 }
 
 size_t selective_ckpt(int B, int H, int N, int L) {
-  return align_up((size_t)B * H * ((L + 255) / 256) * N * sizeof(float), 256);
+  return align_up((size_t)B * H * ((L + kKeep - 1) / kKeep) * N * sizeof(float), 256);
 }
 
 hipError_t launch_selective_forward(const SelectiveCall& c, int dtype, hipStream_t st) {
