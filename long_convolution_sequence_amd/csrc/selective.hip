@@ -178,15 +178,20 @@ __device__ __forceinline__ void read_steps(const float* tile, int seg, float* ou
   }
 }
 
-// Eight steps from t (a multiple of 8, in the tile) to where they are read.
+__device__ __forceinline__ void put_quad(float* to, const float* v) {
+  *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void add_quad(const float* from, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(from);
+  v[0] += a.x;
+  v[1] += a.y;
+  v[2] += a.z;
+  v[3] += a.w;
+}
+// Four steps, the q-th of the tile, to where they are read.
 template <int ST>
-__device__ __forceinline__ void write_steps(float* tile, int t, const float* v) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int q = t / 4 + k;
-    float* to = tile + slot<ST>(q / (ST / 4), q % (ST / 4));
-    *reinterpret_cast<float4*>(to) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  }
+__device__ __forceinline__ void write_quad(float* tile, int q, const float* v) {
+  put_quad(tile + slot<ST>(q / (ST / 4), q % (ST / 4)), v);
 }
 
 // Which batch row, group, row block and segment a workgroup works on.
@@ -221,55 +226,67 @@ __device__ __forceinline__ T* spot(T* shared, uint32_t bytes) {
       (uint32_t)opaque((int)bytes));
 }
 
-// The group's B and C over one tile and kModes modes, on their way to LDS.
+// The group's B and C over one tile and kModes modes, on their way to LDS: 8
+// steps of a mode to a thread.
 template <typename T, int NT, int TILE, bool BOTH>
 struct Stage {
-  static constexpr int kChunks = (BOTH ? 2 : 1) * kModes * (TILE / 8);
-  static constexpr int IT = (kChunks + NT - 1) / NT;
+  static constexpr int ST = TILE / kSeg, kRow = TILE / 8, kHalf = kModes * kRow;
+  static constexpr int kChunks = (BOTH ? 2 : 1) * kHalf, IT = (kChunks + NT - 1) / NT;
   Packed<T, 8> v[IT];
   // modes n0 .. of the tile from t0; steps at or past len are 0
   __device__ __forceinline__ void fetch(const T* Bm, const T* Cm, int N, int L, int n0, int t0,
                                         int len) {
-    const size_t first = (size_t)n0 * L + t0;
+    const size_t from = (size_t)n0 * L + t0;
+    const bool whole = t0 + TILE <= len && n0 + kModes <= N;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int k = opaque((int)threadIdx.x) + i * NT;
-      const int t = (k % (TILE / 8)) * 8, n = k / (TILE / 8) % kModes;
-      const bool second = BOTH && k >= kChunks / 2;
-      const int nv = (IT * NT == kChunks || k < kChunks) && n0 + n < N ? len - t0 - t : 0;
-      const T* from = spot((second ? Cm : Bm) + first, (uint32_t)(n * L + t) * sizeof(T));
-      if (nv >= 8)
-        v[i].load(from);
-      else
-        v[i].load(from, max(nv, 0), (T)0.f);
+      const int k = (int)threadIdx.x + i * NT;
+      // whole waves take B or C, so that the choice is a scalar's
+      const bool second = BOTH && __builtin_amdgcn_readfirstlane(k / kHalf) != 0;
+      const int t = k % kRow * 8, n = k / kRow % kModes;
+      const T* p = spot((second ? Cm : Bm) + from, (uint32_t)(n * L + t) * sizeof(T));
+      if (IT * NT != kChunks && k >= kChunks) break;
+      if (whole) {
+        v[i].load(p);
+      } else {
+        const int nv = n0 + n < N ? len - t0 - t : 0;
+        v[i].load(p, max(nv, 0), (T)0.f);
+      }
     }
   }
   __device__ __forceinline__ void put(float (*to)[kModes][TILE]) const {
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int k = opaque((int)threadIdx.x) + i * NT;
+      const int k = (int)threadIdx.x + i * NT;
       if (IT * NT != kChunks && k >= kChunks) break;
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = v[i][j];
-      write_steps<TILE / kSeg>(to[BOTH && k >= kChunks / 2 ? 1 : 0][k / (TILE / 8) % kModes],
-                               k % (TILE / 8) * 8, f);
+      float* tile = to[0][0] + k / kRow * TILE;
+      write_quad<ST>(tile, k % kRow * 2, f);
+      write_quad<ST>(tile, k % kRow * 2 + 1, f + 4);
     }
   }
 };
 
 // A lane's steps of one row as they lie in memory; row0: the workgroup's first
-// row at the tile's first step.
+// row at the tile's first step; whole: the workgroup's tile has no end in it.
 template <typename T, int SP>
 struct Lane {
   Packed<T, SP> v;
-  __device__ __forceinline__ void fetch(const T* row0, uint32_t own, int nv) {
-    if (nv >= SP)
+  __device__ __forceinline__ void fetch(const T* row0, uint32_t own, int nv, bool whole) {
+    if (whole)
       v.load(spot(row0, own));
     else
       v.load(spot(row0, own), max(nv, 0), (T)0.f);
   }
 };
+
+template <typename T, int SP>
+__device__ __forceinline__ void store_lane(T* row0, uint32_t own, int ns, bool whole,
+                                           const float* v) {
+  store_n<T, SP>(spot(row0, own), whole ? SP : ns, v);
+}
 
 __host__ __device__ inline int padded(int N) { return (N + kModes - 1) / kModes * kModes; }
 
@@ -306,104 +323,120 @@ struct Cells {
   __device__ __forceinline__ float* to(int r, bool mine) const { return row(mine ? r : R + 1); }
 };
 
-// Forward over a row or a segment of it.  RW groups of four rows, the modes of
-// each shared out among NW waves: with NW > 1 every wave forms a part of the
-// lanes' step sizes, and of their outputs.  AGG: only the segment's ends.
+// What a workgroup of RW groups of four rows and NW waves to each works on.  A
+// lane walks the modes over ST steps of one row (r); what is formed once per
+// step (step sizes, gates, outputs) it does for four steps of row `own`, 32
+// (16) neighbouring lanes to a row, so that memory is met in whole lines.  The
+// two are the same where NW == 1.
+template <int ST, int RW, int NW>
+struct Lanes {
+  static constexpr int NT = 64 * RW * NW, R = 4 * RW, TILE = kSeg * ST, LPR = TILE / 4;
+  static_assert(NW * 64 == 4 * LPR, "every step is some lane's own");
+  int lane, seg, rg, nw, r, own, step;  // step: the lane's own first one in a tile
+  __device__ __forceinline__ Lanes() {
+    lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    seg = lane & (kSeg - 1);
+    rg = wave / NW;
+    nw = wave % NW;
+    r = rg * 4 + lane / kSeg;
+    own = rg * 4 + (nw * 64 + lane) / LPR;
+    step = lane % LPR * 4;
+  }
+};
+
+// Forward over a row or a segment of it; the modes of a group of rows are shared
+// out among its NW waves.  AGG: only the segment's ends.
 template <typename T, int ST, int RW, int NW, bool AGG>
 __global__ __launch_bounds__(64 * RW * NW) __attribute__((amdgpu_waves_per_eu(4)))
 void selective_fwd_kernel(Args p) {
-  constexpr int NT = 64 * RW * NW, R = 4 * RW, TILE = kSeg * ST, SP = ST / NW;
-  constexpr int QS = ST / 4, QP = SP / 4;  // a lane's, and its own part's, groups of four steps
-  static_assert(SP % 4 == 0, "the waves of a row exchange 16 bytes a lane");
+  typedef Lanes<ST, RW, NW> Work;
+  constexpr int NT = Work::NT, R = Work::R, TILE = Work::TILE;
   __shared__ float bc[2][AGG ? 1 : 2][kModes][TILE];
-  __shared__ float4 xch[NW > 1 ? RW : 1][2][NW > 1 ? QS : 1][NW > 1 ? 64 : 1];
+  // step sizes and drives of the rows; their outputs, a wave's part each
+  __shared__ float xch[NW > 1 ? 2 : 1][NW > 1 ? R : 1][TILE];
   constexpr bool kJoinY = NW > 1 && !AGG;
-  __shared__ float4 yred[kJoinY ? RW * NW : 1][kJoinY ? QS : 1][kJoinY ? 64 : 1];
+  __shared__ float yred[kJoinY ? NW : 1][kJoinY ? R : 1][TILE];
   extern __shared__ float dyn[];
   const int NP = padded(p.N);
   const Cells kap{dyn, R, NP}, car{dyn + R * NP, R, NP};  // log_re^2; the state entering the tile
   const Place at(p);
   if (AGG && at.seg == p.nseg - 1) return;  // nobody joins the last segment
-  const int lane = threadIdx.x & 63, seg = lane & (kSeg - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rg = wave / NW, nw = wave % NW;
-  const int r = rg * 4 + lane / kSeg;  // the lane's row in the workgroup
-  const bool live = at.rb * R + r < p.HG, first = seg == 0;
-  const int h = at.g * p.HG + min(at.rb * R + r, p.HG - 1);
+  const Work w;
+  const int seg = w.seg, nw = w.nw, r = w.r, lane = w.lane;
   const int len = row_len(p, at.b);
   const int ntile = (p.L + TILE - 1) / TILE;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
   const int t_live = min(t_hi, (len + TILE - 1) / TILE);
-  const size_t row0 = (size_t)at.b * p.H + at.g * p.HG + at.rb * R;  // the workgroup's first row
-  const int nrow = min(R, p.HG - at.rb * R);
+  const int h0 = at.g * p.HG + at.rb * R, nrow = min(R, p.HG - at.rb * R);
+  const size_t row0 = (size_t)at.b * p.H + h0;  // the workgroup's first row
   // the waves of a row group take turns with its modes
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int q = rg * 4 + k;
-    for (int n = lane * NW + nw; n < NP; n += 64 * NW) {
-      float c = 0.f, s = 0.f;
-      if (q < nrow && n < p.N) {
-        s = square_of(p.log_re[(size_t)(row0 - (size_t)at.b * p.H + q) * p.N + n]) * kLog2e;
-        if (!AGG && p.nseg > 1)
-          c = p.agg[((row0 + q) * p.nseg + at.seg) * p.N + n];
-        else if (!AGG && p.x0)
-          c = p.x0[(row0 + q) * p.N + n];
-      }
-      kap.row(q)[n] = s;
-      car.row(q)[n] = c;
+  for (int n = (lane & 15) * NW + nw; n < NP; n += 16 * NW) {
+    float c = 0.f, s = 0.f;
+    if (r < nrow && n < p.N) {
+      s = square_of(p.log_re[(size_t)(h0 + r) * p.N + n]) * kLog2e;
+      if (!AGG && p.nseg > 1)
+        c = p.agg[((row0 + r) * p.nseg + at.seg) * p.N + n];
+      else if (!AGG && p.x0)
+        c = p.x0[(row0 + r) * p.N + n];
     }
+    kap.row(r)[n] = s;
+    car.row(r)[n] = c;
   }
   for (int n = threadIdx.x; n < NP; n += NT) car.row(R)[n] = 0.f;  // before the first barrier
   const float* krow = kap.row(r) + nw;
-  const float* from = car.from(r, first) + nw;
+  const float* from = car.from(r, seg == 0) + nw;
   float* to = car.to(r, seg == kSeg - 1) + nw;
-  const size_t first_row = (size_t)(at.g * p.HG + at.rb * R) * p.L;
+  const size_t first_row = (size_t)h0 * p.L;
   const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + first_row;
   const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + first_row;
   const T* z = static_cast<const T*>(p.z) + (p.z ? (size_t)(at.b * p.sz) + first_row : 0);
   const T* Bm = static_cast<const T*>(p.Bm) + (size_t)(at.b * p.sB) + (size_t)at.g * p.N * p.L;
   const T* Cm = static_cast<const T*>(p.Cm) + (size_t)(at.b * p.sC) + (size_t)at.g * p.N * p.L;
   T* out = static_cast<T*>(p.y) + row0 * p.L;
+  const int h = h0 + min(w.own, nrow - 1);
+  const bool live = w.own < nrow;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
   const float D = !AGG && p.D ? p.D[h] : 0.f;
   const int nblk = (p.N + kModes - 1) / kModes;
-  const int off = seg * ST + nw * SP;  // the lane's own part of a tile
-  const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
+  const uint32_t mine =
+      ((uint32_t)min(w.own, nrow - 1) * (uint32_t)p.L + w.step) * (uint32_t)sizeof(T);
   Stage<T, NT, TILE, !AGG> stage;
-  Lane<T, SP> un, dn;
+  Lane<T, 4> un, dn;
   if (t_lo < t_live) {
     const int t = t_lo * TILE;
     stage.fetch(Bm, Cm, p.N, p.L, 0, t, len);
-    dn.fetch(delta + t, mine, len - t - off);
-    un.fetch(u + t, mine, len - t - off);
+    dn.fetch(delta + t, mine, len - t - w.step, t + TILE <= len);
+    un.fetch(u + t, mine, len - t - w.step, t + TILE <= len);
   }
+  // where the lane's own steps, and those it walks, lie among a tile's rows
+  const int own_at = w.own * TILE + slot<ST>(w.step / ST, w.step % ST / 4), walk_at = r * TILE;
+  uint32_t keep_at = ((uint32_t)r * p.nchunk * p.N + (lane & 15) * NW + nw) * 4u;
   float Sseg = 0.f;
   int buf = 0;
   for (int tile = t_lo; tile < t_live; ++tile) {
-    const int t0 = tile * TILE, nv = len - t0 - off, ln = opaque(lane);
+    const int t0 = tile * TILE, nv = len - t0 - w.step;
+    const bool whole = t0 + TILE <= len;
     // the states entering a chunk, for the backward pass
     if (!AGG && p.bounds && (t0 & (kKeep - 1)) == 0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int q = rg * 4 + k;
-        if (q < nrow)
-          for (int n = ln * NW + nw; n < p.N; n += 64 * NW)
-            p.bounds[((row0 + q) * p.nchunk + t0 / kKeep) * p.N + n] = car.row(q)[n];
-      }
+      float* keep = p.bounds + (row0 * p.nchunk + t0 / kKeep) * p.N;
+      if (r < nrow)
+        for (int n = (lane & 15) * NW + nw, k = 0; n < p.N; n += 16 * NW, k += 64 * NW)
+          *spot(keep, keep_at + k) = car.row(r)[n];
     }
-    Lane<T, SP> zc;
-    float dt[ST], du[ST], y[ST], skip[SP];
+    Lane<T, 4> zc;
+    float dt[ST], du[ST], y[ST], skip[4];
     {
-      float own[2][SP];
+      float own[2][4];
 #pragma unroll
-      for (int j = 0; j < SP; ++j) {
+      for (int j = 0; j < 4; ++j) {
         own[0][j] = softplus(dn.v[j] + bias);
         own[1][j] = own[0][j] * un.v[j];
         skip[j] = D * un.v[j];
       }
-      if (t0 + TILE > len) {
+      if (!whole) {
 #pragma unroll
-        for (int j = 0; j < SP; ++j) {
+        for (int j = 0; j < 4; ++j) {
           own[0][j] = j < nv ? own[0][j] : 0.f;
           own[1][j] = j < nv ? own[1][j] : 0.f;
         }
@@ -413,25 +446,20 @@ void selective_fwd_kernel(Args p) {
         for (int j = 0; j < ST; ++j) {
           dt[j] = own[0][j];
           du[j] = own[1][j];
-          y[j] = skip[j];
         }
       } else {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int i = 0; i < QP; ++i)
-            xch[rg][m][nw * QP + i][ln] = make_float4(own[m][4 * i], own[m][4 * i + 1],
-                                                        own[m][4 * i + 2], own[m][4 * i + 3]);
-#pragma unroll
-        for (int j = 0; j < ST; ++j) y[j] = 0.f;
+        put_quad(xch[0][0] + own_at, own[0]);
+        put_quad(xch[1][0] + own_at, own[1]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < ST; ++j) y[j] = 0.f;
     // the gate is read for this tile's end, the rest for the next tile
-    if (!AGG && p.z) zc.fetch(z + t0, mine, nv);
+    if (!AGG && p.z) zc.fetch(z + t0, mine, nv, whole);
     if (tile + 1 < t_live) {
       const int t = t0 + TILE;
-      dn.fetch(delta + t, mine, len - t - off);
-      un.fetch(u + t, mine, len - t - off);
+      dn.fetch(delta + t, mine, len - t - w.step, t + TILE <= len);
+      un.fetch(u + t, mine, len - t - w.step, t + TILE <= len);
     }
     float S = 0.f;
     for (int blk = 0; blk < nblk; ++blk) {
@@ -445,16 +473,8 @@ void selective_fwd_kernel(Args p) {
         stage.fetch(Bm, Cm, p.N, p.L, 0, t0 + TILE, len);
       if (blk == 0) {
         if constexpr (NW > 1) {
-#pragma unroll
-          for (int k = 0; k < QS; ++k) {
-            const float4 a = xch[rg][0][k][ln], b = xch[rg][1][k][ln];
-            const float va[4] = {a.x, a.y, a.z, a.w}, vb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              dt[4 * k + j] = va[j];
-              du[4 * k + j] = vb[j];
-            }
-          }
+          read_steps<ST>(xch[0][0] + walk_at, seg, dt);
+          read_steps<ST>(xch[1][0] + walk_at, seg, du);
         }
 #pragma unroll
         for (int j = 0; j < ST; ++j) S += dt[j];
@@ -504,65 +524,53 @@ void selective_fwd_kernel(Args p) {
     if constexpr (AGG) {
       if (NW > 1) __syncthreads();  // before the next tile's step sizes take this one's place
     } else {
-      float own[SP];
+      float own[4];
       if constexpr (kJoinY) {
         // the next tile's first barrier keeps these from being overwritten too early
 #pragma unroll
-        for (int k = 0; k < QS; ++k)
-          yred[wave][k][ln] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        for (int k = 0; k < ST / 4; ++k)
+          put_quad(yred[nw][0] + walk_at + slot<ST>(seg, k), y + 4 * k);
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < SP; ++j) own[j] = skip[j];
+        for (int j = 0; j < 4; ++j) own[j] = skip[j];
 #pragma unroll
         for (int k = 0; k < NW; ++k)
-#pragma unroll
-          for (int i = 0; i < QP; ++i) {
-            const float4 a = yred[rg * NW + k][nw * QP + i][ln];
-            own[4 * i] += a.x;
-            own[4 * i + 1] += a.y;
-            own[4 * i + 2] += a.z;
-            own[4 * i + 3] += a.w;
-          }
+          add_quad(yred[k][0] + own_at, own);
       } else {
 #pragma unroll
-        for (int j = 0; j < SP; ++j) own[j] = y[j];
+        for (int j = 0; j < 4; ++j) own[j] = y[j] + skip[j];
       }
+      if (p.z) {
 #pragma unroll
-      for (int j = 0; j < SP; ++j) {
-        float rest;
-        if (p.z) own[j] *= zc.v[j] * sigmoid_pair(zc.v[j], &rest);
+        for (int j = 0; j < 4; ++j) {
+          float rest;
+          own[j] *= zc.v[j] * sigmoid_pair(zc.v[j], &rest);
+        }
       }
-      if (t0 + TILE > len) {
+      if (!whole) {
 #pragma unroll
-        for (int j = 0; j < SP; ++j) own[j] = j < nv ? own[j] : 0.f;
+        for (int j = 0; j < 4; ++j) own[j] = j < nv ? own[j] : 0.f;
       }
-      if (live) store_n<T, SP>(spot(out + t0, mine), p.L - t0 - off, own);
+      if (live) store_lane<T, 4>(out + t0, mine, p.L - t0 - w.step, whole, own);
     }
   }
   if (AGG) {
     const float s = row_total(Sseg);
-    if (live && first && nw == 0) p.aggS[(row0 + r) * p.nseg + at.seg] = s;
+    if (r < nrow && seg == 0 && nw == 0) p.aggS[(row0 + r) * p.nseg + at.seg] = s;
   } else {
     // behind the rows' end: outputs are 0, the states stay
     for (int tile = max(t_lo, t_live); tile < t_hi; ++tile) {
       const int t0 = tile * TILE;
-      float zero[SP];
-#pragma unroll
-      for (int j = 0; j < SP; ++j) zero[j] = 0.f;
-      if (live) store_n<T, SP>(spot(out + t0, mine), p.L - t0 - off, zero);
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      if (live) store_n<T, 4>(spot(out + t0, mine), p.L - t0 - w.step, zero);
     }
   }
   // what leaves: the state after the row, or the segment's own part of it
   float* out_x = AGG ? p.agg + (size_t)at.seg * p.N : at.seg == p.nseg - 1 ? p.xT : nullptr;
-  if (out_x) {
+  if (out_x && r < nrow) {
     const size_t pitch = (size_t)(AGG ? p.nseg : 1) * p.N;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int q = rg * 4 + k;
-      if (q < nrow)
-        for (int n = lane * NW + nw; n < p.N; n += 64 * NW)
-          out_x[(row0 + q) * pitch + n] = car.row(q)[n];
-    }
+    for (int n = (lane & 15) * NW + nw; n < p.N; n += 16 * NW)
+      out_x[(row0 + r) * pitch + n] = car.row(r)[n];
   }
 }
 
@@ -661,10 +669,11 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
   int buf = 0;
   for (int tile = t_live - 1; tile >= t_lo; --tile) {
     const int t0 = tile * TILE, nv = len - t0 - off;
+    const bool whole = t0 + TILE <= len;
     Lane<T, ST> dv, zv, gv;
-    dv.fetch(delta + t0, mine, nv);
-    gv.fetch(dy + t0, mine, nv);
-    if (p.z) zv.fetch(z + t0, mine, nv);
+    dv.fetch(delta + t0, mine, nv, whole);
+    gv.fetch(dy + t0, mine, nv, whole);
+    if (p.z) zv.fetch(z + t0, mine, nv, whole);
     float dt[ST], gy[ST], S = 0.f;
 #pragma unroll
     for (int j = 0; j < ST; ++j) {
@@ -713,49 +722,54 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
 
 // Backward over a row or a segment of it, from its end: every tile's states are
 // formed again from the kept one.  The sums over the group's rows (dB, dC) are
-// added up over a wave's four rows in registers, over the workgroup's waves
-// through LDS, two modes at a time, and left for the last kernel.
-template <typename T, int ST, int RW, bool Z>
-__global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
-  constexpr int NT = 64 * RW, R = 4 * RW, RP = R + 1, TILE = kSeg * ST, Q = ST / 4;
+// added up over a wave's four rows in registers, over the workgroup's row groups
+// through LDS, and left for a kernel of its own.
+template <typename T, int ST, int RW, int NW, bool Z>
+__global__ __launch_bounds__(64 * RW * NW) __attribute__((amdgpu_waves_per_eu(4)))
+void selective_bwd_kernel(Args p) {
+  typedef Lanes<ST, RW, NW> Work;
+  constexpr int NT = Work::NT, R = Work::R, TILE = Work::TILE, Q = ST / 4;
   typedef float Pair __attribute__((ext_vector_type(2)));
   typedef typename std::conditional<Q == 2, Pair, float>::type Part;  // Q steps
-  __shared__ float bc[2][2][kModes][TILE];
-  __shared__ Part slab[2][RW][2][2][64];
+  __shared__ float bc[2][kModes][TILE];
+  __shared__ Part slab[RW][kModes][2][64];
+  // step sizes, drives and the output's gradients of the rows; at a tile's end the
+  // waves' sums over their modes
+  __shared__ float xch[NW > 1 ? 3 * (NW - 1) : 1][NW > 1 ? R : 1][TILE];
   extern __shared__ float dyn[];
-  float* kap = dyn;                  // [N][RP]
-  float* car = dyn + p.N * RP;       // [N][RP] state gradient entering the tile
-  float* dre = dyn + 2 * p.N * RP;   // [N][RP] sum of w dt, and a spare word
+  const int NP = padded(p.N);
+  const Cells kap{dyn, R, NP};                  // log_re^2
+  const Cells car{dyn + R * NP, R, NP};         // state gradient entering the tile
+  const Cells dre{dyn + (2 * R + 2) * NP, R, NP};  // sum of w dt
   const Place at(p);
-  const int lane = threadIdx.x & 63, seg = lane & (kSeg - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = wave * 4 + lane / kSeg;
-  const bool live = at.rb * R + r < p.HG, first = seg == 0, last = seg == kSeg - 1;
-  const int h = at.g * p.HG + min(at.rb * R + r, p.HG - 1);
+  const Work w_;
+  const int seg = w_.seg, rg = w_.rg, nw = w_.nw, r = w_.r, lane = w_.lane;
   const int len = row_len(p, at.b);
   const int ntile = (p.L + TILE - 1) / TILE;
   const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
   const int t_live = min(t_hi, (len + TILE - 1) / TILE);
-  const size_t row0 = (size_t)at.b * p.H + at.g * p.HG + at.rb * R;
-  const int nrow = min(R, p.HG - at.rb * R);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int q = wave * 4 + k;
-    for (int n = lane; n < p.N; n += 64) {
-      float c = 0.f, s = 0.f;
-      if (q < nrow) {
-        s = square_of(p.log_re[(size_t)(row0 - (size_t)at.b * p.H + q) * p.N + n]) * kLog2e;
-        if (p.nseg > 1)
-          c = p.agg[((row0 + q) * p.nseg + at.seg) * p.N + n];
-        else if (p.dx)
-          c = p.dx[(row0 + q) * p.N + n];
-      }
-      kap[n * RP + q] = s;
-      car[n * RP + q] = c;
-      dre[n * RP + q] = 0.f;
+  const int h0 = at.g * p.HG + at.rb * R, nrow = min(R, p.HG - at.rb * R);
+  const size_t row0 = (size_t)at.b * p.H + h0;
+  for (int n = (lane & 15) * NW + nw; n < NP; n += 16 * NW) {
+    float c = 0.f, s = 0.f;
+    if (r < nrow && n < p.N) {
+      s = square_of(p.log_re[(size_t)(h0 + r) * p.N + n]) * kLog2e;
+      if (p.nseg > 1)
+        c = p.agg[((row0 + r) * p.nseg + at.seg) * p.N + n];
+      else if (p.dx)
+        c = p.dx[(row0 + r) * p.N + n];
     }
+    kap.row(r)[n] = s;
+    car.row(r)[n] = c;
+    dre.row(r)[n] = 0.f;
   }
-  const size_t first_row = (size_t)(at.g * p.HG + at.rb * R) * p.L;
+  for (int n = threadIdx.x; n < NP; n += NT) car.row(R)[n] = 0.f;  // before the first barrier
+  const float* krow = kap.row(r) + nw;
+  const float* from = car.from(r, seg == kSeg - 1) + nw;
+  float* to = car.to(r, seg == 0) + nw;
+  const float* dre_row = dre.row(r) + nw;
+  float* dre_to = dre.to(r, seg == 0) + nw;
+  const size_t first_row = (size_t)h0 * p.L;
   const T* u = static_cast<const T*>(p.u) + (size_t)(at.b * p.su) + first_row;
   const T* delta = static_cast<const T*>(p.delta) + (size_t)(at.b * p.sd) + first_row;
   const T* z = static_cast<const T*>(p.z) + (Z ? (size_t)(at.b * p.sz) + first_row : 0);
@@ -765,75 +779,85 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
   T* dz = static_cast<T*>(p.dz) + (Z ? (size_t)(at.b * p.sdz) + first_row : 0);
   const T* Bm = static_cast<const T*>(p.Bm) + (size_t)(at.b * p.sB) + (size_t)at.g * p.N * p.L;
   const T* Cm = static_cast<const T*>(p.Cm) + (size_t)(at.b * p.sC) + (size_t)at.g * p.N * p.L;
+  const int h = h0 + min(w_.own, nrow - 1);
+  const bool live = w_.own < nrow;
   const float bias = p.dt_bias ? p.dt_bias[h] : 0.f, D = p.D ? p.D[h] : 0.f;
   const int nblk = (p.N + kModes - 1) / kModes;
-  const int off = seg * ST;
-  const uint32_t mine = ((uint32_t)min(r, nrow - 1) * (uint32_t)p.L + off) * (uint32_t)sizeof(T);
+  const uint32_t mine =
+      ((uint32_t)min(w_.own, nrow - 1) * (uint32_t)p.L + w_.step) * (uint32_t)sizeof(T);
   const int Lp = p.nchunk * kKeep;
   float* part = p.part_bc +
                 (((size_t)at.rb * p.B + at.b) * p.G + at.g) * 2 * p.N * (size_t)Lp;
-  // the lanes that put a row's values; the others take the spare word: no branch
-  const int put_c = first ? p.N * RP + r : 3 * p.N * RP, pitch_c = first ? RP : 0;
-  const int put_d = first ? 2 * p.N * RP + r : 3 * p.N * RP, pitch_d = first ? RP : 0;
+  // where the lane's own steps, and those it walks, lie among a tile's rows
+  const int own_at = w_.own * TILE + slot<ST>(w_.step / ST, w_.step % ST / 4), walk_at = r * TILE;
+  const uint32_t keep_at = ((uint32_t)r * p.nchunk * p.N + seg * NW + nw) * 4u;
   // behind the rows' end: no gradients
   for (int tile = t_hi - 1; tile >= max(t_lo, t_live); --tile) {
-    const int t0 = tile * TILE, ns = p.L - t0 - off;
-    float zero[ST];
-#pragma unroll
-    for (int j = 0; j < ST; ++j) zero[j] = 0.f;
+    const int t0 = tile * TILE, ns = p.L - t0 - w_.step;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     if (live) {
-      store_n<T, ST>(spot(du + t0, mine), ns, zero);
-      store_n<T, ST>(spot(ddelta + t0, mine), ns, zero);
-      if (Z) store_n<T, ST>(spot(dz + t0, mine), ns, zero);
+      store_n<T, 4>(spot(du + t0, mine), ns, zero);
+      store_n<T, 4>(spot(ddelta + t0, mine), ns, zero);
+      if (Z) store_n<T, 4>(spot(dz + t0, mine), ns, zero);
     }
   }
   Stage<T, NT, TILE, true> stage;
-  // the kept states of a stage's modes, one to each of a row's first lanes
+  // the kept states of the wave's modes of a stage, one to each of a row's first lanes
   float starts = 0.f;
   const auto fetch_starts = [&](int n0, int t0) {
     starts = 0.f;
-    if (live && seg < kModes && n0 + seg < p.N)
-      starts = p.bounds[((row0 + r) * p.nchunk + t0 / kKeep) * p.N + n0 + seg];
+    if (r < nrow && seg < kModes / NW && n0 + seg * NW + nw < p.N)
+      starts = *spot(p.bounds + (row0 * p.nchunk + t0 / kKeep) * p.N + n0, keep_at);
   };
   if (t_lo < t_live) {
     stage.fetch(Bm, Cm, p.N, p.L, 0, (t_live - 1) * TILE, len);
     fetch_starts(0, (t_live - 1) * TILE);
   }
   float sumD = 0.f, sumb = 0.f;
-  int buf = 0, sb = 0;
   for (int tile = t_live - 1; tile >= t_lo; --tile) {
-    const int t0 = tile * TILE, nv = len - t0 - off;
+    const int t0 = tile * TILE, nv = len - t0 - w_.step;
+    const bool whole = t0 + TILE <= len;
     float dt[ST], dtu[ST], gy[ST], y[ST], q[ST], w[ST], S = 0.f;
     {
-      Lane<T, ST> uv, dv, zv, gv;
-      uv.fetch(u + t0, mine, nv);
-      dv.fetch(delta + t0, mine, nv);
-      gv.fetch(dy + t0, mine, nv);
-      if (Z) zv.fetch(z + t0, mine, nv);
+      Lane<T, 4> uv, dv, zv, gv;
+      uv.fetch(u + t0, mine, nv, whole);
+      dv.fetch(delta + t0, mine, nv, whole);
+      gv.fetch(dy + t0, mine, nv, whole);
+      if (Z) zv.fetch(z + t0, mine, nv, whole);
+      float own[3][4];
 #pragma unroll
-      for (int j = 0; j < ST; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const float d = softplus(dv.v[j] + bias);
         float g = gv.v[j], rest;
         if (Z) g *= zv.v[j] * sigmoid_pair(zv.v[j], &rest);
-        dt[j] = d;
-        dtu[j] = d * uv.v[j];
-        gy[j] = g;
-        y[j] = D * uv.v[j];
-        q[j] = w[j] = 0.f;
+        own[0][j] = d;
+        own[1][j] = d * uv.v[j];
+        own[2][j] = g;
       }
-      if (t0 + TILE > len || !live) {
+      if (!whole || nrow < R) {
 #pragma unroll
-        for (int j = 0; j < ST; ++j) {
-          dt[j] = j < nv ? dt[j] : 0.f;
-          dtu[j] = j < nv && live ? dtu[j] : 0.f;
-          gy[j] = j < nv && live ? gy[j] : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          own[0][j] = j < nv ? own[0][j] : 0.f;
+          own[1][j] = j < nv && live ? own[1][j] : 0.f;
+          own[2][j] = j < nv && live ? own[2][j] : 0.f;
         }
       }
+      if constexpr (NW == 1) {
 #pragma unroll
-      for (int j = 0; j < ST; ++j) S += dt[j];
+        for (int j = 0; j < ST; ++j) {
+          dt[j] = own[0][j];
+          dtu[j] = own[1][j];
+          gy[j] = own[2][j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) put_quad(xch[i][0] + own_at, own[i]);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < ST; ++j) y[j] = q[j] = w[j] = 0.f;
     for (int blk = 0; blk < nblk; ++blk) {
-      stage.put(bc[buf]);
+      stage.put(bc);
       float start = starts;
       __syncthreads();
       if (blk + 1 < nblk) {
@@ -843,12 +867,23 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
         stage.fetch(Bm, Cm, p.N, p.L, 0, t0 - TILE, len);
         fetch_starts(0, t0 - TILE);
       }
-      const int n0 = blk * kModes, nm = min(kModes, p.N - n0);
-      for (int m = 0; m < nm; ++m) {
-        const int n = n0 + m;
-        const float k = kap[n * RP + r], carry = car[n * RP + r], was = dre[n * RP + r];
+      if (blk == 0) {
+        if constexpr (NW > 1) {
+          read_steps<ST>(xch[0][0] + walk_at, seg, dt);
+          read_steps<ST>(xch[1][0] + walk_at, seg, dtu);
+          read_steps<ST>(xch[2][0] + walk_at, seg, gy);
+        }
+#pragma unroll
+        for (int j = 0; j < ST; ++j) S += dt[j];
+      }
+      const int n0 = blk * kModes, nm = p.N - n0;
+      // one mode to each of a row group's waves; modes past the last one are zeros
+      const auto walk = [&](auto step) {
+        constexpr int m0 = decltype(step)::value * NW;
+        __builtin_amdgcn_sched_barrier(0);  // steps mixed together would not fit the registers
+        const float k = krow[n0 + m0], right = from[n0 + m0], was = dre_row[n0 + m0];
         float v[ST], a[1][ST], ax[ST], c[1][ST], g[ST];
-        read_steps<ST>(bc[buf][0][m], seg, v);
+        read_steps<ST>(bc[0][m0 + nw], seg, v);
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
           a[0][j] = exp2_fast(-k * dt[j]);
@@ -856,42 +891,39 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
         }
         const float decay = exp2_fast(-k * S);
         float P[1] = {decay}, V[1], xs[1];
-        const float enter[1] = {first ? start : 0.f};
+        const float enter[1] = {seg == 0 ? start : 0.f};
         enter_forward<ST, 1>(a, c, P, enter, xs, V);
         float x = xs[0];
         start = row_move<kRowShl + 1>(start);  // the next mode's to the first lane
-        float cv[ST];
-        read_steps<ST>(bc[buf][1][m], seg, cv);
+        read_steps<ST>(bc[1][m0 + nw], seg, g);
 #pragma unroll
         for (int j = 0; j < ST; ++j) {
           ax[j] = a[0][j] * x;
           x = ax[j] + c[0][j];
-          if (Z) y[j] = fmaf(cv[j], x, y[j]);
+          if (Z) y[j] = fmaf(g[j], x, y[j]);
+          c[0][j] = g[j] * gy[j];
           g[j] = gy[j] * x;
-          c[0][j] = cv[j] * gy[j];
         }
         const auto leave = [&](int which) {
           float o[Q];
 #pragma unroll
           for (int i = 0; i < Q; ++i) o[i] = rows_quad(g[i], g[Q + i], g[2 * Q + i], g[3 * Q + i]);
-          Part to;
+          Part sum;
           if constexpr (Q == 2)
-            to = Part{o[0], o[1]};
+            sum = Part{o[0], o[1]};
           else
-            to = o[0];
-          slab[sb][wave][m & 1][which][lane] = to;
+            sum = o[0];
+          slab[rg][m0 + nw][which][lane] = sum;
         };
         leave(1);
         // against time
         float F = c[0][ST - 1];
 #pragma unroll
         for (int j = ST - 2; j >= 0; --j) F = fmaf(a[0][j + 1], F, c[0][j]);
-        F *= a[0][0];
-        const float right = last ? carry : 0.f;
         P[0] = decay;
-        V[0] = fmaf(decay, right, F);
+        V[0] = fmaf(decay, right, F * a[0][0]);
         row_scan<true>(P, V, xs);
-        dyn[put_c + n * pitch_c] = V[0];
+        to[n0 + m0] = V[0];
         float G = xs[0] + right;
         float acc = 0.f;
 #pragma unroll
@@ -904,74 +936,116 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_kernel(Args p) {
           acc = fmaf(wx, dt[j], acc);
         }
         leave(0);
-        dyn[put_d + n * pitch_d] = was + row_total(acc);
-        if ((m & 1) || m + 1 == nm) {
-          // one barrier for two modes: the slabs alternate
-          __syncthreads();
-          const int count = 128 * ((m & 1) + 1);
-          for (int i = threadIdx.x; i < count; i += NT) {
-            const int e = i & 63, which = i / 64 & 1, mm = i / 128;
-            Part sum = slab[sb][0][mm][which][e];
-#pragma unroll
-            for (int o = 1; o < RW; ++o) sum += slab[sb][o][mm][which][e];
-            const int st = (e & 15) * ST + (e >> 4) * Q;
-            *reinterpret_cast<Part*>(part + (size_t)(which * p.N + n0 + (m & ~1) + mm) * Lp + t0 +
-                                     st) = sum;
-          }
-          sb ^= 1;
-        }
+        dre_to[n0 + m0] = was + row_total(acc);
+      };
+      walk(std::integral_constant<int, 0>());
+      if (nm > NW) walk(std::integral_constant<int, 1>());
+      if (nm > 2 * NW) walk(std::integral_constant<int, 2>());
+      if (nm > 3 * NW) walk(std::integral_constant<int, 3>());
+      if constexpr (kModes > 4 * NW) {
+        if (nm > 4 * NW) walk(std::integral_constant<int, 4>());
+        if (nm > 5 * NW) walk(std::integral_constant<int, 5>());
+        if (nm > 6 * NW) walk(std::integral_constant<int, 6>());
+        if (nm > 7 * NW) walk(std::integral_constant<int, 7>());
       }
-      buf ^= 1;
+      // between this barrier and the next stage's the sums are read, and B and C replaced
+      __syncthreads();
+      const int count = 128 * min(kModes, nm);
+      for (int i = opaque((int)threadIdx.x); i < count; i += NT) {
+        const int e = i & 63, which = i / 64 & 1, m = i / 128;
+        Part sum = slab[0][m][which][e];
+#pragma unroll
+        for (int o = 1; o < RW; ++o) sum += slab[o][m][which][e];
+        *reinterpret_cast<Part*>(part + (size_t)(which * p.N + n0 + m) * Lp + t0 + (e & 15) * ST +
+                                 (e >> 4) * Q) = sum;
+      }
     }
     // the inputs again, from a cache: held through the modes they would not fit the registers
-    Lane<T, ST> uv, dv, zv, gv;
-    uv.fetch(u + t0, mine, nv);
-    dv.fetch(delta + t0, mine, nv);
-    if (Z) {
-      gv.fetch(dy + t0, mine, nv);
-      zv.fetch(z + t0, mine, nv);
-    }
-    float o[3][ST];
+    Lane<T, 4> uv, dv, zv, gv;
+    uv.fetch(u + t0, mine, nv, whole);
+    dv.fetch(delta + t0, mine, nv, whole);
+    gv.fetch(dy + t0, mine, nv, whole);
+    if (Z) zv.fetch(z + t0, mine, nv, whole);
+    float own[3][4];
+    if constexpr (NW > 1) {
+      // the first wave's part, then (after all have read it) the others' onto it; a wave past
+      // the modes' barriers has read the step sizes
 #pragma unroll
-    for (int j = 0; j < ST; ++j) {
-      const float uj = uv.v[j];
-      float rest;
-      const float d = fmaf(uj, q[j], -0.69314718056f * w[j]) * sigmoid_pair(dv.v[j] + bias, &rest);
-      o[0][j] = j < nv ? fmaf(dt[j], q[j], D * gy[j]) : 0.f;
-      o[1][j] = j < nv ? d : 0.f;
-      if (j < nv && live) {
-        sumD = fmaf(gy[j], uj, sumD);
-        sumb += d;
+      for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) own[i][j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        if (nw == k) {
+#pragma unroll
+          for (int e = 0; e < ST / 4; ++e) {
+            const int to = walk_at + slot<ST>(seg, e);
+            put_quad(xch[0][0] + to, q + 4 * e);
+            put_quad(xch[1][0] + to, w + 4 * e);
+            if (Z) put_quad(xch[2][0] + to, y + 4 * e);
+          }
+        }
+        __syncthreads();
+        add_quad(xch[0][0] + own_at, own[0]);
+        add_quad(xch[1][0] + own_at, own[1]);
+        if (Z) add_quad(xch[2][0] + own_at, own[2]);
+        __syncthreads();
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        own[0][j] = q[j];
+        own[1][j] = w[j];
+        own[2][j] = y[j];
+      }
+    }
+    float o[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float uj = uv.v[j], pre = dv.v[j] + bias, dtj = softplus(pre);
+      float rest, g = gv.v[j];
       if (Z) {
-        const float s = sigmoid_pair(zv.v[j], &rest);
-        const float e = gv.v[j] * y[j] * fmaf(zv.v[j] * s, rest, s);
-        o[2][j] = j < nv ? e : 0.f;
+        const float s = sigmoid_pair(zv.v[j], &rest), silu = zv.v[j] * s;
+        o[2][j] = g * fmaf(D, uj, own[2][j]) * fmaf(silu, rest, s);
+        g *= silu;
       }
+      o[0][j] = fmaf(dtj, own[0][j], D * g);
+      o[1][j] = fmaf(uj, own[0][j], -0.69314718056f * own[1][j]) * sigmoid_pair(pre, &rest);
+      if (j < nv && live) {
+        sumD = fmaf(g, uj, sumD);
+        sumb += o[1][j];
+      }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < (Z ? 3 : 2); ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = j < nv ? o[i][j] : 0.f;
     }
     if (live) {
-      const int ns = p.L - t0 - off;
-      store_n<T, ST>(spot(du + t0, mine), ns, o[0]);
-      store_n<T, ST>(spot(ddelta + t0, mine), ns, o[1]);
-      if (Z) store_n<T, ST>(spot(dz + t0, mine), ns, o[2]);
+      const int ns = p.L - t0 - w_.step;
+      store_lane<T, 4>(du + t0, mine, ns, whole, o[0]);
+      store_lane<T, 4>(ddelta + t0, mine, ns, whole, o[1]);
+      if (Z) store_lane<T, 4>(dz + t0, mine, ns, whole, o[2]);
     }
   }
+  // a row's own lanes: 16, or two rows of the vector unit's 16
   sumD = row_total(sumD);
   sumb = row_total(sumb);
-  if (live && first) {
-    float* to = p.part_h + ((row0 + r) * p.nseg + at.seg) * 2;
-    to[0] = sumD;
-    to[1] = sumb;
+  if (Work::LPR == 32) {
+    sumD = rows_sum(sumD);
+    sumb = rows_sum(sumb);
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = wave * 4 + k;
-    if (i < nrow)
-      for (int n = lane; n < p.N; n += 64) {
-        p.part_n[((row0 + i) * p.nseg + at.seg) * p.N + n] = dre[n * RP + i];
-        if (p.dx0 && at.seg == 0) p.dx0[(row0 + i) * p.N + n] = car[n * RP + i];
-      }
+  if (live && w_.step == 0) {
+    float* put = p.part_h + ((row0 + w_.own) * p.nseg + at.seg) * 2;
+    put[0] = sumD;
+    put[1] = sumb;
   }
+  if (r < nrow)
+    for (int n = (lane & 15) * NW + nw; n < p.N; n += 16 * NW) {
+      p.part_n[((row0 + r) * p.nseg + at.seg) * p.N + n] = dre.row(r)[n];
+      if (p.dx0 && at.seg == 0) p.dx0[(row0 + r) * p.N + n] = car.row(r)[n];
+    }
 }
 
 // dB and dC: the row blocks' parts in order; 4 steps to a thread.
@@ -1082,7 +1156,7 @@ Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
   Plan p{8, 8, 1, 1, 1};
   if (L <= 64) p.st = 4;
   const int tile = kSeg * p.st, ntile = std::max(1, (L + tile - 1) / tile), hg = H / G;
-  if (!backward && p.st == 8) p.rw = 4;
+  if (p.st == 8) p.rw = 4;
   p.nrb = (hg + 4 * p.rw - 1) / (4 * p.rw);
   const long have = std::max(1L, (long)B * G * p.nrb);
   const long want = have >= 256 ? 1 : std::min<long>(ntile, 512 / have);
@@ -1198,20 +1272,21 @@ hipError_t run_forward(const SelectiveCall& c, hipStream_t st) {
   return pl.st == 4 ? forward<T, 4, 8, 1>(a, st) : forward<T, 8, 4, 2>(a, st);
 }
 
-template <typename T, int ST, int RW>
+template <typename T, int ST, int RW, int NW>
 hipError_t backward(const Args& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.B * a.G * a.nrb * a.nseg), block(64 * RW);
-  const size_t lds = (size_t)a.N * (4 * RW + 1) * sizeof(float);
+  const dim3 grid((unsigned)a.B * a.G * a.nrb * a.nseg), block(64 * RW * NW);
+  const size_t lds = (size_t)padded(a.N) * (3 * 4 * RW + 4) * sizeof(float);
   if (a.nseg > 1) {
-    hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, block, 2 * lds, st, a);
+    hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, dim3(64 * RW),
+                       2 * (size_t)a.N * (4 * RW + 1) * sizeof(float), st, a);
     hipLaunchKernelGGL((selective_join_kernel<true>), dim3(blocks_of((long)a.B * a.H * a.N)),
                        dim3(256), 0, st, a.agg, a.aggS, a.log_re, a.dx, (long)a.B * a.H, a.H, a.N,
                        a.nseg);
   }
   if (a.z)
-    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, true>), grid, block, 3 * lds + 4, st, a);
+    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
   else
-    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, false>), grid, block, 3 * lds + 4, st, a);
+    hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, false>), grid, block, lds, st, a);
   if (a.L > 0)
     hipLaunchKernelGGL((selective_dbc_kernel<T>),
                        dim3((unsigned)a.B * a.G * 2 * a.N * (unsigned)((a.L + 1023) / 1024)),
@@ -1225,7 +1300,7 @@ hipError_t run_backward(const SelectiveCall& c, hipStream_t st) {
   Args a = make_args(c, pl);
   place(a, c, layout_of(pl, c.B, c.H, c.G, c.N, c.L, true));
   if (c.B > 0) {
-    const hipError_t e = pl.st == 4 ? backward<T, 4, 8>(a, st) : backward<T, 8, 8>(a, st);
+    const hipError_t e = pl.st == 4 ? backward<T, 4, 8, 1>(a, st) : backward<T, 8, 4, 2>(a, st);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(selective_param_kernel, dim3(blocks_of((long)c.H * (c.N + 2) * 16)), dim3(256),
