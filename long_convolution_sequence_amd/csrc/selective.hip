@@ -574,27 +574,45 @@ void selective_fwd_kernel(Args p) {
   }
 }
 
-// What enters each segment of a split row: the segments' ends joined in order,
-// a mode to a thread (REV: from the last to the first, `start` being the
-// gradient of the state after the row).
+// What enters each segment of a split row: the segments' ends joined in order
+// (REV: from the last to the first, `start` being the gradient of the state after
+// the row).  16 modes of a row to a workgroup, the segments in 16 parts: a part's
+// own end first, then what enters the part, then its segments (128 rows of 16
+// modes and 256 segments: 6 us, one thread walking a mode's segments 22).
 template <bool REV>
 __global__ __launch_bounds__(256) void selective_join_kernel(float* agg, const float* aggS,
                                                              const float* log_re,
-                                                             const float* start, long rows, int H,
-                                                             int N, int nseg) {
-  const long k = (long)blockIdx.x * 256 + threadIdx.x;
-  if (k >= rows * N) return;
-  const long row = k / N;
-  const int n = (int)(k - row * N);
-  const float kap = square_of(log_re[(row % H) * N + n]) * kLog2e;
-  float c = start ? start[k] : 0.f;
-  float* v = agg + row * nseg * N + n;
+                                                             const float* start, int H, int N,
+                                                             int nseg) {
+  __shared__ float2 ends[16][16];
+  const int nb = (N + 15) / 16;
+  const long row = blockIdx.x / (unsigned)nb;
+  const int m = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int n = (int)(blockIdx.x - (unsigned)row * nb) * 16 + m, at = min(n, N - 1);
+  const float kap = square_of(log_re[(row % H) * N + at]) * kLog2e;
+  float* v = agg + row * nseg * N + at;
   const float* s = aggS + row * nseg;
-  for (int j = 0; j < nseg; ++j) {
-    const int i = REV ? nseg - 1 - j : j;
-    const float e = v[(size_t)i * N];
-    v[(size_t)i * N] = c;
-    if (j + 1 < nseg) c = fmaf(exp2_fast(-kap * s[i]), c, e);
+  const int per = (nseg + 15) / 16, lo = part * per, hi = min(nseg, lo + per);
+  // the segment nobody joins, the last in order, has no end of its own
+  const auto segment = [&](int j) { return REV ? nseg - 1 - j : j; };
+  float S = 0.f, V = 0.f;
+#pragma unroll 4
+  for (int j = lo; j < hi; ++j) {
+    const int i = segment(j);
+    const float d = j + 1 < nseg ? s[i] : 0.f, e = j + 1 < nseg ? v[(size_t)i * N] : 0.f;
+    V = fmaf(exp2_fast(-kap * d), V, e);
+    S += d;
+  }
+  ends[part][m] = make_float2(S, V);
+  __syncthreads();
+  float c = start ? start[row * N + at] : 0.f;
+  for (int k = 0; k < part; ++k) c = fmaf(exp2_fast(-kap * ends[k][m].x), c, ends[k][m].y);
+#pragma unroll 4
+  for (int j = lo; j < hi; ++j) {
+    const int i = segment(j);
+    const float d = j + 1 < nseg ? s[i] : 0.f, e = j + 1 < nseg ? v[(size_t)i * N] : 0.f;
+    if (n < N) v[(size_t)i * N] = c;
+    c = fmaf(exp2_fast(-kap * d), c, e);
   }
 }
 
@@ -952,7 +970,8 @@ void selective_bwd_kernel(Args p) {
       __syncthreads();
       const int count = 128 * min(kModes, nm);
       for (int i = opaque((int)threadIdx.x); i < count; i += NT) {
-        const int e = i & 63, which = i / 64 & 1, m = i / 128;
+        // neighbouring threads take neighbouring steps
+        const int e = (i & 3) * 16 + (i >> 2 & 15), which = i / 64 & 1, m = i / 128;
         Part sum = slab[0][m][which][e];
 #pragma unroll
         for (int o = 1; o < RW; ++o) sum += slab[o][m][which][e];
@@ -1103,45 +1122,61 @@ __global__ __launch_bounds__(256) void selective_param_kernel(Args p) {
     p.ddt_bias[h] = (float)s;
 }
 
-// One token: `lpr` lanes to a row (a power of two, at most 64), four modes each.
-template <typename T>
+// One token: `lpr` lanes to a row (a power of two, at most 64), four modes each;
+// V rows of the batch to a lane, which share the channel's parameters and are all
+// asked for at once.
+template <typename T, int V>
 __global__ __launch_bounds__(256) void selective_step_kernel(Args p, int lpr) {
-  const long row = (long)blockIdx.x * (256 / lpr) + threadIdx.x / lpr;
-  const int l = threadIdx.x % lpr;
-  const bool in = row < (long)p.B * p.H;
-  const long b = in ? row / p.H : 0;
-  const int h = in ? (int)(row - b * p.H) : 0;
-  const bool live = in && (!p.lens || p.lens[b] > 0);
-  const int n = 4 * l, m = in ? min(max(p.N - n, 0), 4) : 0, nv = live ? m : 0;
-  const size_t xo = (size_t)(in ? row : 0) * p.N + n;
-  const size_t bc = (size_t)(h / p.HG) * p.N + n;
-  float x[4], k[4], Bv[4], Cv[4];
-  load_n<float, 4>(p.x0 + xo, p.x0 ? m : 0, x);
-  load_n<float, 4>(p.log_re + (size_t)h * p.N + n, nv, k);
-  load_n<T, 4>(static_cast<const T*>(p.Bm) + (size_t)(b * p.sB) + bc, nv, Bv);
-  load_n<T, 4>(static_cast<const T*>(p.Cm) + (size_t)(b * p.sC) + bc, nv, Cv);
-  float u = 0.f, d = 0.f, z = 0.f;
-  if (live) {
-    u = (float)static_cast<const T*>(p.u)[(size_t)(b * p.su) + h];
-    d = (float)static_cast<const T*>(p.delta)[(size_t)(b * p.sd) + h];
-    if (p.z) z = (float)static_cast<const T*>(p.z)[(size_t)(b * p.sz) + h];
-  }
-  const float dt = softplus(d + (p.dt_bias ? p.dt_bias[h] : 0.f));
-  float y = 0.f;
+  // workgroups: a batch row's (or V rows') channels side by side
+  const unsigned block = __builtin_amdgcn_readfirstlane(blockIdx.x);
+  const unsigned per = (unsigned)(p.H * lpr + 255) / 256, group = block / per;
+  const int at = (int)((block - group * per) * 256 + threadIdx.x), b0 = (int)group * V;
+  const int l = at & (lpr - 1), row = at / lpr;
+  const bool in = row < p.H;
+  const int h = in ? row : 0;
+  const int n = 4 * l, m = in ? min(max(p.N - n, 0), 4) : 0;
+  const size_t bc = (p.G > 1 ? (size_t)(h / p.HG) * p.N : 0) + n;
+  float x[V][4], Bv[V][4], Cv[V][4], k[4], u[V], d[V], z[V];
+  bool live[V];
+  load_n<float, 4>(p.log_re + (size_t)h * p.N + n, m, k);
+  const float bias = p.dt_bias ? p.dt_bias[h] : 0.f, D = p.D ? p.D[h] : 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j < nv) {
-      x[j] = fmaf(exp2_fast(-(square_of(k[j]) * kLog2e) * dt), x[j], dt * u * Bv[j]);
-      y = fmaf(Cv[j], x[j], y);
+  for (int i = 0; i < V; ++i) {
+    const int b = min(b0 + i, p.B - 1);
+    live[i] = b0 + i < p.B && (!p.lens || p.lens[b] > 0);
+    const int nv = live[i] ? m : 0;
+    load_n<float, 4>(p.x0 + ((size_t)b * p.H + h) * p.N + n, p.x0 && b0 + i < p.B ? m : 0, x[i]);
+    load_n<T, 4>(static_cast<const T*>(p.Bm) + (size_t)(b * p.sB) + bc, nv, Bv[i]);
+    load_n<T, 4>(static_cast<const T*>(p.Cm) + (size_t)(b * p.sC) + bc, nv, Cv[i]);
+    u[i] = d[i] = z[i] = 0.f;
+    if (live[i] && in) {
+      u[i] = (float)static_cast<const T*>(p.u)[(size_t)(b * p.su) + h];
+      d[i] = (float)static_cast<const T*>(p.delta)[(size_t)(b * p.sd) + h];
+      if (p.z) z[i] = (float)static_cast<const T*>(p.z)[(size_t)(b * p.sz) + h];
     }
   }
-  if (p.xT) store_n<float, 4>(p.xT + xo, m, x);
-  for (int o = 1; o < lpr; o <<= 1) y += __shfl_xor(y, o);
-  if (!in || l) return;
-  if (p.D) y = fmaf(p.D[h], u, y);
-  float rest;
-  if (p.z) y *= z * sigmoid_pair(z, &rest);
-  static_cast<T*>(p.y)[row] = (T)(live ? y : 0.f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k[j] = square_of(k[j]) * kLog2e;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float dt = softplus(d[i] + bias), drive = dt * u[i];
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float next = fmaf(exp2_fast(-k[j] * dt), x[i][j], drive * Bv[i][j]);
+      x[i][j] = live[i] ? next : x[i][j];
+      y += j < m ? Cv[i][j] * next : 0.f;
+    }
+    for (int o = 1; o < lpr; o <<= 1) y += __shfl_xor(y, o);
+    if (b0 + i >= p.B || !in) continue;
+    const size_t to = (size_t)(b0 + i) * p.H + h;
+    if (p.xT) store_n<float, 4>(p.xT + to * p.N + n, m, x[i]);
+    if (l) continue;
+    y = fmaf(D, u[i], y);
+    float rest;
+    if (p.z) y *= z[i] * sigmoid_pair(z[i], &rest);
+    static_cast<T*>(p.y)[to] = (T)(live[i] ? y : 0.f);
+  }
 }
 
 // How rows go to workgroups.
@@ -1249,6 +1284,7 @@ void place(Args& a, const SelectiveCall& c, const Layout& o) {
 }
 
 unsigned blocks_of(long n) { return (unsigned)((n + 255) / 256); }
+unsigned join_blocks(const Args& a) { return (unsigned)a.B * a.H * ((a.N + 15) / 16); }
 
 template <typename T, int ST, int RW, int NW>
 hipError_t forward(const Args& a, hipStream_t st) {
@@ -1256,9 +1292,8 @@ hipError_t forward(const Args& a, hipStream_t st) {
   const size_t lds = (size_t)padded(a.N) * (2 * 4 * RW + 2) * sizeof(float);
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
-    hipLaunchKernelGGL((selective_join_kernel<false>), dim3(blocks_of((long)a.B * a.H * a.N)),
-                       dim3(256), 0, st, a.agg, a.aggS, a.log_re, a.x0, (long)a.B * a.H, a.H, a.N,
-                       a.nseg);
+    hipLaunchKernelGGL((selective_join_kernel<false>), dim3(join_blocks(a)), dim3(256), 0, st, a.agg,
+                       a.aggS, a.log_re, a.x0, a.H, a.N, a.nseg);
   }
   hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, false>), grid, block, lds, st, a);
   return hipGetLastError();
@@ -1279,9 +1314,8 @@ hipError_t backward(const Args& a, hipStream_t st) {
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, dim3(64 * RW),
                        2 * (size_t)a.N * (4 * RW + 1) * sizeof(float), st, a);
-    hipLaunchKernelGGL((selective_join_kernel<true>), dim3(blocks_of((long)a.B * a.H * a.N)),
-                       dim3(256), 0, st, a.agg, a.aggS, a.log_re, a.dx, (long)a.B * a.H, a.H, a.N,
-                       a.nseg);
+    hipLaunchKernelGGL((selective_join_kernel<true>), dim3(join_blocks(a)), dim3(256), 0, st, a.agg,
+                       a.aggS, a.log_re, a.dx, a.H, a.N, a.nseg);
   }
   if (a.z)
     hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
@@ -1308,15 +1342,21 @@ hipError_t run_backward(const SelectiveCall& c, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <typename T, int V>
+hipError_t step(const Args& a, int lpr, hipStream_t st) {
+  const long blocks = (long)((a.B + V - 1) / V) * ((a.H * lpr + 255) / 256);
+  hipLaunchKernelGGL((selective_step_kernel<T, V>), dim3((unsigned)blocks), dim3(256), 0, st, a, lpr);
+  return hipGetLastError();
+}
+
+// Few rows fill the device sooner with a row to a lane; many are bound by memory,
+// and by how much of it is under way.
 template <typename T>
 hipError_t run_step(const SelectiveCall& c, hipStream_t st) {
   const Args a = make_args(c, Plan{8, 8, 1, 1, 1});
   int lpr = 1;
   while (lpr * 4 < c.N) lpr *= 2;
-  const long rows = (long)c.B * c.H, per = 256 / lpr;
-  hipLaunchKernelGGL((selective_step_kernel<T>), dim3((unsigned)((rows + per - 1) / per)),
-                     dim3(256), 0, st, a, lpr);
-  return hipGetLastError();
+  return (long)c.B * c.H * lpr >= (1L << 20) ? step<T, 2>(a, lpr, st) : step<T, 1>(a, lpr, st);
 }
 
 }  // namespace

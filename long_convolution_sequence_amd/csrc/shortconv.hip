@@ -42,7 +42,7 @@ struct Args {
   int ntile, nseg, seg_tiles;
 };
 
-__device__ __forceinline__ int row_len(const Args& p, long b) {
+__device__ __forceinline__ int row_len(const Args& p, int b) {
   if (!p.lens) return p.L;
   return min(max(p.lens[b], 0), p.L);
 }
@@ -84,17 +84,31 @@ __device__ __forceinline__ float tap_sum(const float* e, const float* w, float b
   return s;
 }
 
+// The 32-bit number of a row (B H <= 2^24): batch row and channel by an unsigned
+// division, or one for the whole wave.
+template <bool WAVE>
+__device__ __forceinline__ void place_row(unsigned row, int H, int* b, int* h) {
+  if (WAVE) row = __builtin_amdgcn_readfirstlane(row);
+  const unsigned q = row / (unsigned)H;
+  *b = (int)q;
+  *h = (int)(row - q * (unsigned)H);
+}
+
 // A row takes lpr lanes (a power of two, at most the workgroup's 256) and, if
-// it has more than 8 lpr steps, several workgroups.
-template <typename T, int K>
+// it has more than 8 lpr steps, several workgroups.  WAVE: 64 lanes at least, so
+// that a wave's row, weights and end are scalars (4 taps, 2^25 bf16 elements in
+// rows of 2048: 38 us with a 64-bit division per lane, 31 so).
+template <typename T, int K, bool WAVE>
 __global__ __launch_bounds__(256) void shortconv_fwd_kernel(Args p) {
-  const long rb = blockIdx.x / (unsigned)p.ntile;
-  const int tile = (int)(blockIdx.x - (unsigned)rb * (unsigned)p.ntile);
-  const long row = rb * (256 / p.lpr) + threadIdx.x / p.lpr;
-  const int t = (tile * p.lpr + (int)threadIdx.x % p.lpr) * 8;
-  if (row >= p.rows || (t >= p.L && t > 0)) return;  // of a row without steps the state passes
-  const long b = row / p.H;
-  const int h = (int)(row - b * p.H), len = row_len(p, b);
+  const unsigned rb = blockIdx.x / (unsigned)p.ntile;
+  const int tile = (int)(blockIdx.x - rb * (unsigned)p.ntile);
+  unsigned row = rb * (256u / p.lpr) + threadIdx.x / (unsigned)p.lpr;
+  if (WAVE) row = __builtin_amdgcn_readfirstlane(row);
+  const int t = (tile * p.lpr + (int)(threadIdx.x & (p.lpr - 1))) * 8;
+  if (row >= (unsigned)p.rows || (t >= p.L && t > 0)) return;  // without steps the state passes
+  int b, h;
+  place_row<WAVE>(row, p.H, &b, &h);
+  const int len = row_len(p, b);
   const T* u = static_cast<const T*>(p.u) + (size_t)(b * p.su) + (size_t)h * p.L;
   float w[K], e[K + 7], out[8];
   const float bias = load_taps<K>(p, h, w);
@@ -103,13 +117,13 @@ __global__ __launch_bounds__(256) void shortconv_fwd_kernel(Args p) {
   for (int j = 0; j < 8; ++j) out[j] = tap_sum<K>(e + j, w, bias);
   if (p.silu) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float rest;
-      out[j] *= sigmoid_pair(out[j], &rest);
-    }
+    for (int j = 0; j < 8; ++j)
+      out[j] *= __builtin_amdgcn_rcpf(1.f + exp2_fast(-kLog2e * out[j]));
   }
+  if (t + 8 > len) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) out[j] = t + j < len ? out[j] : 0.f;
+    for (int j = 0; j < 8; ++j) out[j] = t + j < len ? out[j] : 0.f;
+  }
   store_n<T, 8>(static_cast<T*>(p.y) + (size_t)row * p.L + t, p.L - t, out);
   // the state after the row: the lane that has read the one before it (which
   // may lie in the same place) writes it
@@ -118,32 +132,32 @@ __global__ __launch_bounds__(256) void shortconv_fwd_kernel(Args p) {
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
       const int i = len + k;
-      s[k] = i < K - 1 ? (p.x0 ? p.x0[row * (K - 1) + i] : 0.f) : (float)u[i - (K - 1)];
+      s[k] = i < K - 1 ? (p.x0 ? p.x0[(size_t)row * (K - 1) + i] : 0.f) : (float)u[i - (K - 1)];
     }
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) p.xT[row * (K - 1) + k] = s[k];
+    for (int k = 0; k < K - 1; ++k) p.xT[(size_t)row * (K - 1) + k] = s[k];
   }
 }
 
 // One token: a channel to a thread.
 template <typename T, int K>
 __global__ __launch_bounds__(256) void shortconv_step_kernel(Args p) {
-  const long row = (long)blockIdx.x * 256 + threadIdx.x;
-  if (row >= p.rows) return;
-  const long b = row / p.H;
-  const int h = (int)(row - b * p.H);
+  const unsigned row = blockIdx.x * 256u + threadIdx.x;
+  if (row >= (unsigned)p.rows) return;
+  int b, h;
+  place_row<false>(row, p.H, &b, &h);
   const bool live = !p.lens || p.lens[b] > 0;
   float w[K], e[K];
   const float bias = load_taps<K>(p, h, w);
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) e[k] = p.x0 ? p.x0[row * (K - 1) + k] : 0.f;
+  for (int k = 0; k < K - 1; ++k) e[k] = p.x0 ? p.x0[(size_t)row * (K - 1) + k] : 0.f;
   e[K - 1] = live ? (float)static_cast<const T*>(p.u)[(size_t)(b * p.su) + h] : 0.f;
   float v = tap_sum<K>(e, w, bias), rest;
   if (p.silu) v *= sigmoid_pair(v, &rest);
   static_cast<T*>(p.y)[row] = (T)(live ? v : 0.f);
   if (p.xT) {
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) p.xT[row * (K - 1) + k] = live ? e[k + 1] : e[k];
+    for (int k = 0; k < K - 1; ++k) p.xT[(size_t)row * (K - 1) + k] = live ? e[k + 1] : e[k];
   }
 }
 
@@ -158,22 +172,24 @@ __device__ __forceinline__ float next_lane(float x) {
 // walks tiles of 63 lanes, the last lane only forming the p that the 63rd
 // needs.  The sums over a row's (or segment's) steps stay with the lanes until
 // its end.
-template <typename T, int K>
+template <typename T, int K, bool WHOLE>
 __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
   const int lane = threadIdx.x & 63;
-  const long wave = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const bool whole = p.ntile > 1;  // a wave to a row or segment
-  const long rs = whole ? wave : wave * (64 / p.lpr) + lane / p.lpr;
-  long row = rs / p.nseg;
-  const int seg = (int)(rs - row * p.nseg);
-  const bool in = row < p.rows;
-  if (!in) row = p.rows - 1;
-  const long b = row / p.H;
-  const int h = (int)(row - b * p.H), len = row_len(p, b);
-  const int gl = whole ? lane : lane % p.lpr;
+  const unsigned wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  constexpr bool whole = WHOLE;  // a wave to a row or segment
+  const unsigned rs = whole ? wave : wave * (64u / p.lpr) + lane / p.lpr;
+  unsigned row = whole ? rs / (unsigned)p.nseg : rs;
+  const int seg = whole ? (int)(rs - row * (unsigned)p.nseg) : 0;
+  const bool in = row < (unsigned)p.rows;
+  if (!in) row = (unsigned)p.rows - 1;
+  int b, h;
+  place_row<whole>(row, p.H, &b, &h);
+  const int len = row_len(p, b);
+  const int gl = whole ? lane : lane & (p.lpr - 1);
   const bool helper = whole && lane == 63;
   const T* u = static_cast<const T*>(p.u) + (size_t)(b * p.su) + (size_t)h * p.L;
   const T* dy = static_cast<const T*>(p.dy) + (size_t)row * p.L;
+  const size_t xs = (size_t)row * (K - 1);
   T* du = static_cast<T*>(p.du) + (size_t)(b * p.sdu) + (size_t)h * p.L;
   float w[K], acc[K + 1];
   const float bias = load_taps<K>(p, h, w);
@@ -199,8 +215,12 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
         const float v = tap_sum<K>(e + j, w, bias);
         float rest;
         const float s = sigmoid_pair(v, &rest);
-        // behind the row's end, where dy counts as 0, whatever the parameters hold
-        d[j] = t + j < len ? d[j] * fmaf(v * s, rest, s) : 0.f;
+        d[j] *= fmaf(v * s, rest, s);
+      }
+      // behind the row's end, where dy counts as 0, whatever the parameters hold
+      if (t + 8 > len) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = t + j < len ? d[j] : 0.f;
       }
     }
 #pragma unroll
@@ -222,11 +242,13 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int i = t + j + K - 1 - len;
-          if (i >= 0 && t + j < len) g[j] += p.dx[row * (K - 1) + i];
+          if (i >= 0 && t + j < len) g[j] += p.dx[xs + i];
         }
       }
+      if (t + 8 > len) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = t + j < len ? g[j] : 0.f;
+        for (int j = 0; j < 8; ++j) g[j] = t + j < len ? g[j] : 0.f;
+      }
       if (t < p.L) store_n<T, 8>(du + t, p.L - t, g);
       if (t < len) {
 #pragma unroll
@@ -243,8 +265,8 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
 #pragma unroll
           for (int k = 0; k <= i; ++k)
             if (i - k < 8) s = fmaf(w[k], d[i - k], s);
-          if (p.dx && i >= len) s += p.dx[row * (K - 1) + i - len];
-          p.dx0[row * (K - 1) + i] = len > 0 ? s : (p.dx ? p.dx[row * (K - 1) + i] : 0.f);
+          if (p.dx && i >= len) s += p.dx[xs + i - len];
+          p.dx0[xs + i] = len > 0 ? s : (p.dx ? p.dx[xs + i] : 0.f);
         }
       }
     }
@@ -255,7 +277,7 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
     for (int k = 0; k <= K; ++k) acc[k] += __shfl_xor(acc[k], o);
   if (in && gl == 0) {
 #pragma unroll
-    for (int k = 0; k <= K; ++k) p.part[rs * (K + 1) + k] = acc[k];
+    for (int k = 0; k <= K; ++k) p.part[(size_t)rs * (K + 1) + k] = acc[k];
   }
 }
 
@@ -347,7 +369,12 @@ hipError_t run(const ShortconvCall& c, Pass pass, hipStream_t st) {
     a.lpr = pow2_from(chunks, 256);
     a.ntile = (chunks + a.lpr - 1) / a.lpr;
     const long per = 256 / a.lpr, blocks = (a.rows + per - 1) / per * a.ntile;
-    hipLaunchKernelGGL((shortconv_fwd_kernel<T, K>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    if (a.lpr >= 64)
+      hipLaunchKernelGGL((shortconv_fwd_kernel<T, K, true>), dim3((unsigned)blocks), dim3(256), 0,
+                         st, a);
+    else
+      hipLaunchKernelGGL((shortconv_fwd_kernel<T, K, false>), dim3((unsigned)blocks), dim3(256), 0,
+                         st, a);
   } else {
     BwdPlan pl = bwd_plan(a.rows, c.L);
     a.lpr = pl.lpr;
@@ -357,7 +384,12 @@ hipError_t run(const ShortconvCall& c, Pass pass, hipStream_t st) {
     if (a.rows > 0) {
       const long per = pl.ntile > 1 ? 4 : 4 * (64 / pl.lpr);
       const long blocks = (a.rows * pl.nseg + per - 1) / per;
-      hipLaunchKernelGGL((shortconv_bwd_kernel<T, K>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+      if (pl.ntile > 1)
+        hipLaunchKernelGGL((shortconv_bwd_kernel<T, K, true>), dim3((unsigned)blocks), dim3(256), 0,
+                           st, a);
+      else
+        hipLaunchKernelGGL((shortconv_bwd_kernel<T, K, false>), dim3((unsigned)blocks), dim3(256), 0,
+                           st, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
