@@ -161,19 +161,36 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
   const size_t base = (size_t)b * p.H * p.L + t0;
   const size_t plane = (size_t)p.B * p.L, at = (size_t)b * p.L + t;
   const auto channel = [&](int j) { return (j / 4) * C4 + rs * 4 + (j & 3); };
-  // lanes past the last channel take the last one's place; they read it again and
-  // never count or store it
-  const auto spot = [&](int j) {
-    return (size_t)min(channel(j), p.H - 1) * p.L + lt * VE;
+  // groups of channels that all lanes have need no check (a scalar's choice)
+  const auto has = [&](int j) { return (j / 4 + 1) * C4 <= p.H || channel(j) < p.H; };
+  // A lane's place in a strip's first four channels, made opaque: the compiler
+  // would keep the address of every channel of every tensor in registers.
+  const size_t own = ((size_t)rs * 4 * p.L + lt * VE) * sizeof(T);
+  const auto spot = [&](const T* row, int j) {
+    size_t o = own;
+    asm volatile("" : "+v"(o));
+    const char* c = reinterpret_cast<const char*>(row + (size_t)((j / 4) * C4 + (j & 3)) * p.L);
+    return const_cast<T*>(reinterpret_cast<const T*>(c + o));
   };
+  // channels past the last one, and steps behind the row's end, are 0
   const auto get = [&](Vec& v, const T* row, int j) {
-    if (whole)
-      v.load(row + spot(j));
+    if (whole && (j / 4 + 1) * C4 <= p.H)
+      v.load(spot(row, j));
     else
-      v.load(row + spot(j), nv, (T)0.f);
+      v.load(spot(row, j), has(j) ? nv : 0, (T)0.f);
+  };
+  // with many channels held, no more than four of them in flight
+  const auto pause = [&](int j) {
+    if (KH > 8 && j % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+  };
+  // forget what was derived from the held words (their float32 values)
+  const auto refresh = [&](Vec* v) {
+#pragma unroll
+    for (int j = 0; j < KH; ++j) v[j].refresh();
   };
   const T* x = static_cast<const T*>(p.x) + base;
   const T* y = static_cast<const T*>(p.y) + (FORM ? base : 0);
+  T* o = static_cast<T*>(p.o) + (FORM ? base : 0);
   Vec a[KH];
   float mean[1][VE], s[1][VE];
   uint32_t top[VE];
@@ -186,7 +203,7 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
     if (LAYER) {
 #pragma unroll
       for (int j = 0; j < KH; ++j)
-        if (channel(j) < p.H)
+        if (has(j))
 #pragma unroll
           for (int k = 0; k < VE; ++k) mean[0][k] += a[j][k];
       strip_sum<NT, LT, VE, 1>(mean, reinterpret_cast<float*>(buf));
@@ -195,12 +212,13 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
     }
 #pragma unroll
     for (int j = 0; j < KH; ++j)
-      if (channel(j) < p.H)
+      if (!LAYER || has(j))
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
           const float d = a[j][k] - mean[0][k];
           s[0][k] = fmaf(d, d, s[0][k]);
         }
+    refresh(a);
     strip_sum<NT, LT, VE, 1>(s, reinterpret_cast<float*>(buf));
     float rstd[VE];
 #pragma unroll
@@ -212,8 +230,9 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
     }
 #pragma unroll
     for (int j = 0; j < KH; ++j) {
+      pause(j);
       const int h = channel(j);
-      const bool in = h < p.H;
+      const bool in = has(j);
       Vec xv, gv;
       get(xv, x, j);
       if (p.g) get(gv, g, j);
@@ -227,11 +246,13 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
       }
       live_only<VE>(out, nv, whole);
       a[j].set(out);
-      if (in) a[j].store(static_cast<T*>(p.o) + base + spot(j), ns);
+      a[j].refresh();
+      if (in) a[j].store(spot(o, j), ns);
     }
   } else if (FORM == 1) {
 #pragma unroll
     for (int j = 0; j < KH; ++j) {
+      pause(j);
       Vec xv, yv;
       get(xv, x, j);
       get(yv, y, j);
@@ -239,7 +260,8 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
 #pragma unroll
       for (int k = 0; k < VE; ++k) out[k] = xv[k] + yv[k];
       a[j].set(out);
-      if (channel(j) < p.H) a[j].store(static_cast<T*>(p.o) + base + spot(j), ns);
+      a[j].refresh();
+      if (has(j)) a[j].store(spot(o, j), ns);
     }
   } else {
 #pragma unroll
@@ -254,18 +276,18 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
   if (LAYER) {
 #pragma unroll
     for (int j = 0; j < KH; ++j)
-      if (channel(j) < p.H)
 #pragma unroll
-        for (int k = 0; k < VE; ++k) mean[0][k] += a[j][k];
+      for (int k = 0; k < VE; ++k) mean[0][k] += a[j][k];
+    refresh(a);
     strip_sum<NT, LT, VE, 1>(mean, reinterpret_cast<float*>(buf));
 #pragma unroll
     for (int k = 0; k < VE; ++k) mean[0][k] *= inv_h;
   }
 #pragma unroll
   for (int j = 0; j < KH; ++j) {
-    const int h = channel(j);
-    if (h >= p.H) continue;
-    const float w = p.w[h];
+    pause(j);
+    if (!has(j)) continue;
+    const float w = p.w[channel(j)];
 #pragma unroll
     for (int k = 0; k < VE; ++k) {
       const float d = a[j][k] - mean[0][k];
@@ -273,6 +295,7 @@ __global__ __launch_bounds__(NT) void resnorm8_kernel(Args p) {
       top[k] = max(top[k], abs_bits(d * w));
     }
   }
+  refresh(a);
   strip_sum_max<NT, LT, VE>(s[0], top, buf);
   const float most = p.e4m3 ? 448.f : 127.f;
   float rstd[VE], unit[VE], mul[VE];
