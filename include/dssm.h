@@ -671,7 +671,7 @@ typedef struct {
 
 /* Bytes of workspace of dssm_selective_forward or (backward != 0)
  * dssm_selective_backward (host only).  Requires H <= 65535, B H <= 2^24, L <=
- * 2^24, B H L <= 2^40, B H N ceil(L / 128) <= 2^36. */
+ * 2^24, B H L <= 2^40, B H N ceil(L / 128) <= 2^36, B G N ceil(L / 1024) <= 2^29. */
 int dssm_selective_workspace_size(const dssm_selective_shape* s, int backward, size_t* bytes);
 
 /* Bytes of a checkpoint: the states [B, H, ceil(L / 128), N] float32 entering
