@@ -595,24 +595,26 @@ __global__ __launch_bounds__(256) void selective_join_kernel(float* agg, const f
   const int per = (nseg + 15) / 16, lo = part * per, hi = min(nseg, lo + per);
   // the segment nobody joins, the last in order, has no end of its own
   const auto segment = [&](int j) { return REV ? nseg - 1 - j : j; };
+  // steps of no length decay nothing, whatever the parameter
+  const auto decay = [&](float d) { return d == 0.f ? 1.f : exp2_fast(-kap * d); };
   float S = 0.f, V = 0.f;
 #pragma unroll 4
   for (int j = lo; j < hi; ++j) {
     const int i = segment(j);
     const float d = j + 1 < nseg ? s[i] : 0.f, e = j + 1 < nseg ? v[(size_t)i * N] : 0.f;
-    V = fmaf(exp2_fast(-kap * d), V, e);
+    V = fmaf(decay(d), V, e);
     S += d;
   }
   ends[part][m] = make_float2(S, V);
   __syncthreads();
   float c = start ? start[row * N + at] : 0.f;
-  for (int k = 0; k < part; ++k) c = fmaf(exp2_fast(-kap * ends[k][m].x), c, ends[k][m].y);
+  for (int k = 0; k < part; ++k) c = fmaf(decay(ends[k][m].x), c, ends[k][m].y);
 #pragma unroll 4
   for (int j = lo; j < hi; ++j) {
     const int i = segment(j);
     const float d = j + 1 < nseg ? s[i] : 0.f, e = j + 1 < nseg ? v[(size_t)i * N] : 0.f;
     if (n < N) v[(size_t)i * N] = c;
-    c = fmaf(exp2_fast(-kap * d), c, e);
+    c = fmaf(decay(d), c, e);
   }
 }
 

@@ -121,3 +121,124 @@ def test_forward(shape):
         assert (np.abs(a - b) <= 2 * c_norm(H) * STEP * np.maximum(np.abs(b), 1.0)).all()
     again = run(s)
     assert torch.equal(q.view(torch.int8), again[1].view(torch.int8)) and torch.equal(qs, again[2])
+
+
+@pytest.mark.parametrize("form", ["int8", "e4m3"])
+@pytest.mark.parametrize("H,L", [(40, 9), (600, 3), (2500, 1), (100, 1)])
+def test_steps_without_numbers(H, L, form):
+    """A step that holds Inf or NaN stands for NaN, one of zeros for 0, its neighbours for what
+    they were."""
+    torch = torch_()
+    s = prepared(6, H, L, "bf16", form, "a", seed=H)
+    _, q0, s0 = run(s)
+    s["x"][1, H // 2, L // 2] = float("inf")
+    s["x"][2, 0, 0] = float("nan")
+    s["x"][3, :, L - 1] = s["y"][3, :, L - 1] = 0.0
+    s["x"][4, :, 0] *= 1e-38
+    s["y"][4, :, 0] = 0.0
+    _, q, qs = run(s)
+    touched = torch.zeros(6, L, dtype=torch.bool, device="cuda")
+    touched[1, L // 2] = touched[2, 0] = touched[3, L - 1] = touched[4, 0] = True
+    assert torch.isnan(qs[1, L // 2]) and torch.isnan(qs[2, 0])
+    assert qs[3, L - 1] == 0.0 and qs[4, 0] == 0.0
+    assert not q.float()[touched].any()
+    assert torch.equal(q.view(torch.int8)[~touched], q0.view(torch.int8)[~touched])
+    assert torch.equal(qs[~touched], s0[~touched])
+
+
+@pytest.mark.parametrize("H,L", [(40, 33), (700, 9), (700, 1)])
+def test_rows_of_no_steps_with_any_parameters(H, L):
+    torch = torch_()
+    s = prepared(3, H, L, "f32", "int8", "pgr", seed=5)
+    s["lens"][:] = torch.tensor([0, 0, 0], dtype=torch.int32)
+    for k in ("w_post", "scale", "w_pre"):
+        s[k].fill_(float("nan"))
+    o, q, qs = run(s)
+    assert not o.any() and not q.any() and not qs.any()
+
+
+@pytest.mark.parametrize("L", [33, 1])
+def test_captured_and_replayed_on_streams(L):
+    torch = torch_()
+    s = prepared(3, 300, L, "bf16", "e4m3", "pg", seed=7)
+    run(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(s)
+    other = torch.cuda.Stream()
+    for rep in range(4):
+        new = prepared(3, 300, L, "bf16", "e4m3", "pg", seed=40 + rep)
+        for k in ("x", "y", "g", "w_post", "scale", "w_pre"):
+            s[k].copy_(new[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        torch.cuda.synchronize()
+        eager = run(s, stream=other)
+        torch.cuda.synchronize()
+        for a, b in zip(got, eager):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), rep
+
+
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("L", [40, 1])
+def test_gradients_of_the_sum_through_the_norms_backward_pass(L, layer):
+    """o = x + y, n = norm(o) w: the statistics with the residual norm's backward pass, called
+    without y, give the gradient of both."""
+    torch = torch_()
+    B, H = 3, 70
+    s = prepared(B, H, L, "f32", "int8", "al" if layer else "a", seed=9)
+    o, _, _, stats = run(s, stats=True)
+    g = bd.resnorm_backward(o, None, None, stats, None, None, s["w_pre"], s["do"], s["dn"],
+                            norm=s["norm"])
+    one = np.zeros((B, H, L))
+    args = (np64(o), one + 1.0, None, np.ones(H), np.zeros(H), np64(s["w_pre"]), np64(s["do"]),
+            np64(s["dn"]), layer, EPS)
+    ref = oracle.resnorm_backward(*args)
+    mag = oracle.resnorm_backward(*args, magnitude=True)
+    close(g["dx"], ref[0], mag[0], 2 * c_norm(H), "f32", "dx")
+    close(g["dw_pre"], ref[-1], mag[-1], 2 * c_norm(H) + B * L, "f32", "dw_pre")
+
+
+def test_binding_refuses():
+    torch = torch_()
+    s = prepared(2, 8, 20, "bf16", "int8", "pg", seed=1)
+    x, y, g, wp, sc, wr = (s[k] for k in ("x", "y", "g", "w_post", "scale", "w_pre"))
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, g, None, None, wr)  # a gate without the norm it follows
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, None, None, sc, wr)
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, None, g, None, None, wr)
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, g, wp, sc, None)
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, g, wp, sc, wr, form=2)
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, g, wp, sc, wr, q=torch.empty(2, 8, 20, dtype=torch.int8,
+                                                              device="cuda"))
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, g, wp, sc, wr, form=bd.Q8_E4M3,
+                            q=torch.empty(2, 20, 8, dtype=torch.int8, device="cuda"))
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x, y, g, wp, sc, wr, qs=torch.empty(2, 8, device="cuda"))
+    with pytest.raises(TypeError):
+        bd.resnorm8_forward(x, y.float(), g, wp, sc, wr)
+    with pytest.raises(ValueError):
+        bd.resnorm8_forward(x[..., ::2], y[..., ::2], None, wp, sc, wr)
+    with pytest.raises(bd.DSSMError):
+        bd.resnorm8_forward(x, y, g, wp, sc, wr, o=x)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last steps of the last row against the same steps alone."""
+    torch = torch_()
+    B, H, L = 2, 1100, 1 << 20
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(B, H, L, device="cuda", generator=gen, dtype=torch.bfloat16)
+    w = torch.randn(H, device="cuda", generator=gen)
+    _, q, qs = bd.resnorm8_forward(x, None, None, None, None, w)
+    tail = x[1:, :, L - 64:].contiguous()
+    _, q2, s2 = bd.resnorm8_forward(tail, None, None, None, None, w)
+    assert torch.equal(q[1:, L - 64:], q2) and torch.equal(qs[1:, L - 64:], s2)
