@@ -12,17 +12,24 @@
 //   dlog_re = -2 log_re sum_{b,t} w dt,  dD = sum p u,  ddt_bias = sum ddelta,
 //   dz = dy (sum_n C x + D u) silu'(z),  dx0 = a_0 G_0.
 //
-// Layout.  A row (b, h) takes 16 lanes, ST consecutive steps each; a wave four
-// rows.  16 lanes are what the data-parallel primitives shift and rotate
-// within, so that joining the lanes of a mode costs about one vector operation
-// per step where a lane holds 16 steps; the modes are walked one by one, a
-// lane's decays and drives of a mode in registers.  B and C are the same for
+// Layout.  A row (b, h) takes 16 lanes, ST = 8 consecutive steps each; a wave four
+// rows.  16 lanes are what the data-parallel primitives shift and rotate within:
+// joining the lanes of a mode takes 8 vector operations, one per step.  The modes
+// are walked two at a time, a lane's decays and drives of them in registers, and
+// two waves share the modes of a row.  With 16 steps to a lane and one wave the
+// joins cost half, but the registers leave two waves per SIMD instead of four, and
+// instructions issue slower for it: forward the same (0.20 ms of 4 x 4096 rows of
+// 2048 steps and 16 modes), backward 643 us against 595.  B and C are the same for
 // all rows of a group: the workgroup's tile of them lies in LDS as float32.
 //
-// What bounds it is the vector unit: a product for the exponent, the
-// exponential (its own rate a quarter), the drive, two passes of the
-// recurrence (one to join the lanes, one from the joined state) and the
-// read-out, about 6 operations and an exponential per mode and step.
+// What bounds it is the vector unit (its instructions issue in 84 to 96% of the
+// cycles): a product for the exponent, the exponential (its own rate a quarter),
+// the drive, two passes of the recurrence (one to join the lanes, one from the
+// joined state), the join and the read-out, about 7 operations and an exponential
+// per mode and step; the backward pass forms the states again, walks their
+// gradients the other way and sums two products over rows, about 19 and an
+// exponential.  Those 4 x 4096 rows in bf16 with a gate: forward 0.21 ms (0.27 GB of
+// tensors take 0.05), backward 0.60 + 0.07 ms to add the row blocks' dB and dC.
 #include <algorithm>
 #include <type_traits>
 
@@ -1181,9 +1188,21 @@ __global__ __launch_bounds__(256) void selective_step_kernel(Args p, int lpr) {
   }
 }
 
-// How rows go to workgroups.
+// How rows go to workgroups.  A workgroup has 16 rows of 8 steps to a lane; rows of
+// at most 64 steps fill 4 to a lane, and it has 32 of them.
+//
+// 128 workgroups and fewer leave half the device idle: a row's tiles are cut into
+// segments, up to 512 workgroups, whose ends a first pass forms and a small kernel
+// joins.  That is half the work again and two launches more, so it needs a row
+// long enough.  Measured, whole rows against segments, 16 modes, bf16, in us
+// (H channels x L steps):
+//   forward   1024 x 512 18 / 22, 1024 x 1024 32 / 24, 2048 x 1024 33 / 34, 2048 x 2048 62 / 52
+//   backward  1024 x 256 52 / 55, 1024 x 512  71 / 53, 2048 x 512  91 / 82, 2048 x 2048 225 / 152
+// At 192 workgroups (3 x 1024 rows of 4096 steps) whole rows win, 119 / 159 and 405 /
+// 417; half as many segments lose (2048 x 4096: 117 and 411 whole, 89 and 244 in 512
+// workgroups), 1024 workgroups gain no more.
 struct Plan {
-  int st;         // steps of a lane: 8, or 4 where rows have at most 64 steps
+  int st;         // steps of a lane
   int rw;         // groups of four rows
   int nrb;        // row blocks of a group of channels
   int nseg, seg_tiles;
@@ -1196,7 +1215,8 @@ Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
   if (p.st == 8) p.rw = 4;
   p.nrb = (hg + 4 * p.rw - 1) / (4 * p.rw);
   const long have = std::max(1L, (long)B * G * p.nrb);
-  const long want = have >= 256 ? 1 : std::min<long>(ntile, 512 / have);
+  const bool split = have <= 128 && ntile >= (backward ? 4 : 8);
+  const long want = split ? std::min<long>(ntile, 512 / have) : 1;
   p.seg_tiles = (int)((ntile + want - 1) / want);
   p.nseg = (ntile + p.seg_tiles - 1) / p.seg_tiles;
   return p;

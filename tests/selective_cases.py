@@ -8,8 +8,8 @@ c counts roundings (each 2^-24):
   3, the exponent of a decay carries the step size's 16 and two more (times the
   exponent, which costs more than it weighs past 2: 36), the lane's steps in
   two passes 32, the lanes' joins 10, the gate 30, the skip 2, the read-out's N
-  modes N + 4: below 134 + N; 12 for every tile of 256 steps the state is
-  carried over;
+  modes N + 4: below 134 + N; 6 for every tile of 128 steps the state is
+  carried over (its entry, four joins, the decay's product);
 * selective backward: its products take two such sums, and the sums over a
   group's rows and a lane's steps 32 + H / 32 more;
 * short convolution: K products, the gate 20: 2 (K + 20) covers both passes;

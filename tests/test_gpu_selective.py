@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 # (B, H, N, G, L, type, what): lengths around the borders of a lane, a short tile and a tile;
 # modes around a stage's eight; channels around a wave's four and a workgroup's rows; few rows,
-# whose modes are shared by four waves and whose steps are cut into segments; many rows
+# whose steps are cut into segments; many rows
 SHAPES = [
     (2, 3, 1, 1, 1, "f32", "gsb"), (3, 4, 4, 2, 2, "bf16", "gsbr"), (2, 5, 3, 1, 3, "f16", "sb"),
     (3, 6, 16, 3, 4, "f32", "gr"), (2, 33, 8, 1, 5, "bf16", "gsbj"), (4, 7, 9, 1, 15, "f32", "sbr"),
