@@ -31,6 +31,10 @@ SHAPES = [
     (2, 2049, 15, "f32", "int8", "pg"), (1, 4096, 70, "bf16", "e4m3", "ar"), (2, 4099, 18, "f16", "int8", "pgr"),
     (1, 8192, 35, "bf16", "int8", "pgl"), (1, 8191, 9, "f32", "e4m3", "n"), (40, 96, 2, "bf16", "int8", "a"),
     (3, 100, 5000, "bf16", "e4m3", "ar"),
+    (2, 63, 34, "bf16", "int8", "pgl"), (3, 64, 21, "f32", "e4m3", "pgr"), (2, 65, 48, "f16", "int8", "al"),
+    (2, 127, 33, "bf16", "e4m3", "nl"), (3, 128, 31, "f16", "int8", "pgj"), (2, 129, 64, "f32", "int8", "ar"),
+    (2, 1023, 20, "f32", "int8", "pgl"), (2, 1025, 37, "f32", "e4m3", "al"), (1, 2047, 50, "bf16", "int8", "pgl"),
+    (2, 2048, 17, "f32", "int8", "pgr"),
     (1, 1, 1, "f32", "int8", "a"), (5, 7, 1, "bf16", "e4m3", "pgr"), (9, 512, 1, "f16", "int8", "pgl"),
     (6, 513, 1, "f32", "e4m3", "ar"), (3, 2048, 1, "bf16", "int8", "n"), (4, 2055, 1, "bf16", "int8", "pgrj"),
     (64, 4096, 1, "bf16", "int8", "a"), (2, 8192, 1, "f32", "e4m3", "pgl"),
