@@ -9,7 +9,9 @@
 // max |d w|, q = d w M / m and s = m rstd / M: the factor of the norm meets only
 // the scale.
 //
-// Memory bounds it: o's inputs read once, o written, a byte a channel written.
+// Memory bounds it: o's inputs read once, o written, a byte a channel written (2^25
+// bf16 elements in rows of 64 to 1024 channels: x + y 45 us, 5.2 TB/s; with the norm
+// and gate of y 74 to 80, its vector work only partly behind the loads: 4 TB/s).
 // A workgroup takes a strip of LT VE steps with all its channels, o held in
 // registers as stored; four neighbouring channels to a lane, so that their bytes
 // of a step make one word, turned to rows of channels through LDS.

@@ -11,7 +11,8 @@
 // de's first K - 1 being the gradient of the state before the row.
 //
 // Memory bounds it: an input read and an output written forward, two and one
-// backward.  A lane holds 8 consecutive steps and asks for the 8 before them
+// backward (rows of 8191 steps, 4 x 1024 of them, 7 taps, float32: 56 us forward, 4.8
+// TB/s, 96 backward, 4.2).  A lane holds 8 consecutive steps and asks for the 8 before them
 // too, which its neighbour has just brought into the cache.
 #include <algorithm>
 
@@ -97,7 +98,7 @@ __device__ __forceinline__ void place_row(unsigned row, int H, int* b, int* h) {
 // A row takes lpr lanes (a power of two, at most the workgroup's 256) and, if
 // it has more than 8 lpr steps, several workgroups.  WAVE: 64 lanes at least, so
 // that a wave's row, weights and end are scalars (4 taps, 2^25 bf16 elements in
-// rows of 2048: 38 us with a 64-bit division per lane, 31 so).
+// rows of 2048: 38 us with a 64-bit division per lane, 34 so).
 template <typename T, int K, bool WAVE>
 __global__ __launch_bounds__(256) void shortconv_fwd_kernel(Args p) {
   const unsigned rb = blockIdx.x / (unsigned)p.ntile;
@@ -319,7 +320,8 @@ struct BwdPlan {
 };
 
 // Rows that are too few to fill the device's wave slots are cut into segments
-// of whole tiles.
+// of whole tiles (256 rows of 65536 steps, float32: 30 us, whole 149; 1024 of
+// 16384: 29 and 45; from 8192 rows on they stay whole).
 BwdPlan bwd_plan(long rows, int L) {
   BwdPlan pl;
   const int chunks = (L + 7) / 8;
