@@ -606,7 +606,8 @@ typedef struct {
  *   K - 1 up to the last live step (with fewer live steps, x0's last are kept
  *   ahead of them); it may be x0.
  * silu is 0 at the type's lowest value, NaN at -infinity.  Requires B H <= 2^24
- * and the limits of the gated recurrence. */
+ * and the limits of the gated recurrence; a sequence needs a lane per 8 steps, of
+ * which a launch has fewer than 2^32. */
 int dssm_shortconv_forward(const void* u, long long stride_b, const float* w, const float* bias,
                            const dssm_shortconv_shape* s, const int* lens, const float* x0,
                            float* x_end, void* y, void* stream);
@@ -671,7 +672,9 @@ typedef struct {
 
 /* Bytes of workspace of dssm_selective_forward or (backward != 0)
  * dssm_selective_backward (host only).  Requires H <= 65535, B H <= 2^24, L <=
- * 2^24, B H L <= 2^40, B H N ceil(L / 128) <= 2^36, B G N ceil(L / 1024) <= 2^29. */
+ * 2^24, B H L <= 2^40, B H N ceil(L / 128) <= 2^36, B G N ceil(L / 1024) <= 2^29;
+ * the calls over sequences B G ceil(H / (16 G)) < 2^23 (16 channels of a group, or one,
+ * to 512 lanes; 32 where L <= 64). */
 int dssm_selective_workspace_size(const dssm_selective_shape* s, int backward, size_t* bytes);
 
 /* Bytes of a checkpoint: the states [B, H, ceil(L / 128), N] float32 entering

@@ -92,4 +92,11 @@ inline int check_space(const void* ws, size_t have, size_t need) {
   return need ? check_buffer(ws, "workspace") : DSSM_OK;
 }
 
+// A launch that the launcher refuses to make: its grid has too many lanes.
+inline int launch_check(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(DSSM_ERR_UNSUPPORTED, "%s: a grid of 2^32 lanes or more", what);
+  return hip_check(e, what);
+}
+
 }  // namespace dssm

@@ -76,9 +76,9 @@ int shortconv_run(bool step, const void* u, long long stride_b, const float* w, 
   c.xT = x_end;
   c.y = y;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if ((rc = hip_check(step ? launch_shortconv_step(c, s->dtype, st)
-                           : launch_shortconv_forward(c, s->dtype, st),
-                      "shortconv launch")))
+  if ((rc = launch_check(step ? launch_shortconv_step(c, s->dtype, st)
+                              : launch_shortconv_forward(c, s->dtype, st),
+                         "shortconv launch")))
     return rc;
   return ok();
 }
@@ -219,8 +219,8 @@ int dssm_shortconv_backward(const void* u, long long stride_b, const float* w, c
   c.dbias = g->dbias;
   c.dx0 = g->dx0;
   c.ws = ws;
-  if ((rc = hip_check(launch_shortconv_backward(c, s->dtype, static_cast<hipStream_t>(stream)),
-                      "shortconv backward launch")))
+  if ((rc = launch_check(launch_shortconv_backward(c, s->dtype, static_cast<hipStream_t>(stream)),
+                         "shortconv backward launch")))
     return rc;
   return ok();
 }
@@ -268,8 +268,8 @@ int dssm_selective_forward(const dssm_selective_inputs* in, const dssm_selective
   c.y = y;
   c.ckpt = ckpt;
   c.ws = ws;
-  if ((rc = hip_check(launch_selective_forward(c, s->dtype, static_cast<hipStream_t>(stream)),
-                      "selective forward launch")))
+  if ((rc = launch_check(launch_selective_forward(c, s->dtype, static_cast<hipStream_t>(stream)),
+                         "selective forward launch")))
     return rc;
   return ok();
 }
@@ -288,8 +288,8 @@ int dssm_selective_step(const dssm_selective_inputs* in, const dssm_selective_sh
   c.x0 = x0;
   c.xT = x_end;
   c.y = y;
-  if ((rc = hip_check(launch_selective_step(c, s->dtype, static_cast<hipStream_t>(stream)),
-                      "selective step launch")))
+  if ((rc = launch_check(launch_selective_step(c, s->dtype, static_cast<hipStream_t>(stream)),
+                         "selective step launch")))
     return rc;
   return ok();
 }
@@ -358,8 +358,8 @@ int dssm_selective_backward(const dssm_selective_inputs* in, const dssm_selectiv
   c.ddt_bias = g->ddt_bias;
   c.dx0 = g->dx0;
   c.ws = ws;
-  if ((rc = hip_check(launch_selective_backward(c, s->dtype, static_cast<hipStream_t>(stream)),
-                      "selective backward launch")))
+  if ((rc = launch_check(launch_selective_backward(c, s->dtype, static_cast<hipStream_t>(stream)),
+                         "selective backward launch")))
     return rc;
   return ok();
 }

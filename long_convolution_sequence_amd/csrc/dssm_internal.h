@@ -16,6 +16,9 @@ int fail(int code, const char* fmt, ...);
 int ok();
 int hip_check(hipError_t e, const char* what);
 
+// A launch counts its lanes in 32 bits.
+inline bool launchable(long blocks, int lanes) { return blocks <= 0xffffffffL / lanes; }
+
 // Optional pair of caller-owned events that the GPU stamps at the start and
 // the end of one kernel (hipExtLaunchKernel): timing of that kernel alone,
 // without the dispatch gap before it.

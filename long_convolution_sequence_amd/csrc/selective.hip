@@ -29,8 +29,9 @@
 // per mode and step; the backward pass forms the states again, walks their
 // gradients the other way and sums two products over rows, about 19 and an
 // exponential; and what is done once a step (inputs, gates, turns through LDS) takes
-// a third of the time at 16 modes.  Those 4 x 4096 rows in bf16 with a gate: forward 0.21 ms (0.27 GB of
-// tensors take 0.05), backward 0.60 + 0.07 ms to add the row blocks' dB and dC.
+// a third of the time at 16 modes.  Those 4 x 4096 rows in bf16 with a gate: forward
+// 0.21 ms (0.27 GB of tensors take 0.05), backward 0.60 + 0.07 ms to add the row
+// blocks' dB and dC.
 #include <algorithm>
 #include <type_traits>
 
@@ -1077,35 +1078,39 @@ void selective_bwd_kernel(Args p) {
     }
 }
 
-// dB and dC: the row blocks' parts in order; 4 steps to a thread.
+// dB and dC: the row blocks' parts in order; 4 steps to a thread, workgroups taking
+// turns where there are more than 2^23 of 1024 steps.
 template <typename T>
 __global__ __launch_bounds__(256) void selective_dbc_kernel(Args p) {
-  const int per = (p.L + 1023) / 1024;  // workgroups of a row of steps
-  const unsigned k = blockIdx.x / (unsigned)per;  // ((b G + g) 2 + which) N + n
-  const int t = ((int)(blockIdx.x - k * per) * 256 + (int)threadIdx.x) * 4;
-  if (t >= p.L) return;
-  const unsigned n = k % (unsigned)p.N, bg2 = k / (unsigned)p.N;
-  const int which = bg2 & 1;
-  const unsigned bg = bg2 >> 1;
-  const int b = bg / (unsigned)p.G, g = bg - b * p.G;
-  const int Lp = p.nchunk * kKeep, len = row_len(p, b);
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (t < len) {
-    const size_t step = (size_t)p.B * p.G * 2 * p.N * Lp;
-    const float* v = p.part_bc + (size_t)k * Lp + t;
-    for (int i = 0; i < p.nrb; ++i) {
-      const float4 f = *reinterpret_cast<const float4*>(v + i * step);
-      s[0] += f.x;
-      s[1] += f.y;
-      s[2] += f.z;
-      s[3] += f.w;
-    }
+  const unsigned per = (p.L + 1023u) / 1024;  // parts of a row of steps
+  const unsigned count = (unsigned)p.B * p.G * 2 * p.N * per;
+  for (unsigned w = blockIdx.x; w < count; w += gridDim.x) {
+    const unsigned k = w / per;  // ((b G + g) 2 + which) N + n
+    const int t = ((int)(w - k * per) * 256 + (int)threadIdx.x) * 4;
+    if (t >= p.L) continue;
+    const unsigned n = k % (unsigned)p.N, bg2 = k / (unsigned)p.N;
+    const int which = bg2 & 1;
+    const unsigned bg = bg2 >> 1;
+    const int b = bg / (unsigned)p.G, g = bg - b * p.G;
+    const int Lp = p.nchunk * kKeep, len = row_len(p, b);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t < len) {
+      const size_t step = (size_t)p.B * p.G * 2 * p.N * Lp;
+      const float* v = p.part_bc + (size_t)k * Lp + t;
+      for (int i = 0; i < p.nrb; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(v + i * step);
+        s[0] += f.x;
+        s[1] += f.y;
+        s[2] += f.z;
+        s[3] += f.w;
+      }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = t + j < len ? s[j] : 0.f;
+      for (int j = 0; j < 4; ++j) s[j] = t + j < len ? s[j] : 0.f;
+    }
+    T* to = static_cast<T*>(which ? p.dC : p.dB) + (size_t)(b * (which ? p.sdC : p.sdB)) +
+            ((size_t)g * p.N + n) * p.L + t;
+    store_n<T, 4>(to, p.L - t, s);
   }
-  T* to = static_cast<T*>(which ? p.dC : p.dB) + (size_t)(b * (which ? p.sdC : p.sdB)) +
-          ((size_t)g * p.N + n) * p.L + t;
-  store_n<T, 4>(to, p.L - t, s);
 }
 
 // The parameters' gradients: sums over the batch and segments in a fixed order,
@@ -1312,7 +1317,9 @@ unsigned join_blocks(const Args& a) { return (unsigned)a.B * a.H * ((a.N + 15) /
 
 template <typename T, int ST, int RW, int NW>
 hipError_t forward(const Args& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.B * a.G * a.nrb * a.nseg), block(64 * RW * NW);
+  const long blocks = (long)a.B * a.G * a.nrb * a.nseg;
+  if (!launchable(blocks, 64 * RW * NW)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks), block(64 * RW * NW);
   const size_t lds = (size_t)padded(a.N) * (2 * 4 * RW + 2) * sizeof(float);
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
@@ -1333,7 +1340,9 @@ hipError_t run_forward(const SelectiveCall& c, hipStream_t st) {
 
 template <typename T, int ST, int RW, int NW>
 hipError_t backward(const Args& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.B * a.G * a.nrb * a.nseg), block(64 * RW * NW);
+  const long blocks = (long)a.B * a.G * a.nrb * a.nseg;
+  if (!launchable(blocks, 64 * RW * NW)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks), block(64 * RW * NW);
   const size_t lds = (size_t)padded(a.N) * (3 * 4 * RW + 4) * sizeof(float);
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, dim3(64 * RW),
@@ -1347,7 +1356,8 @@ hipError_t backward(const Args& a, hipStream_t st) {
     hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, false>), grid, block, lds, st, a);
   if (a.L > 0)
     hipLaunchKernelGGL((selective_dbc_kernel<T>),
-                       dim3((unsigned)a.B * a.G * 2 * a.N * (unsigned)((a.L + 1023) / 1024)),
+                       dim3(std::min((unsigned)a.B * a.G * 2 * a.N * ((a.L + 1023u) / 1024),
+                                     1u << 23)),
                        dim3(256), 0, st, a);
   return hipGetLastError();
 }

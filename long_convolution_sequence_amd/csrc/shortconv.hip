@@ -371,6 +371,7 @@ hipError_t run(const ShortconvCall& c, Pass pass, hipStream_t st) {
     a.lpr = pow2_from(chunks, 256);
     a.ntile = (chunks + a.lpr - 1) / a.lpr;
     const long per = 256 / a.lpr, blocks = (a.rows + per - 1) / per * a.ntile;
+    if (!launchable(blocks, 256)) return hipErrorInvalidConfiguration;
     if (a.lpr >= 64)
       hipLaunchKernelGGL((shortconv_fwd_kernel<T, K, true>), dim3((unsigned)blocks), dim3(256), 0,
                          st, a);
@@ -386,6 +387,7 @@ hipError_t run(const ShortconvCall& c, Pass pass, hipStream_t st) {
     if (a.rows > 0) {
       const long per = pl.ntile > 1 ? 4 : 4 * (64 / pl.lpr);
       const long blocks = (a.rows * pl.nseg + per - 1) / per;
+      if (!launchable(blocks, 256)) return hipErrorInvalidConfiguration;
       if (pl.ntile > 1)
         hipLaunchKernelGGL((shortconv_bwd_kernel<T, K, true>), dim3((unsigned)blocks), dim3(256), 0,
                            st, a);

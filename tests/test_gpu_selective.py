@@ -380,6 +380,23 @@ def test_gradients_against_differences():
         assert abs(num - ana) <= 1e-3 * scale + 1e-2, name
 
 
+def test_more_gradient_parts_than_workgroups():
+    """A group per channel and many modes: dB and dC by workgroups that take turns.  One step
+    from no state has dB = C dy dt u and dC = B dy dt u: the step size's rounding (2e-7, its
+    polynomial's among it) and four products'."""
+    torch = torch_()
+    B, H, N = 2, 16400, 128
+    gen = torch.Generator("cuda").manual_seed(3)
+    u, delta, dy = [torch.randn(B, H, 1, device="cuda", generator=gen) for _ in range(3)]
+    Bm, Cm = [torch.randn(B, H, N, 1, device="cuda", generator=gen) for _ in range(2)]
+    log_re = torch.rand(H, N, device="cuda", generator=gen)
+    y, ckpt = bd.selective_forward_ckpt(u, delta, Bm, Cm, log_re)
+    g = bd.selective_backward(dy, ckpt, u, delta, Bm, Cm, log_re)
+    drive = (dy.double() * torch.nn.functional.softplus(delta.double()) * u.double())[:, :, None]
+    for got, ref in ((g["dB"], Cm.double() * drive), (g["dC"], Bm.double() * drive)):
+        assert ((got.double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all()
+
+
 def test_binding_refuses():
     torch = torch_()
     s = prepared(2, 4, 3, 2, 64, "bf16", "gsb", seed=61)

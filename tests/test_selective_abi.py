@@ -226,6 +226,26 @@ def test_selective_backward_refuses():
     assert call(s=sshape(H=0, G=1), inp=sinputs(u=None)) == 0
 
 
+def test_launches_of_2_to_the_32_lanes():
+    """Calls within the other limits that one launch cannot hold are refused before any."""
+    L = bd.lib()
+    rows = ctypes.byref(cshape(B=1 << 7, H=1 << 10, L=1 << 18))  # 2^35 steps, 8 to a lane
+    assert L.dssm_shortconv_forward(at(0), 1 << 28, at(1), at(2), rows, None, None, None, at(5),
+                                    None) == UNS
+    assert b"2^32 lanes" in L.dssm_last_error()
+    # a channel to a group: a workgroup of 512 lanes to each of 2^23 rows
+    for length in (1, 65):
+        s = sshape(B=1 << 12, H=1 << 11, G=1 << 11, N=1, L=length)
+        t = length << 11
+        inp = sinputs(stride_u=t, stride_delta=t, stride_z=t, stride_B=t, stride_C=t)
+        assert L.dssm_selective_forward(ctypes.byref(inp), ctypes.byref(s), None, None, at(12),
+                                        None, at(14), 1 << 40, None) == UNS
+        g = sgrads(stride_u=t, stride_delta=t, stride_z=t, stride_B=t, stride_C=t)
+        assert L.dssm_selective_backward(ctypes.byref(inp), ctypes.byref(s), at(13), at(15), None,
+                                         ctypes.byref(g), at(14), 1 << 50, None) == UNS
+        assert b"2^32 lanes" in L.dssm_last_error()
+
+
 def test_resnorm8_refuses():
     L = bd.lib()
 
