@@ -162,6 +162,16 @@ __device__ __forceinline__ float square_of(float log_re) {
   return s > 0x1p126f ? 0x1p126f : s;
 }
 
+// A sum of step sizes, finite unless NaN: resets (steps of 2^127, say) side by side pass
+// float32, and a mode with log_re 0 decays by no step however long.
+__device__ __forceinline__ float finite_sum(float s) {
+  return s > 0x1.fffffep127f ? 0x1.fffffep127f : s;
+}
+
+// What stands for log_re^2 in the modes and rows that only fill a workgroup: their
+// states are 0 whatever the step, and at 0 a step past float32 would make NaN.
+constexpr float kFill = 1.f;
+
 __device__ __forceinline__ int row_len(const Args& p, int b) {
   if (!p.lens) return p.L;
   return min(max(p.lens[b], 0), p.L);
@@ -381,7 +391,7 @@ void selective_fwd_kernel(Args p) {
   const size_t row0 = (size_t)at.b * p.H + h0;  // the workgroup's first row
   // the waves of a row group take turns with its modes
   for (int n = (lane & 15) * NW + nw; n < NP; n += 16 * NW) {
-    float c = 0.f, s = 0.f;
+    float c = 0.f, s = kFill;
     if (r < nrow && n < p.N) {
       s = square_of(p.log_re[(size_t)(h0 + r) * p.N + n]) * kLog2e;
       if (!AGG && p.nseg > 1)
@@ -487,7 +497,8 @@ void selective_fwd_kernel(Args p) {
         }
 #pragma unroll
         for (int j = 0; j < ST; ++j) S += dt[j];
-        if (AGG) Sseg += S;
+        S = finite_sum(S);
+        if (AGG) Sseg = finite_sum(Sseg + S);
       }
       const int n0 = blk * kModes, nm = p.N - n0;
       // two modes at a time: the passes are chains, and two fill each other's
@@ -564,7 +575,7 @@ void selective_fwd_kernel(Args p) {
     }
   }
   if (AGG) {
-    const float s = row_total(Sseg);
+    const float s = finite_sum(row_total(Sseg));
     if (r < nrow && seg == 0 && nw == 0) p.aggS[(row0 + r) * p.nseg + at.seg] = s;
   } else {
     // behind the rows' end: outputs are 0, the states stay
@@ -612,7 +623,7 @@ __global__ __launch_bounds__(256) void selective_join_kernel(float* agg, const f
     const int i = segment(j);
     const float d = j + 1 < nseg ? s[i] : 0.f, e = j + 1 < nseg ? v[(size_t)i * N] : 0.f;
     V = fmaf(decay(d), V, e);
-    S += d;
+    S = finite_sum(S + d);
   }
   ends[part][m] = make_float2(S, V);
   __syncthreads();
@@ -679,7 +690,7 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
       kap[n * RP + q] =
           q < nrow
               ? square_of(p.log_re[(size_t)(row0 - (size_t)at.b * p.H + q) * p.N + n]) * kLog2e
-              : 0.f;
+              : kFill;
       car[n * RP + q] = 0.f;
     }
   }
@@ -713,7 +724,8 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
       gy[j] = j < nv && live ? g : 0.f;
       S += dt[j];
     }
-    Sseg += S;
+    S = finite_sum(S);
+    Sseg = finite_sum(Sseg + S);
     for (int blk = 0; blk < nblk; ++blk) {
       stage.put(bc[buf]);
       __syncthreads();
@@ -738,7 +750,7 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
       buf ^= 1;
     }
   }
-  const float s = row_total(Sseg);
+  const float s = finite_sum(row_total(Sseg));
   if (live && seg == 0) p.aggS[(row0 + r) * p.nseg + at.seg] = s;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -780,7 +792,7 @@ void selective_bwd_kernel(Args p) {
   const int h0 = at.g * p.HG + at.rb * R, nrow = min(R, p.HG - at.rb * R);
   const size_t row0 = (size_t)at.b * p.H + h0;
   for (int n = (lane & 15) * NW + nw; n < NP; n += 16 * NW) {
-    float c = 0.f, s = 0.f;
+    float c = 0.f, s = kFill;
     if (r < nrow && n < p.N) {
       s = square_of(p.log_re[(size_t)(h0 + r) * p.N + n]) * kLog2e;
       if (p.nseg > 1)
@@ -866,7 +878,7 @@ void selective_bwd_kernel(Args p) {
       if (!whole || nrow < R) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          own[0][j] = j < nv ? own[0][j] : 0.f;
+          own[0][j] = j < nv && live ? own[0][j] : 0.f;
           own[1][j] = j < nv && live ? own[1][j] : 0.f;
           own[2][j] = j < nv && live ? own[2][j] : 0.f;
         }
@@ -904,6 +916,7 @@ void selective_bwd_kernel(Args p) {
         }
 #pragma unroll
         for (int j = 0; j < ST; ++j) S += dt[j];
+        S = finite_sum(S);
       }
       const int n0 = blk * kModes, nm = p.N - n0;
       // one mode to each of a row group's waves; modes past the last one are zeros
@@ -1128,10 +1141,13 @@ __global__ __launch_bounds__(256) void selective_param_kernel(Args p) {
   }
   for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o);
   if (sub) return;
-  if (n < p.N)  // nothing to add up is 0, whatever the parameter
+  if (n < p.N) {
+    // nothing to add up is 0, whatever the parameter; so is what a parameter of 0
+    // multiplies, whose sum w dt resets may take past float32
+    const float lr = p.log_re[(size_t)h * p.N + n];
     p.dlog_re[(size_t)h * p.N + n] =
-        (float)(s != 0.0 ? -2.0 * (double)p.log_re[(size_t)h * p.N + n] * s : 0.0);
-  else if (n == p.N && p.dD)
+        (float)(s != 0.0 && lr != 0.f ? -2.0 * (double)lr * s : 0.0);
+  } else if (n == p.N && p.dD)
     p.dD[h] = (float)s;
   else if (n == p.N + 1 && p.ddt_bias)
     p.ddt_bias[h] = (float)s;
