@@ -59,8 +59,9 @@ struct Args {
   void* y;
   float* bounds;          // [rows][chunks][N] state entering each chunk
   int nchunk;
-  // a row's tiles in nseg segments of seg_tiles
+  // a row's (backward: a slab's) tiles in nseg segments of seg_tiles
   int nrb, nseg, seg_tiles;
+  int pair0;              // the launch's first pair of batch row and group
   float* agg;             // [rows][nseg][N]: ends of the segments, then what enters them
   float* aggS;            // [rows][nseg]: sum of dt
   // backward
@@ -69,9 +70,12 @@ struct Args {
   void *du, *ddelta, *dz, *dB, *dC;
   long long sdu, sdd, sdz, sdB, sdC;
   float *dlog_re, *dD, *ddt_bias, *dx0;
-  float* part_bc;         // [nrb][B][G][2][N][nchunk kKeep]
-  float* part_n;          // [rows][nseg][N]
-  float* part_h;          // [rows][nseg][2]
+  int npair, tile0, tile1;  // the launch's pairs; the slab's tiles
+  int steps;              // of a row of part_bc
+  int nparts, part0;      // parts of a row in all; before this slab
+  float* part_bc;         // [nrb][npair][2][N][steps]
+  float* part_n;          // [rows][nparts][N]
+  float* part_h;          // [rows][nparts][2]
 };
 
 // Inclusive scan over a row's 16 lanes, in time order or (REV) against it, of
@@ -221,7 +225,7 @@ struct Place {
     seg = (int)(k % (unsigned)p.nseg);
     k /= (unsigned)p.nseg;
     rb = (int)(k % (unsigned)p.nrb);
-    k /= (unsigned)p.nrb;
+    k = k / (unsigned)p.nrb + (unsigned)p.pair0;
     g = (int)(k % (unsigned)p.G);
     b = (int)(k / (unsigned)p.G);
   }
@@ -678,8 +682,7 @@ __global__ __launch_bounds__(64 * RW) void selective_bwd_agg_kernel(Args p) {
   const bool live = at.rb * R + r < p.HG, last = seg == kSeg - 1;
   const int h = at.g * p.HG + min(at.rb * R + r, p.HG - 1);
   const int len = row_len(p, at.b);
-  const int ntile = (p.L + TILE - 1) / TILE;
-  const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  const int t_lo = p.tile0 + at.seg * p.seg_tiles, t_hi = min(p.tile1, t_lo + p.seg_tiles);
   const int t_live = min(t_hi, (len + TILE - 1) / TILE);
   const size_t row0 = (size_t)at.b * p.H + at.g * p.HG + at.rb * R;
   const int nrow = min(R, p.HG - at.rb * R);
@@ -786,8 +789,7 @@ void selective_bwd_kernel(Args p) {
   const Work w_;
   const int seg = w_.seg, rg = w_.rg, nw = w_.nw, r = w_.r, lane = w_.lane;
   const int len = row_len(p, at.b);
-  const int ntile = (p.L + TILE - 1) / TILE;
-  const int t_lo = at.seg * p.seg_tiles, t_hi = min(ntile, t_lo + p.seg_tiles);
+  const int t_lo = p.tile0 + at.seg * p.seg_tiles, t_hi = min(p.tile1, t_lo + p.seg_tiles);
   const int t_live = min(t_hi, (len + TILE - 1) / TILE);
   const int h0 = at.g * p.HG + at.rb * R, nrow = min(R, p.HG - at.rb * R);
   const size_t row0 = (size_t)at.b * p.H + h0;
@@ -826,9 +828,9 @@ void selective_bwd_kernel(Args p) {
   const int nblk = (p.N + kModes - 1) / kModes;
   const uint32_t mine =
       ((uint32_t)min(w_.own, nrow - 1) * (uint32_t)p.L + w_.step) * (uint32_t)sizeof(T);
-  const int Lp = p.nchunk * kKeep;
-  float* part = p.part_bc +
-                (((size_t)at.rb * p.B + at.b) * p.G + at.g) * 2 * p.N * (size_t)Lp;
+  const int first = p.tile0 * TILE;
+  float* part = p.part_bc + ((size_t)at.rb * p.npair + (at.b * p.G + at.g - p.pair0)) * 2 * p.N *
+                                (size_t)p.steps;
   // where the lane's own steps, and those it walks, lie among a tile's rows
   const int own_at = w_.own * TILE + slot<ST>(w_.step / ST, w_.step % ST / 4), walk_at = r * TILE;
   const uint32_t keep_at = ((uint32_t)r * p.nchunk * p.N + seg * NW + nw) * 4u;
@@ -999,8 +1001,8 @@ void selective_bwd_kernel(Args p) {
         Part sum = slab[0][m][which][e];
 #pragma unroll
         for (int o = 1; o < RW; ++o) sum += slab[o][m][which][e];
-        *reinterpret_cast<Part*>(part + (size_t)(which * p.N + n0 + m) * Lp + t0 + (e & 15) * ST +
-                                 (e >> 4) * Q) = sum;
+        *reinterpret_cast<Part*>(part + (size_t)(which * p.N + n0 + m) * p.steps + (t0 - first) +
+                                 (e & 15) * ST + (e >> 4) * Q) = sum;
       }
     }
     // the inputs again, from a cache: held through the modes they would not fit the registers
@@ -1080,50 +1082,47 @@ void selective_bwd_kernel(Args p) {
     sumb = rows_sum(sumb);
   }
   if (live && w_.step == 0) {
-    float* put = p.part_h + ((row0 + w_.own) * p.nseg + at.seg) * 2;
+    float* put = p.part_h + ((row0 + w_.own) * p.nparts + p.part0 + at.seg) * 2;
     put[0] = sumD;
     put[1] = sumb;
   }
   if (r < nrow)
     for (int n = (lane & 15) * NW + nw; n < p.N; n += 16 * NW) {
-      p.part_n[((row0 + r) * p.nseg + at.seg) * p.N + n] = dre.row(r)[n];
+      p.part_n[((row0 + r) * p.nparts + p.part0 + at.seg) * p.N + n] = dre.row(r)[n];
       if (p.dx0 && at.seg == 0) p.dx0[(row0 + r) * p.N + n] = car.row(r)[n];
     }
 }
 
-// dB and dC: the row blocks' parts in order; 4 steps to a thread, workgroups taking
-// turns where there are more than 2^23 of 1024 steps.
-template <typename T>
+// dB and dC of a slab: the row blocks' parts in order; 4 steps to a thread.
+template <typename T, int TILE>
 __global__ __launch_bounds__(256) void selective_dbc_kernel(Args p) {
-  const unsigned per = (p.L + 1023u) / 1024;  // parts of a row of steps
-  const unsigned count = (unsigned)p.B * p.G * 2 * p.N * per;
-  for (unsigned w = blockIdx.x; w < count; w += gridDim.x) {
-    const unsigned k = w / per;  // ((b G + g) 2 + which) N + n
-    const int t = ((int)(w - k * per) * 256 + (int)threadIdx.x) * 4;
-    if (t >= p.L) continue;
-    const unsigned n = k % (unsigned)p.N, bg2 = k / (unsigned)p.N;
-    const int which = bg2 & 1;
-    const unsigned bg = bg2 >> 1;
-    const int b = bg / (unsigned)p.G, g = bg - b * p.G;
-    const int Lp = p.nchunk * kKeep, len = row_len(p, b);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (t < len) {
-      const size_t step = (size_t)p.B * p.G * 2 * p.N * Lp;
-      const float* v = p.part_bc + (size_t)k * Lp + t;
-      for (int i = 0; i < p.nrb; ++i) {
-        const float4 f = *reinterpret_cast<const float4*>(v + i * step);
-        s[0] += f.x;
-        s[1] += f.y;
-        s[2] += f.z;
-        s[3] += f.w;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = t + j < len ? s[j] : 0.f;
+  const int first = p.tile0 * TILE, end = min(p.L, p.tile1 * TILE);
+  const unsigned per = (end - first + 1023u) / 1024;  // parts of a row of steps
+  const unsigned k = blockIdx.x / per;                // (pair 2 + which) N + n
+  const int t = first + ((int)(blockIdx.x - k * per) * 256 + (int)threadIdx.x) * 4;
+  if (t >= end) return;
+  const unsigned n = k % (unsigned)p.N, half = k / (unsigned)p.N;
+  const int which = half & 1;
+  const unsigned bg = (half >> 1) + (unsigned)p.pair0;
+  const int b = bg / (unsigned)p.G, g = bg - b * p.G;
+  const int len = row_len(p, b);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (t < len) {
+    const size_t block = (size_t)p.npair * 2 * p.N * p.steps;
+    const float* v = p.part_bc + (size_t)k * p.steps + (t - first);
+    for (int i = 0; i < p.nrb; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(v + i * block);
+      s[0] += f.x;
+      s[1] += f.y;
+      s[2] += f.z;
+      s[3] += f.w;
     }
-    T* to = static_cast<T*>(which ? p.dC : p.dB) + (size_t)(b * (which ? p.sdC : p.sdB)) +
-            ((size_t)g * p.N + n) * p.L + t;
-    store_n<T, 4>(to, p.L - t, s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = t + j < len ? s[j] : 0.f;
   }
+  T* to = static_cast<T*>(which ? p.dC : p.dB) + (size_t)(b * (which ? p.sdC : p.sdB)) +
+          ((size_t)g * p.N + n) * p.L + t;
+  store_n<T, 4>(to, p.L - t, s);
 }
 
 // The parameters' gradients: sums over the batch and segments in a fixed order,
@@ -1134,9 +1133,9 @@ __global__ __launch_bounds__(256) void selective_param_kernel(Args p) {
   if (k >= (long)p.H * (p.N + 2)) return;
   const int h = (int)(k / (p.N + 2)), n = (int)(k - (long)h * (p.N + 2));
   double s = 0.0;
-  const long count = (long)p.B * p.nseg;
+  const long count = (long)p.B * p.nparts;
   for (long i = sub; i < count; i += 16) {
-    const long b = i / p.nseg, at = (b * p.H + h) * p.nseg + (i - b * p.nseg);
+    const long b = i / p.nparts, at = (b * p.H + h) * p.nparts + (i - b * p.nparts);
     s += (double)(n < p.N ? p.part_n[at * p.N + n] : p.part_h[at * 2 + (n - p.N)]);
   }
   for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o);
@@ -1224,24 +1223,42 @@ __global__ __launch_bounds__(256) void selective_step_kernel(Args p, int lpr) {
 // At 192 workgroups (3 x 1024 rows of 4096 steps) whole rows win, 119 / 159 and 405 /
 // 417; half as many segments lose (2048 x 4096: 117 and 411 whole, 89 and 244 in 512
 // workgroups), 1024 workgroups gain no more.
+//
+// The backward pass leaves dB and dC of every row block in float32, B G ceil(H / (16 G))
+// 2 N L values: at 128 modes 32 times a tensor of 16 bits, were they all held at once.
+// A slab of tiles of all rows holds at most kPartFloats of them (one tile's of
+// some pairs of batch row and group, where all pairs' are more); the slabs go from the
+// last to the first, each from the state gradient that the one behind it leaves.
 struct Plan {
   int st;         // steps of a lane
   int rw;         // groups of four rows
   int nrb;        // row blocks of a group of channels
+  int nslab, slab_tiles, npair;
   int nseg, seg_tiles;
 };
+constexpr long kPartFloats = 1L << 28;
 
 Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
-  Plan p{8, 8, 1, 1, 1};
-  if (L <= 64) p.st = 4;
+  Plan p{};
+  p.st = L <= 64 ? 4 : 8;
+  p.rw = 8;
   const int tile = kSeg * p.st, ntile = std::max(1, (L + tile - 1) / tile), hg = H / G;
   if (p.st == 8) p.rw = 4;
   p.nrb = (hg + 4 * p.rw - 1) / (4 * p.rw);
-  const long have = std::max(1L, (long)B * G * p.nrb);
-  const bool split = have <= 128 && ntile >= (backward ? 4 : 8);
-  const long want = split ? std::min<long>(ntile, 512 / have) : 1;
-  p.seg_tiles = (int)((ntile + want - 1) / want);
-  p.nseg = (ntile + p.seg_tiles - 1) / p.seg_tiles;
+  const long pairs = std::max(1L, (long)B * G), have = pairs * p.nrb;
+  p.slab_tiles = ntile;
+  p.npair = (int)pairs;
+  if (backward) {
+    const long least = (long)p.nrb * 2 * N * kKeep;  // a pair's in one tile: 2^27 at most
+    const long most = std::min<long>(ntile, std::max(1L, kPartFloats / (pairs * least)));
+    p.slab_tiles = (int)((ntile + (ntile + most - 1) / most - 1) / ((ntile + most - 1) / most));
+    p.npair = (int)std::min(pairs, kPartFloats / least);
+  }
+  p.nslab = (ntile + p.slab_tiles - 1) / p.slab_tiles;
+  const bool split = have <= 128 && p.slab_tiles >= (backward ? 4 : 8);
+  const long want = split ? std::min<long>(p.slab_tiles, 512 / have) : 1;
+  p.seg_tiles = (int)((p.slab_tiles + want - 1) / want);
+  p.nseg = (p.slab_tiles + p.seg_tiles - 1) / p.seg_tiles;
   return p;
 }
 
@@ -1275,6 +1292,7 @@ Args make_args(const SelectiveCall& c, const Plan& pl) {
   a.nrb = pl.nrb;
   a.nseg = pl.nseg;
   a.seg_tiles = pl.seg_tiles;
+  a.nparts = pl.nslab * pl.nseg;
   a.dy = c.dy;
   a.dx = c.dx;
   a.du = c.du;
@@ -1296,7 +1314,7 @@ Args make_args(const SelectiveCall& c, const Plan& pl) {
 
 // The workspace's parts; the backward pass's after the split rows'.
 struct Layout {
-  size_t agg, aggS, bc, n, h, total;
+  size_t agg, aggS, carry, bc, n, h, total;
 };
 
 Layout layout_of(const Plan& pl, int B, int H, int G, int N, int L, bool backward) {
@@ -1311,9 +1329,11 @@ Layout layout_of(const Plan& pl, int B, int H, int G, int N, int L, bool backwar
   o.agg = take(pl.nseg > 1 ? rows * pl.nseg * N : 0);
   o.aggS = take(pl.nseg > 1 ? rows * pl.nseg : 0);
   if (backward) {
-    o.bc = take((size_t)pl.nrb * B * G * 2 * N * ((size_t)(L + kKeep - 1) / kKeep * kKeep));
-    o.n = take(rows * pl.nseg * N);
-    o.h = take(rows * pl.nseg * 2);
+    const size_t parts = (size_t)pl.nslab * pl.nseg;
+    o.carry = take(pl.nslab > 1 ? rows * N : 0);
+    o.bc = take(L ? (size_t)pl.nrb * pl.npair * 2 * N * pl.slab_tiles * kKeep : 0);
+    o.n = take(rows * parts * N);
+    o.h = take(rows * parts * 2);
   }
   o.total = at;
   return o;
@@ -1354,11 +1374,10 @@ hipError_t run_forward(const SelectiveCall& c, hipStream_t st) {
   return pl.st == 4 ? forward<T, 4, 8, 1>(a, st) : forward<T, 8, 4, 2>(a, st);
 }
 
+// A slab of the launch's pairs.
 template <typename T, int ST, int RW, int NW>
 hipError_t backward(const Args& a, hipStream_t st) {
-  const long blocks = (long)a.B * a.G * a.nrb * a.nseg;
-  if (!launchable(blocks, 64 * RW * NW)) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), block(64 * RW * NW);
+  const dim3 grid((unsigned)a.npair * a.nrb * a.nseg), block(64 * RW * NW);
   const size_t lds = (size_t)padded(a.N) * (3 * 4 * RW + 4) * sizeof(float);
   if (a.nseg > 1) {
     hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, dim3(64 * RW),
@@ -1370,22 +1389,37 @@ hipError_t backward(const Args& a, hipStream_t st) {
     hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
   else
     hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, false>), grid, block, lds, st, a);
-  if (a.L > 0)
-    hipLaunchKernelGGL((selective_dbc_kernel<T>),
-                       dim3(std::min((unsigned)a.B * a.G * 2 * a.N * ((a.L + 1023u) / 1024),
-                                     1u << 23)),
-                       dim3(256), 0, st, a);
+  const int steps = std::min(a.L, a.tile1 * kSeg * ST) - a.tile0 * kSeg * ST;
+  if (steps > 0)
+    hipLaunchKernelGGL((selective_dbc_kernel<T, kSeg * ST>),
+                       dim3((unsigned)a.npair * 2 * a.N * ((steps + 1023u) / 1024)), dim3(256), 0,
+                       st, a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t run_backward(const SelectiveCall& c, hipStream_t st) {
   const Plan pl = plan_of(c.B, c.H, c.G, c.N, c.L, true);
+  const Layout o = layout_of(pl, c.B, c.H, c.G, c.N, c.L, true);
   Args a = make_args(c, pl);
-  place(a, c, layout_of(pl, c.B, c.H, c.G, c.N, c.L, true));
-  if (c.B > 0) {
-    const hipError_t e = pl.st == 4 ? backward<T, 4, 8, 1>(a, st) : backward<T, 8, 4, 2>(a, st);
-    if (e != hipSuccess) return e;
+  place(a, c, o);
+  float* carry = reinterpret_cast<float*>(static_cast<char*>(c.ws) + o.carry);
+  const long pairs = (long)c.B * c.G;
+  if (!launchable(pairs * pl.nrb * pl.nseg, 512)) return hipErrorInvalidConfiguration;
+  const int tile = kSeg * pl.st, ntile = (c.L + tile - 1) / tile;
+  for (long pair = 0; pair < pairs; pair += pl.npair) {
+    a.pair0 = (int)pair;
+    a.npair = (int)std::min<long>(pl.npair, pairs - pair);
+    for (int slab = pl.nslab - 1; slab >= 0; --slab) {
+      a.tile0 = slab * pl.slab_tiles;
+      a.tile1 = std::min(ntile, a.tile0 + pl.slab_tiles);
+      a.steps = pl.slab_tiles * kKeep;
+      a.part0 = slab * pl.nseg;
+      a.dx = slab == pl.nslab - 1 ? c.dx : carry;
+      a.dx0 = slab == 0 ? c.dx0 : carry;
+      const hipError_t e = pl.st == 4 ? backward<T, 4, 8, 1>(a, st) : backward<T, 8, 4, 2>(a, st);
+      if (e != hipSuccess) return e;
+    }
   }
   hipLaunchKernelGGL(selective_param_kernel, dim3(blocks_of((long)c.H * (c.N + 2) * 16)), dim3(256),
                      0, st, a);
@@ -1405,7 +1439,7 @@ hipError_t step(const Args& a, int lpr, hipStream_t st) {
 // launch's latency, 3.5 us, either way (replayed graphs, states warm).
 template <typename T>
 hipError_t run_step(const SelectiveCall& c, hipStream_t st) {
-  const Args a = make_args(c, Plan{8, 8, 1, 1, 1});
+  const Args a = make_args(c, Plan{});
   int lpr = 1;
   while (lpr * 4 < c.N) lpr *= 2;
   return (long)c.B * c.H * lpr >= (1L << 20) ? step<T, 2>(a, lpr, st) : step<T, 1>(a, lpr, st);

@@ -1,0 +1,73 @@
+"""The selective scan's backward pass where dB and dC of all steps at once would pass its
+workspace: slabs of time one after another, and launches that take a part of the batch."""
+import numpy as np
+import pytest
+
+import oracle
+from long_convolution_sequence_amd import binding as bd
+
+from selective_cases import c_selective_back
+from seq_cases import close, dtype_of, np64, say, torch_
+
+pytestmark = pytest.mark.gpu
+
+
+# 130 workgroups to a tile (whole rows), 64 (segments), 8400 (a part of the batch to a launch),
+# two groups; the gradient enters at a few rows' channels, so that the oracle needs no others
+@pytest.mark.parametrize("B,H,N,G,L,dtype,what", [
+    (2, 1040, 128, 1, 8325, "f32", "gsb"), (1, 1024, 128, 1, 17000, "bf16", "sbr"),
+    (2800, 48, 128, 1, 129, "bf16", "gsbr"), (2, 1050, 127, 2, 8400, "f16", "gr"),
+    (2700, 60, 127, 2, 40, "f32", "b")])
+def test_backward_in_parts(B, H, N, G, L, dtype, what):
+    torch = torch_()
+    say("case: B=%d H=%d N=%d G=%d L=%d %s %s" % (B, H, N, G, L, dtype, what))
+    dt = dtype_of(dtype)
+    gen = torch.Generator("cuda").manual_seed(B + L)
+    rnd = lambda *n: torch.randn(*n, device="cuda", generator=gen)
+    u, delta, Bm, Cm = (rnd(*n).to(dt) for n in ((B, H, L), (B, H, L), (B, G, N, L), (B, G, N, L)))
+    log_re = torch.rand(H, N, device="cuda", generator=gen) * 1.4 + 0.05
+    o = dict(z=rnd(B, H, L).to(dt) if "g" in what else None, D=rnd(H) if "s" in what else None,
+             dt_bias=rnd(H) - 2.0 if "b" in what else None, lens=None)
+    rows = sorted({0, B // 2, B - 1})
+    heads = [0, 17, H - 1] if G == 1 else [0, 17, H // G - 1, H // G, H - 2]
+    if "r" in what:
+        o["lens"] = torch.full((B,), L, dtype=torch.int32, device="cuda")
+        o["lens"][1::7] = 0
+        o["lens"][rows[-1]] = L * 3 // 5
+    dy, dx = torch.zeros(B, H, L, dtype=dt, device="cuda"), torch.zeros(B, H, N, device="cuda")
+    ix = np.ix_(rows, heads)
+    put = tuple(torch.from_numpy(a).cuda() for a in ix)
+    dy[put] = rnd(len(rows), len(heads), L).to(dt)
+    dx[put] = rnd(len(rows), len(heads), N)
+    five = [u, delta, Bm, Cm, log_re]
+    y, ckpt = bd.selective_forward_ckpt(*five, **o)
+    need = bd._selective_bytes(B, H, L, N, G, bd._dtype_code(u, "u"), 1)
+    # of exactly its size, between two guards
+    buf = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+    got = bd.selective_backward(dy, ckpt, *five, dx=dx, workspace=buf[256:256 + need], **o)
+    torch.cuda.synchronize()
+    assert (buf[:256] == 77).all() and (buf[256 + need:] == 77).all()
+    sub = lambda t: np64(t[put])
+    par = lambda t: None if t is None else np64(t)[heads]
+    each = [h * G // H for h in heads]
+    spread = lambda t: np64(t[rows])[:, each]  # a head's own B and C
+    kw = dict(D=par(o["D"]), dt_bias=par(o["dt_bias"]), z=None if o["z"] is None else sub(o["z"]),
+              dx=sub(dx), lens=None if o["lens"] is None else o["lens"][rows].cpu().numpy())
+    args = (sub(u), sub(delta), spread(Bm), spread(Cm), par(log_re), sub(dy))
+    ref, mag = oracle.selective_backward(*args, **kw), oracle.selective_backward(*args, magnitude=True, **kw)
+    c = c_selective_back(H, N, L)
+    for n in ("du", "ddelta", "dz", "dx0"):
+        if ref[n] is not None:
+            close(got[n][put], ref[n], mag[n], c, "f32" if n == "dx0" else dtype, n)
+    for n in ("dlog_re", "dD", "ddt_bias"):
+        if ref[n] is not None:
+            close(got[n][heads], ref[n], mag[n], c, "f32", n)
+            got[n][heads] = 0
+            assert not got[n].any(), n
+    for n in ("dB", "dC"):
+        for g in sorted(set(each)):
+            mine = [i for i, e in enumerate(each) if e == g]
+            close(got[n][rows][:, g], ref[n][:, mine].sum(1), mag[n][:, mine].sum(1), c, dtype, n)
+    got["du"][put] = 0
+    got["dx0"][put] = 0
+    assert not got["du"].any() and not got["dx0"].any()
