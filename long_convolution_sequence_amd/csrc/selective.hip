@@ -1237,6 +1237,7 @@ struct Plan {
   int nseg, seg_tiles;
 };
 constexpr long kPartFloats = 1L << 28;
+constexpr int kSplitSteps = 8;  // steps of a lane of rows that may be split: shorter are one tile
 
 Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
   Plan p{};
@@ -1255,7 +1256,7 @@ Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
     p.npair = (int)std::min(pairs, kPartFloats / least);
   }
   p.nslab = (ntile + p.slab_tiles - 1) / p.slab_tiles;
-  const bool split = have <= 128 && p.slab_tiles >= (backward ? 4 : 8);
+  const bool split = p.st == kSplitSteps && have <= 128 && p.slab_tiles >= (backward ? 4 : 8);
   const long want = split ? std::min<long>(p.slab_tiles, 512 / have) : 1;
   p.seg_tiles = (int)((p.slab_tiles + want - 1) / want);
   p.nseg = (p.slab_tiles + p.seg_tiles - 1) / p.seg_tiles;
@@ -1357,10 +1358,12 @@ hipError_t forward(const Args& a, hipStream_t st) {
   if (!launchable(blocks, 64 * RW * NW)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(64 * RW * NW);
   const size_t lds = (size_t)padded(a.N) * (2 * 4 * RW + 2) * sizeof(float);
-  if (a.nseg > 1) {
-    hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
-    hipLaunchKernelGGL((selective_join_kernel<false>), dim3(join_blocks(a)), dim3(256), 0, st, a.agg,
-                       a.aggS, a.log_re, a.x0, a.H, a.N, a.nseg);
+  if constexpr (ST == kSplitSteps) {
+    if (a.nseg > 1) {
+      hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
+      hipLaunchKernelGGL((selective_join_kernel<false>), dim3(join_blocks(a)), dim3(256), 0, st,
+                         a.agg, a.aggS, a.log_re, a.x0, a.H, a.N, a.nseg);
+    }
   }
   hipLaunchKernelGGL((selective_fwd_kernel<T, ST, RW, NW, false>), grid, block, lds, st, a);
   return hipGetLastError();
@@ -1379,11 +1382,13 @@ template <typename T, int ST, int RW, int NW>
 hipError_t backward(const Args& a, hipStream_t st) {
   const dim3 grid((unsigned)a.npair * a.nrb * a.nseg), block(64 * RW * NW);
   const size_t lds = (size_t)padded(a.N) * (3 * 4 * RW + 4) * sizeof(float);
-  if (a.nseg > 1) {
-    hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, dim3(64 * RW),
-                       2 * (size_t)a.N * (4 * RW + 1) * sizeof(float), st, a);
-    hipLaunchKernelGGL((selective_join_kernel<true>), dim3(join_blocks(a)), dim3(256), 0, st, a.agg,
-                       a.aggS, a.log_re, a.dx, a.H, a.N, a.nseg);
+  if constexpr (ST == kSplitSteps) {
+    if (a.nseg > 1) {
+      hipLaunchKernelGGL((selective_bwd_agg_kernel<T, ST, RW>), grid, dim3(64 * RW),
+                         2 * (size_t)a.N * (4 * RW + 1) * sizeof(float), st, a);
+      hipLaunchKernelGGL((selective_join_kernel<true>), dim3(join_blocks(a)), dim3(256), 0, st,
+                         a.agg, a.aggS, a.log_re, a.dx, a.H, a.N, a.nseg);
+    }
   }
   if (a.z)
     hipLaunchKernelGGL((selective_bwd_kernel<T, ST, RW, NW, true>), grid, block, lds, st, a);
