@@ -15,6 +15,7 @@
 // TB/s, 96 backward, 4.2).  A lane holds 8 consecutive steps and asks for the 8 before them
 // too, which its neighbour has just brought into the cache.
 #include <algorithm>
+#include <type_traits>
 
 #include "dssm_internal.h"
 #include "seq_common.h"
@@ -172,7 +173,7 @@ __device__ __forceinline__ float next_lane(float x) {
 // Rows of up to 512 steps belong to lpr <= 64 lanes; of longer ones a wave
 // walks tiles of 63 lanes, the last lane only forming the p that the 63rd
 // needs.  The sums over a row's (or segment's) steps stay with the lanes until
-// its end.
+// its end: a lane's 8 steps in float32, tiles and lanes in float64.
 template <typename T, int K, bool WHOLE>
 __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
   const int lane = threadIdx.x & 63;
@@ -192,10 +193,12 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
   const T* dy = static_cast<const T*>(p.dy) + (size_t)row * p.L;
   const size_t xs = (size_t)row * (K - 1);
   T* du = static_cast<T*>(p.du) + (size_t)(b * p.sdu) + (size_t)h * p.L;
-  float w[K], acc[K + 1];
+  float w[K];
+  typedef typename std::conditional<WHOLE, double, float>::type Sum;
+  Sum total[K + 1];
   const float bias = load_taps<K>(p, h, w);
 #pragma unroll
-  for (int k = 0; k <= K; ++k) acc[k] = 0.f;
+  for (int k = 0; k <= K; ++k) total[k] = 0;
   const int step = whole ? 63 * 8 : 0;
   const int lo = seg * p.seg_tiles, hi = min(p.ntile, lo + p.seg_tiles);
   for (int tile = lo; tile < hi; ++tile) {
@@ -252,12 +255,17 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
       }
       if (t < p.L) store_n<T, 8>(du + t, p.L - t, g);
       if (t < len) {
+        float acc[K + 1];
+#pragma unroll
+        for (int k = 0; k <= K; ++k) acc[k] = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
           for (int k = 0; k < K; ++k) acc[k] = fmaf(d[j], e[j + k], acc[k]);
           acc[K] += d[j];
         }
+#pragma unroll
+        for (int k = 0; k <= K; ++k) total[k] += acc[k];
       }
       if (K > 1 && t == 0 && p.dx0) {
 #pragma unroll
@@ -275,10 +283,10 @@ __global__ __launch_bounds__(256) void shortconv_bwd_kernel(Args p) {
   const int width = whole ? 64 : p.lpr;
   for (int o = 1; o < width; o <<= 1)
 #pragma unroll
-    for (int k = 0; k <= K; ++k) acc[k] += __shfl_xor(acc[k], o);
+    for (int k = 0; k <= K; ++k) total[k] += __shfl_xor(total[k], o);
   if (in && gl == 0) {
 #pragma unroll
-    for (int k = 0; k <= K; ++k) p.part[(size_t)rs * (K + 1) + k] = acc[k];
+    for (int k = 0; k <= K; ++k) p.part[(size_t)rs * (K + 1) + k] = (float)total[k];
   }
 }
 
