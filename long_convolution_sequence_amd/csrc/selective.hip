@@ -45,6 +45,7 @@ namespace {
 constexpr int kSeg = 16;  // lanes of a row
 constexpr int kKeep = 128; // steps between two kept states
 constexpr int kModes = 8; // modes whose B and C are in LDS at once
+constexpr int kSumTiles = 16;  // tiles whose sums for the parameters are one float32 part
 constexpr int kPair = 2;  // modes a wave walks side by side
 constexpr int kRowShl = 0x100, kRowRor = 0x120;
 
@@ -72,7 +73,8 @@ struct Args {
   float *dlog_re, *dD, *ddt_bias, *dx0;
   int npair, tile0, tile1;  // the launch's pairs; the slab's tiles
   int steps;              // of a row of part_bc
-  int nparts, part0;      // parts of a row in all; before this slab
+  // parts of a row's sums: in all, before this slab, of a segment
+  int nparts, part0, seg_parts;
   float* part_bc;         // [nrb][npair][2][N][steps]
   float* part_n;          // [rows][nparts][N]
   float* part_h;          // [rows][nparts][2]
@@ -859,7 +861,30 @@ void selective_bwd_kernel(Args p) {
     stage.fetch(Bm, Cm, p.N, p.L, 0, (t_live - 1) * TILE, len);
     fetch_starts(0, (t_live - 1) * TILE);
   }
+  // the parameters' sums over kSumTiles tiles leave, to be added up in float64; a row's
+  // own lanes: 16, or two rows of the vector unit's 16
   float sumD = 0.f, sumb = 0.f;
+  const auto leave_sums = [&](int which) {
+    sumD = row_total(sumD);
+    sumb = row_total(sumb);
+    if (Work::LPR == 32) {
+      sumD = rows_sum(sumD);
+      sumb = rows_sum(sumb);
+    }
+    const int to = p.part0 + at.seg * p.seg_parts + which;
+    if (live && w_.step == 0) {
+      float* put = p.part_h + ((row0 + w_.own) * p.nparts + to) * 2;
+      put[0] = sumD;
+      put[1] = sumb;
+    }
+    sumD = sumb = 0.f;
+    if (r < nrow)
+      for (int n = (lane & 15) * NW + nw; n < p.N; n += 16 * NW) {
+        p.part_n[((row0 + r) * p.nparts + to) * p.N + n] = dre.row(r)[n];
+        dre.row(r)[n] = 0.f;
+      }
+  };
+  for (int k = p.seg_parts - 1; t_lo + k * kSumTiles >= t_live && k >= 0; --k) leave_sums(k);
   for (int tile = t_live - 1; tile >= t_lo; --tile) {
     const int t0 = tile * TILE, nv = len - t0 - w_.step;
     const bool whole = t0 + TILE <= len;
@@ -1047,7 +1072,7 @@ void selective_bwd_kernel(Args p) {
         own[2][j] = y[j];
       }
     }
-    float o[3][4];
+    float o[3][4], tileD = 0.f, tileb = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float uj = uv.v[j], pre = dv.v[j] + bias, dtj = softplus(pre);
@@ -1059,11 +1084,11 @@ void selective_bwd_kernel(Args p) {
       }
       o[0][j] = fmaf(dtj, own[0][j], D * g);
       o[1][j] = fmaf(uj, own[0][j], -0.69314718056f * own[1][j]) * sigmoid_pair(pre, &rest);
-      if (j < nv && live) {
-        sumD = fmaf(g, uj, sumD);
-        sumb += o[1][j];
-      }
+      tileD = fmaf(g, j < nv ? uj : 0.f, tileD);
+      tileb += j < nv ? o[1][j] : 0.f;
     }
+    sumD += tileD;
+    sumb += tileb;
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < (Z ? 3 : 2); ++i)
@@ -1076,24 +1101,11 @@ void selective_bwd_kernel(Args p) {
       store_lane<T, 4>(ddelta + t0, mine, ns, whole, o[1]);
       if (Z) store_lane<T, 4>(dz + t0, mine, ns, whole, o[2]);
     }
+    if ((tile - t_lo) % kSumTiles == 0) leave_sums((tile - t_lo) / kSumTiles);
   }
-  // a row's own lanes: 16, or two rows of the vector unit's 16
-  sumD = row_total(sumD);
-  sumb = row_total(sumb);
-  if (Work::LPR == 32) {
-    sumD = rows_sum(sumD);
-    sumb = rows_sum(sumb);
-  }
-  if (live && w_.step == 0) {
-    float* put = p.part_h + ((row0 + w_.own) * p.nparts + p.part0 + at.seg) * 2;
-    put[0] = sumD;
-    put[1] = sumb;
-  }
-  if (r < nrow)
-    for (int n = (lane & 15) * NW + nw; n < p.N; n += 16 * NW) {
-      p.part_n[((row0 + r) * p.nparts + p.part0 + at.seg) * p.N + n] = dre.row(r)[n];
-      if (p.dx0 && at.seg == 0) p.dx0[(row0 + r) * p.N + n] = car.row(r)[n];
-    }
+  if (p.dx0 && at.seg == 0 && r < nrow)
+    for (int n = (lane & 15) * NW + nw; n < p.N; n += 16 * NW)
+      p.dx0[(row0 + r) * p.N + n] = car.row(r)[n];
 }
 
 // dB and dC of a slab: the row blocks' parts in order; 4 steps to a thread.
@@ -1237,7 +1249,7 @@ struct Plan {
   int rw;         // groups of four rows
   int nrb;        // row blocks of a group of channels
   int nslab, slab_tiles, npair;
-  int nseg, seg_tiles;
+  int nseg, seg_tiles, seg_parts;
 };
 constexpr long kPartFloats = 1L << 28;
 constexpr int kSplitSteps = 8;  // steps of a lane of rows that may be split: shorter are one tile
@@ -1263,6 +1275,7 @@ Plan plan_of(int B, int H, int G, int N, int L, bool backward) {
   const long want = split ? std::min<long>(p.slab_tiles, 512 / have) : 1;
   p.seg_tiles = (int)((p.slab_tiles + want - 1) / want);
   p.nseg = (p.slab_tiles + p.seg_tiles - 1) / p.seg_tiles;
+  p.seg_parts = (p.seg_tiles + kSumTiles - 1) / kSumTiles;
   return p;
 }
 
@@ -1296,7 +1309,8 @@ Args make_args(const SelectiveCall& c, const Plan& pl) {
   a.nrb = pl.nrb;
   a.nseg = pl.nseg;
   a.seg_tiles = pl.seg_tiles;
-  a.nparts = pl.nslab * pl.nseg;
+  a.nparts = pl.nslab * pl.nseg * pl.seg_parts;
+  a.seg_parts = pl.seg_parts;
   a.dy = c.dy;
   a.dx = c.dx;
   a.du = c.du;
@@ -1333,7 +1347,7 @@ Layout layout_of(const Plan& pl, int B, int H, int G, int N, int L, bool backwar
   o.agg = take(pl.nseg > 1 ? rows * pl.nseg * N : 0);
   o.aggS = take(pl.nseg > 1 ? rows * pl.nseg : 0);
   if (backward) {
-    const size_t parts = (size_t)pl.nslab * pl.nseg;
+    const size_t parts = (size_t)pl.nslab * pl.nseg * pl.seg_parts;
     o.carry = take(pl.nslab > 1 ? rows * N : 0);
     o.bc = take(L ? (size_t)pl.nrb * pl.npair * 2 * N * pl.slab_tiles * kKeep : 0);
     o.n = take(rows * parts * N);
@@ -1422,7 +1436,7 @@ hipError_t run_backward(const SelectiveCall& c, hipStream_t st) {
       a.tile0 = slab * pl.slab_tiles;
       a.tile1 = std::min(ntile, a.tile0 + pl.slab_tiles);
       a.steps = pl.slab_tiles * kKeep;
-      a.part0 = slab * pl.nseg;
+      a.part0 = slab * pl.nseg * pl.seg_parts;
       a.dx = slab == pl.nslab - 1 ? c.dx : carry;
       a.dx0 = slab == 0 ? c.dx0 : carry;
       const hipError_t e = pl.st == 4 ? backward<T, 4, 8, 1>(a, st) : backward<T, 8, 4, 2>(a, st);
