@@ -171,10 +171,11 @@ __device__ __forceinline__ float square_of(float log_re) {
   return s > 0x1p126f ? 0x1p126f : s;
 }
 
-// A sum of step sizes, finite unless NaN: resets (steps of 2^127, say) side by side pass
-// float32, and a mode with log_re 0 decays by no step however long.
+// A sum of step sizes, kept finite: resets (steps of 2^127, say) side by side pass
+// float32, and a mode with log_re 0 decays by no step however long.  One instruction,
+// which takes NaN for 0: the decays of the steps themselves carry it.
 __device__ __forceinline__ float finite_sum(float s) {
-  return s > 0x1.fffffep127f ? 0x1.fffffep127f : s;
+  return __builtin_amdgcn_fmed3f(s, 0.f, 0x1.fffffep127f);
 }
 
 // What stands for log_re^2 in the modes and rows that only fill a workgroup: their
