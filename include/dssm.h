@@ -671,9 +671,9 @@ typedef struct {
 } dssm_selective_grads;
 
 /* Bytes of workspace of dssm_selective_forward or (backward != 0)
- * dssm_selective_backward (host only): forward at most a checkpoint's size twice,
- * backward at most 1 GiB (parts of dB and dC, in float32) and six times a checkpoint's.
- * Requires H <= 65535, B H <= 2^24, L <=
+ * dssm_selective_backward (host only): forward at most twice a checkpoint's, backward
+ * at most 2 GiB (parts of dB and dC in float32, B G ceil(H / (16 G)) 2 N L of them where
+ * that is less) and six times a checkpoint's.  Requires H <= 65535, B H <= 2^24, L <=
  * 2^24, B H L <= 2^40, B H N ceil(L / 128) <= 2^36, B G N ceil(L / 1024) <= 2^29;
  * the calls over sequences B G ceil(H / (16 G)) < 2^23 (16 channels of a group, or one,
  * to 512 lanes; 32 where L <= 64). */

@@ -1252,7 +1252,7 @@ struct Plan {
   int nslab, slab_tiles, npair;
   int nseg, seg_tiles, seg_parts;
 };
-constexpr long kPartFloats = 1L << 28;
+constexpr long kPartFloats = 1L << 29;
 constexpr int kSplitSteps = 8;  // steps of a lane of rows that may be split: shorter are one tile
 
 Plan plan_of(int B, int H, int G, int N, int L, bool backward) {

@@ -12,12 +12,12 @@ from seq_cases import close, dtype_of, np64, say, torch_
 pytestmark = pytest.mark.gpu
 
 
-# 130 workgroups to a tile (whole rows), 64 (segments), 8400 (a part of the batch to a launch),
+# 130 workgroups to a tile (whole rows), 64 (segments), 16800 (a part of the batch to a launch),
 # two groups; the gradient enters at a few rows' channels, so that the oracle needs no others
 @pytest.mark.parametrize("B,H,N,G,L,dtype,what", [
-    (2, 1040, 128, 1, 8325, "f32", "gsb"), (1, 1024, 128, 1, 17000, "bf16", "sbr"),
-    (2800, 48, 128, 1, 129, "bf16", "gsbr"), (2, 1050, 127, 2, 8400, "f16", "gr"),
-    (2700, 60, 127, 2, 40, "f32", "b")])
+    (2, 1040, 128, 1, 16513, "f32", "gsb"), (1, 1024, 128, 1, 33000, "bf16", "sbr"),
+    (5600, 48, 128, 1, 129, "bf16", "gsbr"), (2, 1050, 127, 2, 16400, "f16", "gr"),
+    (8400, 40, 127, 2, 40, "f32", "b")])
 def test_backward_in_parts(B, H, N, G, L, dtype, what):
     torch = torch_()
     say("case: B=%d H=%d N=%d G=%d L=%d %s %s" % (B, H, N, G, L, dtype, what))
@@ -42,6 +42,8 @@ def test_backward_in_parts(B, H, N, G, L, dtype, what):
     five = [u, delta, Bm, Cm, log_re]
     y, ckpt = bd.selective_forward_ckpt(*five, **o)
     need = bd._selective_bytes(B, H, L, N, G, bd._dtype_code(u, "u"), 1)
+    rows_of = 32 if L <= 64 else 16
+    assert B * G * -(-H // G // rows_of) * 2 * N * -(-L // 128) * 128 > 1 << 29  # parts in all
     # of exactly its size, between two guards
     buf = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
     got = bd.selective_backward(dy, ckpt, *five, dx=dx, workspace=buf[256:256 + need], **o)
