@@ -688,7 +688,8 @@ int dssm_selective_ckpt_size(const dssm_selective_shape* s, size_t* bytes);
  *   x_t = exp(-log_re[h]^2 dt_t) x_{t-1} + dt_t B_t u_t         (N values each),
  *   y_t = (sum_n C_t x_t + D[h] u_t) silu(z_t)
  * (a step of length 1 decays as the mode exp(-log_re^2) of the layer above;
- * delta = -infinity is a step that changes nothing).
+ * delta = -infinity, with finite u_t and B_t, is a step that changes nothing; a step of
+ * 2^127 without a drive is one that forgets all).
  *   x0 [B, H, N] float32 (may be NULL: zero): the state before step 0;
  *   x_end [B, H, N] float32 (may be NULL): receives the state after the last
  *   live step; it may be x0.

@@ -10,8 +10,9 @@
 // the scale.
 //
 // Memory bounds it: o's inputs read once, o written, a byte a channel written (2^25
-// bf16 elements in rows of 64 to 1024 channels: x + y 45 us, 5.2 TB/s; with the norm
-// and gate of y 74 to 80, its vector work only partly behind the loads: 4 TB/s).
+// bf16 elements in rows of 64 to 1024 channels, inputs from memory: x + y 62 to 68 us,
+// 3.8 TB/s; with the norm and gate of y 74 to 83, 4 TB/s; inputs that a cache still
+// holds, x + y 45).
 // A workgroup takes a strip of LT VE steps with all its channels, o held in
 // registers as stored; four neighbouring channels to a lane, so that their bytes
 // of a step make one word, turned to rows of channels through LDS.
@@ -465,6 +466,8 @@ void token(const Args& a, hipStream_t st) {
 // channels in 64 threads and in 256: 74 us and 181 (2^25 bf16 elements, gate and norm
 // of y); 1024 in 512 threads of 8 channels and in 1024 of 4: 84 and 98.  2048 channels
 // of 16 bits in 512 threads of 16 and in 1024 of 8: 92 and 97; of 32 bits, 171 and 165.
+// (The same inputs every pass, of either side.)  Layer norms of 2049 to 4096 channels of
+// 16 bits keep 4 to 26 registers in scratch, beyond that 1 or 2.
 template <typename T, bool LAYER, int FORM>
 hipError_t run(const Args& a, hipStream_t st) {
   constexpr int kWide = sizeof(T) == 2 ? 512 : 1024;

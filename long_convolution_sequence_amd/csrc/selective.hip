@@ -18,20 +18,27 @@
 // are walked two at a time, a lane's decays and drives of them in registers, and
 // two waves share the modes of a row.  With 16 steps to a lane and one wave the
 // joins cost half, but the registers leave two waves per SIMD instead of four, and
-// instructions issue slower for it: forward the same (0.20 ms of 4 x 4096 rows of
-// 2048 steps and 16 modes), backward 643 us against 595.  B and C are the same for
+// instructions issue slower for it: forward the same (0.20 ms of 4 x 2048 rows of
+// 4096 steps and 16 modes), backward 643 us against 595.  B and C are the same for
 // all rows of a group: the workgroup's tile of them lies in LDS as float32.
 //
-// What bounds it is the vector unit (its instructions issue in 84 to 96% of the
-// cycles): a product for the exponent, the exponential (its own rate a quarter),
+// What bounds it is the vector unit (busy in 76% of the cycles, either direction): a product for the exponent, the exponential (its own rate a quarter),
 // the drive, two passes of the recurrence (one to join the lanes, one from the
 // joined state), the join and the read-out, about 7 operations and an exponential
 // per mode and step; the backward pass forms the states again, walks their
 // gradients the other way and sums two products over rows, about 19 and an
 // exponential; and what is done once a step (inputs, gates, turns through LDS) takes
-// a third of the time at 16 modes.  Those 4 x 4096 rows in bf16 with a gate: forward
-// 0.21 ms (0.27 GB of tensors take 0.05), backward 0.60 + 0.07 ms to add the row
-// blocks' dB and dC.
+// a third of the time at 16 modes.  4 x 2048 rows of 4096 steps and 16 modes in bf16
+// with a gate: forward 0.21 ms (0.27 GB of tensors take 0.05), backward 0.61 + 0.07 ms
+// to add the row blocks' dB and dC.  At the 128 registers that four waves per SIMD
+// leave, the output kernel keeps 10 to 17 in scratch and the backward kernel 17 to 28.
+// The backward pass's LDS, 64 KB and 208 bytes a mode, holds two workgroups to a
+// compute unit up to 72 modes and one beyond (B=4 H=2048 L=2048 bf16, a training step's
+// us per mode: 64 modes 20.7, 72 20.4, 80 24.0, 128 22.9).
+//
+// Decays are float32, also those next to 1, and a lane multiplies its 8; from lane to
+// lane and tile to tile a state decays by one exponential of the summed step sizes, so
+// that a long memory does not pile up a rounding per step.
 #include <algorithm>
 #include <type_traits>
 
@@ -1244,7 +1251,9 @@ __global__ __launch_bounds__(256) void selective_step_kernel(Args p, int lpr) {
 // 2 N L values: at 128 modes 32 times a tensor of 16 bits, were they all held at once.
 // A slab of tiles of all rows holds at most kPartFloats of them (one tile's of
 // some pairs of batch row and group, where all pairs' are more); the slabs go from the
-// last to the first, each from the state gradient that the one behind it leaves.
+// last to the first, each from the state gradient that the one behind it leaves (8 x 4096
+// rows of 8192 steps and 128 modes: all at once 16 GiB and 37.2 ms, in slabs of 1 GiB
+// 38.6, of 2 GiB 37.5).
 struct Plan {
   int st;         // steps of a lane
   int rw;         // groups of four rows
