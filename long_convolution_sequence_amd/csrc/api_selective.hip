@@ -95,7 +95,7 @@ int check_selective(const dssm_selective_shape* s, bool* empty) {
     return fail(DSSM_ERR_UNSUPPORTED, "selective: B*H=%ld exceeds 2^24", (long)s->B * s->H);
   if ((__int128)s->B * s->H * s->N * ((s->L + 127) / 128) > ((__int128)1 << 36))
     return fail(DSSM_ERR_UNSUPPORTED, "selective: B*H*N*ceil(L/128) exceeds 2^36");
-  // a workgroup to 1024 steps of a mode's B and C gradients
+  // parts of 1024 steps of the modes' B and C gradients, numbered in 32 bits
   if ((__int128)s->B * s->G * s->N * ((s->L + 1023) / 1024) > ((__int128)1 << 29))
     return fail(DSSM_ERR_UNSUPPORTED, "selective: B*G*N*ceil(L/1024) exceeds 2^29");
   return DSSM_OK;

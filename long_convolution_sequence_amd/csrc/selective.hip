@@ -22,11 +22,12 @@
 // 4096 steps and 16 modes), backward 643 us against 595.  B and C are the same for
 // all rows of a group: the workgroup's tile of them lies in LDS as float32.
 //
-// What bounds it is the vector unit (busy in 76% of the cycles, either direction): a product for the exponent, the exponential (its own rate a quarter),
-// the drive, two passes of the recurrence (one to join the lanes, one from the
-// joined state), the join and the read-out, about 7 operations and an exponential
-// per mode and step; the backward pass forms the states again, walks their
-// gradients the other way and sums two products over rows, about 19 and an
+// What bounds it is the vector unit (busy in 76% of the cycles, either direction): a
+// product for the exponent, the exponential (its own rate a quarter), the drive, two
+// passes of the recurrence (one to join the lanes, one from the joined state), the
+// join and the read-out, about 7 operations and an exponential per mode and step; the
+// backward pass forms the states again, walks their gradients the other way and sums
+// two products over rows, about 19 and an
 // exponential; and what is done once a step (inputs, gates, turns through LDS) takes
 // a third of the time at 16 modes.  4 x 2048 rows of 4096 steps and 16 modes in bf16
 // with a gate: forward 0.21 ms (0.27 GB of tensors take 0.05), backward 0.61 + 0.07 ms
